@@ -406,6 +406,110 @@ int sfx_build_suffix_array(const int32_t* text, int64_t n, int32_t* sa, void* wo
  * different streams, or from several threads) race: order them, for example on one stream. */
 int sfx_build_suffix_array_noalloc(const int32_t* text, int64_t n, int32_t* sa, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The verification step around the drafter.  sfx_propose drafts up to k tokens; the target model
+ * then runs on the last sampled token and the draft, k + 1 rows a request: their keys and values
+ * go into the cache (sfx_kv_write), every layer attends over it (sfx_kv_attention), and the
+ * logits decide which drafted tokens stay (sfx_verify).  sfx_verify's `sampled` and
+ * `num_accepted` are the next inputs of sfx_propose / sfx_update_state and of
+ * sfx_accept_feedback.  These calls need no context; they neither allocate nor synchronise, use
+ * no memory clears, and can be captured in a HIP graph.  Workspaces are the caller's; calls that
+ * may overlap need one each. */
+
+/* Element types of the arrays marked `type`. */
+enum { SFX_TYPE_BF16 = 0, SFX_TYPE_FP16 = 1, SFX_TYPE_FP32 = 2 };
+
+/* A paged 8-bit KV cache.  A request's token at position p lies in page
+ * page_table[b, p / page_size] (an id outside [0, num_pages) is an unmapped page), which holds
+ * page_size tokens of every head.  Values are e4m3 codes (OCP, no infinity) times one
+ * power-of-two scale per block of 32 tokens, head and tensor: the least 2^e with
+ * max|x| <= 448 * 2^e over the block's finite values, e within [-32, 31] (so magnitudes from
+ * 2^-41 to 448 * 2^31 are held; larger ones, infinities among them, saturate; NaN stays NaN).
+ * Buffers, in the order in which the attention reads them:
+ *   k       [num_pages, kv_heads, head_dim / 64, page_size, 64]
+ *   v       [num_pages, kv_heads, page_size / 32, head_dim / 32, 16, 4, 2, 2, 4], whose last five
+ *           indices r, g, f, j, i hold token 16 j + 4 g + i of the 32-token block and dim
+ *           32 * slab + 2 r + f
+ *   k_scale, v_scale  [num_pages, kv_heads, page_size / 32] float
+ * k and v are aligned to 16 bytes.  page_size: a multiple of 32 up to 2048; head_dim: 64, 128 or
+ * 256; max_pages * page_size at most 2^31 - 256.  Contents need no initialisation. */
+typedef struct sfx_kv_cache {
+  int32_t num_pages, page_size, kv_heads, head_dim;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} sfx_kv_cache;
+
+/* Quantise new tokens into the cache as they are written.
+ *   page_table [B, max_pages]; start [B]: position of the first new token; count [B]: how many,
+ *   clamped to [0, T] (NULL: T); a negative start writes nothing, and so do tokens of unmapped
+ *   pages or past max_pages.
+ *   k, v [B, T, kv_heads, head_dim] of `type`; k_strides, v_strides: element strides of
+ *   {batch, token, head} (host arrays; NULL: dense), the dims of a head contiguous.
+ * A block that starts before `start` keeps its earlier tokens: its exponent becomes the larger of
+ * its own and the one the new tokens need, and when it grows the earlier codes are rounded to
+ * the new scale (exact unless they become subnormal).  A block that starts at or after `start`
+ * takes its scale from the new tokens alone, so positions can be written again after drafted
+ * tokens were rejected.  Requests must not write the same page in one call. */
+int sfx_kv_write(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t max_pages,
+                 const int32_t* page_table, const int32_t* start, const int32_t* count,
+                 const void* k, const int64_t* k_strides, const void* v,
+                 const int64_t* v_strides, int32_t type, void* stream);
+
+/* Read tokens back: k, v [B, T, kv_heads, head_dim] receive positions start[b] + 0 .. T-1,
+ * rounded once to `type`; zero for rows at or past count[b] (NULL: T), on unmapped pages or of a
+ * negative start.  Strides as for sfx_kv_write; k and v must not overlap themselves. */
+int sfx_kv_read(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t max_pages,
+                const int32_t* page_table, const int32_t* start, const int32_t* count, void* k,
+                const int64_t* k_strides, void* v, const int64_t* v_strides, int32_t type,
+                void* stream);
+
+/* Attention of each request's newest tokens over its cached ones (their own included).
+ *   q [B, T, q_heads, head_dim] of `type` (bf16 or fp16), strides as above; query heads
+ *   h * q_heads / kv_heads + 0, 1, ... read cached head h.  out: the same shape, dense, aligned
+ *   to 16 bytes.
+ *   seq_lens [B]: tokens in the cache, clamped to [0, max_pages * page_size]; q_lens [B]: how
+ *   many of the T rows are real, clamped to [0, T] (NULL: T).  Row t < q_len stands at position
+ *   p = seq_len - q_len + t and sees the cached tokens j <= p; with window > 0 those with
+ *   j > p - window or j < sinks.  Tokens of unmapped pages are not seen.
+ *   out = softmax(scale * q k) v in fp32 sums; zero for rows that see nothing or t >= q_len.
+ * T = 1 is plain decoding, T = k + 1 the verification of a draft, larger T a prompt.
+ * workspace: sfx_kv_attention_workspace_bytes (may be 0), aligned to 16 bytes; its contents
+ * mean nothing before or after.  scale: positive and finite. */
+int sfx_kv_attention_workspace_bytes(const sfx_kv_cache* cache, int32_t B, int32_t T,
+                                     int32_t q_heads, int32_t max_pages, int32_t window,
+                                     int32_t sinks, size_t* bytes);
+int sfx_kv_attention(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t q_heads,
+                     int32_t max_pages, const int32_t* page_table, const int32_t* seq_lens,
+                     const int32_t* q_lens, const void* q, const int64_t* q_strides, void* out,
+                     int32_t type, float scale, int32_t window, int32_t sinks, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Verify drafts against the target's logits with given random numbers.  The drafts of this
+ * library carry no probabilities (each is certain to its drafter), so the rule that leaves the
+ * target's distribution unchanged is, with p = softmax(logits / temperature) in each row:
+ *   slot i's draft d is accepted when u_accept[b, i] < p_i(d); at the first rejection a token is
+ *   drawn from p_i without d, renormalised; if all are accepted, one from row num_valid[b].
+ *   The draw is the least token whose running sum of p passes u_sample[b] times the total.
+ *   logits [B, k + 1, V] of `type`, element strides batch_stride and slot_stride, V contiguous;
+ *   only rows 0 .. num_valid[b] are read.  -inf masks a token; NaN counts as -inf; +inf entries
+ *   share the row evenly.
+ *   temperature [B] (NULL: 1); a value not above 0 is greedy: accepted while the draft is the
+ *   row's largest logit (lowest index of equals), and that token is what is drawn.
+ *   draft [B, k]; an id outside [0, V) is never accepted.  num_valid [B], clamped to [0, k]
+ *   (NULL: k).  u_accept [B, k], u_sample [B]: uniform in [0, 1).
+ *   sampled [B, k + 1] receives the accepted tokens, then the drawn one, then -1;
+ *   num_accepted [B] the number accepted.  A row with no token above -inf draws -1.
+ * Comparisons are decided as in exact arithmetic up to fp64 rounding.  k within [0, 32].
+ * workspace: sfx_verify_workspace_bytes, aligned to 16 bytes. */
+int sfx_verify_workspace_bytes(int32_t B, int32_t k, int32_t V, size_t* bytes);
+int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batch_stride,
+               int64_t slot_stride, int32_t type, const float* temperature, const int32_t* draft,
+               const int32_t* num_valid, const float* u_accept, const float* u_sample,
+               int32_t* sampled, int32_t* num_accepted, void* workspace, size_t workspace_bytes,
+               void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,7 +33,9 @@ EXPORTS = ("sfx_create", "sfx_destroy", "sfx_last_error", "sfx_propose", "sfx_pr
            "sfx_debug_fail_next_rebuild", "sfx_debug_index", "sfx_rebuild_stats",
            "sfx_suffix_array_workspace_bytes", "sfx_build_suffix_array",
            "sfx_build_suffix_array_noalloc", "sfx_graphs_create", "sfx_graphs_propose",
-           "sfx_graphs_stats", "sfx_graphs_destroy")
+           "sfx_graphs_stats", "sfx_graphs_destroy", "sfx_kv_write", "sfx_kv_read",
+           "sfx_kv_attention_workspace_bytes", "sfx_kv_attention",
+           "sfx_verify_workspace_bytes", "sfx_verify")
 
 
 FLAG_STREAM_CONTEXT = 1  # read contexts from device memory instead of staging them in LDS
@@ -49,6 +51,9 @@ GRAPHS_DEBUG_BREAK_ODD = 8   # test hook: captures of odd-indexed buckets fail
 # bits of the sticky error word (include/sfx.h)
 ERR_LENGTH, ERR_NEGATIVE_TOKEN, ERR_SAMPLED_AFTER_PAD, ERR_ROW_INDEX = 1, 2, 4, 8
 ERR_SYNC_TIMEOUT = 16    # a propose workgroup's bounded internal wait ran out
+
+# element types of the verification step's arrays (include/sfx.h)
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class SfxError(RuntimeError):
@@ -78,6 +83,19 @@ class _Config(ctypes.Structure):
     ]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
 @dataclasses.dataclass
 class Config:
     k: int
@@ -104,6 +122,7 @@ class Config:
 _V = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_SIZE_P = ctypes.POINTER(ctypes.c_size_t)
 _lib = None
 
 
@@ -154,6 +173,18 @@ def load(path: str = LIB_PATH):
                                             ctypes.POINTER(ctypes.c_uint64),
                                             ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
         "sfx_graphs_destroy": (None, [_V]),
+        "sfx_kv_write": (ctypes.c_int, [_V, _I32, _I32, _I32, _V, _V, _V, _V, _V, _V, _V, _I32,
+                                        _V]),
+        "sfx_kv_read": (ctypes.c_int, [_V, _I32, _I32, _I32, _V, _V, _V, _V, _V, _V, _V, _I32,
+                                       _V]),
+        "sfx_kv_attention_workspace_bytes": (ctypes.c_int, [_V, _I32, _I32, _I32, _I32, _I32,
+                                                            _I32, _SIZE_P]),
+        "sfx_kv_attention": (ctypes.c_int, [_V, _I32, _I32, _I32, _I32, _V, _V, _V, _V, _V, _V,
+                                            _I32, ctypes.c_float, _I32, _I32, _V,
+                                            ctypes.c_size_t, _V]),
+        "sfx_verify_workspace_bytes": (ctypes.c_int, [_I32, _I32, _I32, _SIZE_P]),
+        "sfx_verify": (ctypes.c_int, [_I32, _I32, _I32, _V, _I64, _I64, _I32, _V, _V, _V, _V,
+                                      _V, _V, _V, _V, ctypes.c_size_t, _V]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -487,3 +518,220 @@ def build_suffix_array(text: torch.Tensor, stream=None) -> torch.Tensor:
     ws = torch.empty(wsb, dtype=torch.uint8, device=t.device)
     _check(L.sfx_build_suffix_array(_ptr(t), n, _ptr(sa), _ptr(ws), wsb, _stream(stream)))
     return sa
+
+
+# ------------------------------------------------------------------ the verification step
+def _on(device):
+    """The kernels run on the current device: the tensors have to be there."""
+    if device.type != "cuda":
+        raise TypeError("tensors must be on a CUDA/HIP device")
+    cur = torch.cuda.current_device()
+    if device.index is not None and device.index != cur:
+        raise ValueError(f"tensors are on {device}, the current device is {cur}")
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to `stream` (the current one if None), so that its memory is
+    not handed to other work while a kernel there still uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(
+            stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _vec(t, name, n, dtype, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D tensor of {n} entries")
+    return t
+
+
+def _heads(t, name, heads, dim, device=None):
+    """A [B, T, heads, dim] tensor of any batch, token and head strides."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES or not t.is_cuda or \
+            (device is not None and t.device != device):
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 CUDA/HIP tensor" +
+                        (f" on {device}" if device is not None else ""))
+    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != dim:
+        raise ValueError(f"{name} must be [B, T, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t
+
+
+def _strides(t):
+    if t.is_contiguous():
+        return None
+    return (_I64 * 3)(t.stride(0), t.stride(1), t.stride(2))
+
+
+class KVCache:
+    """A paged 8-bit KV cache: e4m3 codes with a power-of-two scale for each block of 32 tokens
+    and head, in the layout that the attention reads (sfx_kv_cache in include/sfx.h).
+
+    The buffers are allocated here, or given as ``buffers = (k, v, k_scale, v_scale)``: uint8 (or
+    float8_e4m3fn) codes and float32 scales of the shapes of :meth:`shapes`.  Page tables, starts
+    and lengths are int32 tensors in device memory; which pages a request owns is the caller's
+    business."""
+
+    def __init__(self, num_pages, page_size, kv_heads, head_dim, device="cuda", buffers=None):
+        if head_dim not in (64, 128, 256):
+            raise ValueError("head_dim must be 64, 128 or 256")
+        if page_size % 32 or not 32 <= page_size <= 2048:
+            raise ValueError("page_size must be a multiple of 32 in [32, 2048]")
+        if num_pages < 0 or kv_heads < 1:
+            raise ValueError("num_pages must not be negative, kv_heads at least 1")
+        codes = self.shapes(num_pages, page_size, kv_heads, head_dim)
+        if buffers is None:
+            dev = torch.device(device)
+            self.k, self.v = (torch.zeros(s, dtype=torch.uint8, device=dev) for s in codes[:2])
+            self.k_scale, self.v_scale = (torch.zeros(s, dtype=torch.float32, device=dev)
+                                          for s in codes[2:])
+        else:
+            for t, s, name in zip(buffers, codes, ("k", "v", "k_scale", "v_scale")):
+                kinds = (torch.float32,) if name.endswith("scale") else \
+                    (torch.uint8, torch.float8_e4m3fn)
+                if t.dtype not in kinds or not t.is_cuda or t.device != buffers[0].device:
+                    raise TypeError(f"{name} must be a {kinds[0]} CUDA/HIP tensor")
+                if t.shape != s or not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous of shape {tuple(s)}")
+            self.k, self.v, self.k_scale, self.v_scale = buffers
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
+        self.device = self.k.device
+        self._c = _KvCache(self.num_pages, self.page_size, self.kv_heads, self.head_dim,
+                           self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                           self.v_scale.data_ptr())
+        self._p = ctypes.byref(self._c)
+
+    @staticmethod
+    def shapes(num_pages, page_size, kv_heads, head_dim):
+        """Shapes of k, v, k_scale and v_scale."""
+        s = torch.Size((num_pages, kv_heads, page_size // 32))
+        return (torch.Size((num_pages, kv_heads, head_dim // 64, page_size, 64)),
+                torch.Size((num_pages, kv_heads, page_size // 32, head_dim // 32, 16, 4, 2, 2,
+                            4)), s, s)
+
+    def _table(self, page_table, B):
+        t = _i32(page_table, "page_table", 2)
+        if t.shape[0] != B or t.device != self.device:
+            raise ValueError(f"page_table must be [{B}, pages] on {self.device}")
+        return t
+
+    def write(self, k, v, page_table, start, count=None, stream=None):
+        """sfx_kv_write: quantise k, v [B, T, kv_heads, head_dim] into positions start[b] .."""
+        _on(self.device)
+        k = _heads(k, "k", self.kv_heads, self.head_dim, self.device)
+        v = _heads(v, "v", self.kv_heads, self.head_dim, self.device)
+        if v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v differ in shape or type")
+        B, T = k.shape[:2]
+        tab = self._table(page_table, B)
+        st = _vec(start, "start", B, torch.int32, self.device)
+        ct = None if count is None else _vec(count, "count", B, torch.int32, self.device)
+        _check(load().sfx_kv_write(self._p, B, T, tab.shape[1], _ptr(tab), _ptr(st), _ptr(ct),
+                                   _ptr(k), _strides(k), _ptr(v), _strides(v),
+                                   _TYPES[k.dtype], _stream(stream)))
+
+    def read(self, page_table, start, count, T, dtype=torch.bfloat16, k=None, v=None,
+             stream=None):
+        """sfx_kv_read: positions start[b] .. start[b] + T - 1 as k, v [B, T, kv_heads,
+        head_dim]; zero past count[b]."""
+        _on(self.device)
+        if dtype not in _TYPES:
+            raise TypeError("dtype must be bfloat16, float16 or float32")
+        B = page_table.shape[0]
+        tab = self._table(page_table, B)
+        st = _vec(start, "start", B, torch.int32, self.device)
+        ct = None if count is None else _vec(count, "count", B, torch.int32, self.device)
+        shape = (B, int(T), self.kv_heads, self.head_dim)
+        if k is None:
+            k = _empty(shape, dtype, self.device, stream)
+        if v is None:
+            v = _empty(shape, dtype, self.device, stream)
+        k = _heads(k, "k", self.kv_heads, self.head_dim, self.device)
+        v = _heads(v, "v", self.kv_heads, self.head_dim, self.device)
+        if k.shape != shape or v.shape != shape or k.dtype != dtype or v.dtype != dtype:
+            raise ValueError(f"k and v must be {shape} of {dtype}")
+        _check(load().sfx_kv_read(self._p, B, int(T), tab.shape[1], _ptr(tab), _ptr(st),
+                                  _ptr(ct), _ptr(k), _strides(k), _ptr(v), _strides(v),
+                                  _TYPES[dtype], _stream(stream)))
+        return k, v
+
+    def attend(self, q, page_table, seq_lens, q_lens=None, scale=None, window=0, sinks=0,
+               out=None, stream=None):
+        """sfx_kv_attention: rows t < q_lens[b] of q [B, T, heads, head_dim] (bf16 or fp16), the
+        newest tokens of seq_lens[b] cached ones, attend causally over the cache; window and
+        sinks restrict what they see (0: everything).  scale defaults to head_dim ** -0.5."""
+        _on(self.device)
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("q must be [B, T, heads, head_dim]")
+        B, T, H = q.shape[:3]
+        q = _heads(q, "q", H, self.head_dim, self.device)
+        if q.dtype == torch.float32:
+            raise TypeError("q must be bfloat16 or float16")
+        tab = self._table(page_table, B)
+        sl = _vec(seq_lens, "seq_lens", B, torch.int32, self.device)
+        ql = None if q_lens is None else _vec(q_lens, "q_lens", B, torch.int32, self.device)
+        if out is None:
+            out = _empty((B, T, H, self.head_dim), q.dtype, self.device, stream)
+        elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or \
+                not out.is_contiguous():
+            raise ValueError("out must be contiguous and like q")
+        L, n = load(), ctypes.c_size_t(0)
+        mp = tab.shape[1]
+        window, sinks = int(window), int(sinks)
+        _check(L.sfx_kv_attention_workspace_bytes(self._p, B, T, H, mp, window, sinks,
+                                                  ctypes.byref(n)))
+        ws = _empty((n.value,), torch.uint8, self.device, stream) if n.value else None
+        _check(L.sfx_kv_attention(self._p, B, T, H, mp, _ptr(tab), _ptr(sl), _ptr(ql), _ptr(q),
+                                  _strides(q), _ptr(out), _TYPES[q.dtype],
+                                  self.head_dim ** -0.5 if scale is None else float(scale),
+                                  window, sinks, _ptr(ws), n.value, _stream(stream)))
+        return out
+
+
+def verify(logits, draft, num_valid, u_accept, u_sample, temperature=None, sampled=None,
+           num_accepted=None, stream=None):
+    """sfx_verify: accept or reject drafts [B, k] against the target's logits [B, k + 1, V] with
+    the given uniform numbers u_accept [B, k] and u_sample [B].  Returns sampled [B, k + 1]
+    (accepted tokens, one drawn token, then -1) and num_accepted [B]: the next inputs of
+    propose / update_state and accept_feedback."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _TYPES or not logits.is_cuda:
+        raise TypeError("logits must be a bfloat16, float16 or float32 CUDA/HIP tensor")
+    if logits.dim() != 3 or logits.shape[1] < 1 or (logits.shape[2] > 1 and
+                                                    logits.stride(2) != 1):
+        raise ValueError("logits must be [B, k + 1, V] with V contiguous")
+    dev = logits.device
+    _on(dev)
+    B, k1, V = logits.shape
+    dr = _i32(draft, "draft", 2)
+    if dr.shape != (B, k1 - 1) or dr.device != dev:
+        raise ValueError(f"draft must be [{B}, {k1 - 1}] on {dev}")
+    nv = None if num_valid is None else _vec(num_valid, "num_valid", B, torch.int32, dev)
+    if not isinstance(u_accept, torch.Tensor) or u_accept.dtype != torch.float32 or \
+            u_accept.device != dev:
+        raise TypeError(f"u_accept must be a float32 tensor on {dev}")
+    if u_accept.shape != dr.shape or not u_accept.is_contiguous():
+        raise ValueError(f"u_accept must be a contiguous [{B}, {k1 - 1}] tensor")
+    us = _vec(u_sample, "u_sample", B, torch.float32, dev)
+    tp = None if temperature is None else _vec(temperature, "temperature", B, torch.float32, dev)
+    if sampled is None:
+        sampled = _empty((B, k1), torch.int32, dev, stream)
+    if num_accepted is None:
+        num_accepted = _empty((B,), torch.int32, dev, stream)
+    if _i32(sampled, "sampled", 2).shape != (B, k1) or sampled.device != dev:
+        raise ValueError(f"sampled must be [{B}, {k1}] on {dev}")
+    _vec(num_accepted, "num_accepted", B, torch.int32, dev)
+    L, n = load(), ctypes.c_size_t(0)
+    _check(L.sfx_verify_workspace_bytes(B, k1 - 1, V, ctypes.byref(n)))
+    ws = _empty((n.value,), torch.uint8, dev, stream) if n.value else None
+    _check(L.sfx_verify(B, k1 - 1, V, _ptr(logits), logits.stride(0), logits.stride(1),
+                        _TYPES[logits.dtype], _ptr(tp), _ptr(dr), _ptr(nv), _ptr(u_accept),
+                        _ptr(us), _ptr(sampled), _ptr(num_accepted), _ptr(ws), n.value,
+                        _stream(stream)))
+    return sampled, num_accepted

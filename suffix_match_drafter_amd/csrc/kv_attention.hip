@@ -1,0 +1,613 @@
+// kv_attention.hip -- attention of a request's newest tokens over its paged 8-bit cache.
+//
+// Row t of the q_len newest tokens stands at position p = seq_len - q_len + t and sees the tokens
+// j <= p with, under a window, p - window < j or j < sinks:
+//   out_t = sum_j softmax_j(scale q_t . k_j) v_j,    zero for a row that sees nothing.
+//
+// Decomposition.  The rows of one request and cached head (tokens x query heads of its group)
+// are cut into chunks of up to 64, the tokens into splits; a workgroup takes one (chunk, split)
+// and its four wavefronts take the 32-token tiles of it in turn, each on its own: a wavefront
+// holds its rows' queries and outputs in registers, streams keys and values from memory into
+// operand registers in the order in which the cache keeps them, and meets the other three only
+// at the end.  No LDS and no barrier lies on the way of a tile.
+//
+// Per tile, with the 16x16x32 matrix instructions (lane = 16 g + n):
+//   S^T = K Q^T: rows are tokens, columns query rows, so lane (n, g) gets the scores of query
+//         row n for tokens 16 j + 4 g + i, j < 2, i < 4;
+//   O^T = V^T P^T: the same eight tokens are the contraction slots that the lane has to supply
+//         of P^T, so the probabilities stay where they are, and the values are stored with the
+//         tokens of a block in that order.
+// Codes become 16-bit operands exactly: four significant bits, and the block's power of two
+// is applied by the conversion relative to a reference exponent (kept so that the products stay
+// normal numbers in fp16), whose own power of two sits in the softmax scale (keys) or in
+// the unit of the output sums (values).  A change of the values' reference rescales the sums.
+//
+// Softmax.  One pass with a running maximum m per row, in base 2.  P = 2^(s - m + 8) in fp16: m
+// follows a new maximum only once a score passes m + 7 (P would near fp16's largest value), so
+// most tiles touch neither the sums nor the other lanes.  Weights down to 2^-22 of the largest
+// keep fp16's full 11 bits; their rounding (2^-11 relative) is the only one between the
+// stored values and the fp32 sums.  The denominators add the unrounded weights in fp32.
+//
+// A NaN among the values reaches only the rows that see its token: a tile that some row does not
+// see in full is searched for NaN codes, and where there are any they are taken out of the
+// product and put into the visible rows by a second one over indicators.
+#include "kv_attention.h"
+
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+
+namespace sfx {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr float kPShift = 8.f;   // P = 2^(s - m + kPShift)
+constexpr float kPLimit = 15.f;  // m moves when some s - m + kPShift passes this
+constexpr float kNoMax = -1e30f;
+constexpr int kRefLo = -5, kRefHi = 7;  // block exponent minus reference: code * 2^that is normal
+                                        // in fp16 (2^-9 * 2^-5 = 2^-14, 448 * 2^7 < 65504)
+
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+struct Bf16 {
+  using Vec = bf16x8;
+  static __device__ Vec widen(unsigned lo, unsigned hi, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return Vec{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+  static __device__ f32x4 mfma(Vec a, Vec b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ unsigned pack(float a, float b) {
+    const bf16x2 v{(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(unsigned, v);
+  }
+};
+
+struct Fp16 {
+  using Vec = f16x8;
+  static __device__ Vec widen(unsigned lo, unsigned hi, float scale) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, false);
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, true);
+    return Vec{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+  static __device__ f32x4 mfma(Vec a, Vec b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ unsigned pack(float a, float b) {
+    const f16x2 v{(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(unsigned, v);
+  }
+};
+
+// Largest / sum over the four lane groups g of a row (lanes n, n + 16, n + 32, n + 48).
+__device__ __forceinline__ float group_max(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float group_sum(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// What rows [r0, r0 + n) of request b look at: tiles [0, nsink) for the sinks, then
+// [first, last).  Tile i of the list is i < nsink ? i : first + i - nsink.
+struct Span {
+  int pos0;  // position of the first of the newest tokens
+  int rows;  // live rows of the request and head
+  int lo_pos, hi_pos;
+  int nsink, first, tiles;
+};
+
+__device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int r0, int n) {
+  Span s{};
+  const int cap = a.max_pages * a.c.page_size;
+  int len = a.seq_lens[b], nq = a.q_lens ? a.q_lens[b] : a.T;
+  len = len < 0 ? 0 : (len > cap ? cap : len);
+  nq = nq < 0 ? 0 : (nq > a.T ? a.T : nq);
+  s.pos0 = len - nq;
+  s.rows = nq * a.group;
+  const int r1 = r0 + n < s.rows ? r0 + n : s.rows;
+  if (r0 >= r1) return s;
+  s.lo_pos = s.pos0 + r0 / a.group;
+  s.hi_pos = s.pos0 + (r1 - 1) / a.group;
+  const int end = s.hi_pos + 1;
+  if (end <= 0) return s;
+  const int64_t from = a.window > 0 ? (int64_t)s.lo_pos - a.window + 1 : 0;
+  const int lo = from < 0 ? 0 : (int)from;
+  s.first = lo / kKvBlock;
+  const int sinks = a.sinks < end ? a.sinks : end;
+  s.nsink = (sinks + kKvBlock - 1) / kKvBlock;
+  s.nsink = s.nsink < s.first ? s.nsink : s.first;
+  s.tiles = s.nsink + (end + kKvBlock - 1) / kKvBlock - s.first;
+  return s;
+}
+
+// One tile's codes and scales as they come from memory.
+template <int D>
+struct Tile {
+  u32x4 k[D / 32];
+  u32x4 v[D / 32];
+  float ks, vs;
+  bool mapped;
+};
+
+// Block number of list entry i; its page id (-1: unmapped), read through the scalar cache.
+__device__ __forceinline__ int block_of(const Span& s, int i) {
+  return __builtin_amdgcn_readfirstlane(i < s.nsink ? i : s.first + i - s.nsink);
+}
+__device__ __forceinline__ int page_id(const KvAttentionArgs& a, const int32_t* table, int block) {
+  return __builtin_amdgcn_readfirstlane(table[kv_page_of(a.c, block)]);
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(Tile<D>& t, const KvAttentionArgs& a, int h, int block,
+                                          int page, int lane) {
+  t.mapped = page >= 0 && page < a.c.num_pages;
+  if (!t.mapped) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) t.k[c] = t.v[c] = u32x4{0, 0, 0, 0};
+    t.ks = t.vs = 1.f;
+    return;
+  }
+  const int per_page = a.c.page_size / kKvBlock;
+  const int sub = block - kv_page_of(a.c, block) * per_page;
+  const int64_t ph = (int64_t)page * a.c.heads + h;
+  const uint8_t* kb = a.c.k + ph * a.c.page_size * D + (int64_t)sub * kKvBlock * 64;
+  const uint8_t* vb = a.c.v + ph * a.c.page_size * D + (int64_t)sub * kKvBlock * D;
+  const int off = (lane & 15) * 64 + (lane >> 4) * 16;
+#pragma unroll
+  for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+      t.k[tt * (D / 64) + j] =
+          *(const u32x4*)(kb + (int64_t)j * a.c.page_size * 64 + tt * 1024 + off);
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) t.v[c] = *(const u32x4*)(vb + c * 1024 + off);
+  t.ks = a.c.k_scale[ph * per_page + sub];
+  t.vs = a.c.v_scale[ph * per_page + sub];
+}
+
+// Bytes of a dword that are e4m3 NaNs, as 0x80 flags.
+__device__ __forceinline__ unsigned nan_bytes(unsigned w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// One (chunk, split): RT 16-row tiles by the split's tokens.
+template <typename T, int D, int RT>
+__global__ __launch_bounds__(64 * kWaves) void kv_attention_kernel(KvAttentionArgs a) {
+  constexpr int kSlabs = D / 64, kVc = D / 32;
+  constexpr int kPiece = D < 128 ? D : 128;  // dims of one pass of the final reduction
+  __shared__ float red[kWaves][16][kPiece + 4];
+  __shared__ float sm[kWaves][RT * 16], sl[kWaves][RT * 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = lane & 15, g = lane >> 4;
+
+  // Workgroups of one (request, head, split) share its keys and values: their ids are 8 apart, so
+  // they run on one XCD and meet in its L2.
+  const int per8 = 8 * a.chunks;
+  const int chunk = (int)(blockIdx.x % per8) / 8;
+  int64_t gi = (int64_t)(blockIdx.x / per8) * 8 + blockIdx.x % 8;
+  const int split = (int)(gi % a.splits);
+  gi /= a.splits;
+  const int h = (int)(gi % a.c.heads);
+  const int64_t b64 = gi / a.c.heads;
+  if (b64 >= a.B) return;
+  const int b = (int)b64;
+  const int r0 = chunk * RT * 16, all_rows = a.T * a.group;
+  const Span s = span_of(a, b, r0, RT * 16);
+  const int i0 = split * a.tiles_per_split;
+  if (split > 0 && i0 >= s.tiles) return;
+  const int i1 = i0 + a.tiles_per_split < s.tiles ? i0 + a.tiles_per_split : s.tiles;
+  const int active = (s.tiles + a.tiles_per_split - 1) / a.tiles_per_split;
+
+  // queries as the second operand: dims 64 j + 16 g + 8 f + i of row n
+  typename T::Vec q[RT][2 * kSlabs];
+  int pos[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int row = r0 + rt * 16 + n;
+    const int t = row / a.group;
+    const bool live = row < s.rows;
+    pos[rt] = live ? s.pos0 + t : -1;
+    const char* p = (const char*)a.q +
+                    (b * a.qs.batch + t * a.qs.token + (h * a.group + row % a.group) * a.qs.head) *
+                        2 + g * 32;
+#pragma unroll
+    for (int m = 0; m < 2 * kSlabs; ++m) {
+      const u32x4 w = live ? (u32x4) * (const u32x4_a2*)(p + (m >> 1) * 128 + (m & 1) * 16)
+                           : u32x4{0, 0, 0, 0};
+      q[rt][m] = __builtin_bit_cast(typename T::Vec, w);
+    }
+  }
+
+  f32x4 o[RT][kVc][2];
+  float mx[RT], l[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    mx[rt] = kNoMax;
+    l[rt] = 0.f;
+#pragma unroll
+    for (int c = 0; c < kVc; ++c) o[rt][c][0] = o[rt][c][1] = f32x4{0, 0, 0, 0};
+  }
+  int kref = 0, vref = 0;
+  float cs = a.scale_log2;
+  bool first_tile = true;
+
+  const int32_t* table = a.page_table + (int64_t)b * a.max_pages;
+  Tile<D> cur;
+  int i = i0 + wave;
+  int nblock = 0, npage = -1;
+  if (i < i1) {
+    const int blk = block_of(s, i);
+    load_tile<D>(cur, a, h, blk, page_id(a, table, blk), lane);
+    if (i + kWaves < i1) {
+      nblock = block_of(s, i + kWaves);
+      npage = page_id(a, table, nblock);
+    }
+  }
+  for (; i < i1; i += kWaves) {
+    const int block = block_of(s, i);
+    Tile<D> nxt;
+    if (i + kWaves < i1) {
+      load_tile<D>(nxt, a, h, nblock, npage, lane);
+      if (i + 2 * kWaves < i1) {
+        nblock = block_of(s, i + 2 * kWaves);
+        npage = page_id(a, table, nblock);
+      }
+    }
+    // reference exponents
+    const int ek = __builtin_amdgcn_readfirstlane(kv_exp_of(cur.ks));
+    const int ev = __builtin_amdgcn_readfirstlane(kv_exp_of(cur.vs));
+    if (first_tile || ek - kref < kRefLo || ek - kref > kRefHi) {
+      kref = ek - 1;
+      cs = a.scale_log2 * kv_pow2(kref);
+    }
+    if (first_tile || ev - vref < kRefLo || ev - vref > kRefHi) {
+      const float f = kv_pow2(first_tile ? 0 : vref - (ev - 1));
+      vref = ev - 1;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int c = 0; c < kVc; ++c) {
+          o[rt][c][0] *= f;
+          o[rt][c][1] *= f;
+        }
+    }
+    first_tile = false;
+
+    // scores
+    const float kscale = kv_pow2(ek - kref);
+    f32x4 sc[RT][2];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) sc[rt][0] = sc[rt][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+      for (int m = 0; m < 2 * kSlabs; ++m) {
+        const u32x4 w = cur.k[tt * kSlabs + (m >> 1)];
+        const auto kf = T::widen(w[2 * (m & 1)], w[2 * (m & 1) + 1], kscale);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sc[rt][tt] = T::mfma(kf, q[rt][m], sc[rt][tt]);
+      }
+
+    // masks: only where some row does not see the whole tile
+    const int j0 = block * kKvBlock;
+    const bool whole = cur.mapped && j0 + kKvBlock - 1 <= s.lo_pos &&
+                       (a.window == 0 || s.hi_pos - j0 < a.window || j0 + kKvBlock <= a.sinks);
+    unsigned seen[RT];  // bit 4 tt + i: the lane's row sees token 16 tt + 4 g + i
+    if (!whole) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        seen[rt] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = j0 + 16 * (e >> 2) + 4 * g + (e & 3);
+          const bool see = cur.mapped && j <= pos[rt] &&
+                           (a.window == 0 || pos[rt] - j < a.window || j < a.sinks);
+          if (see) seen[rt] |= 1u << e;
+          sc[rt][e >> 2][e & 3] = see ? sc[rt][e >> 2][e & 3] : -__builtin_inff();
+        }
+      }
+    }
+
+    // running maximum
+    bool move = false;
+    float top[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float t = sc[rt][0][0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) t = fmaxf(t, sc[rt][e >> 2][e & 3]);
+      top[rt] = t;
+      move |= fmaf(t, cs, kPShift - mx[rt]) > kPLimit;
+    }
+    if (__any(move)) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float m = fmaxf(mx[rt], group_max(top[rt]) * cs);
+        const float f = __builtin_amdgcn_exp2f(mx[rt] - m);
+        mx[rt] = m;
+        l[rt] *= f;
+#pragma unroll
+        for (int c = 0; c < kVc; ++c) {
+          o[rt][c][0] *= f;
+          o[rt][c][1] *= f;
+        }
+      }
+    }
+    f16x8 p[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const float bias = kPShift - mx[rt];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(sc[rt][e >> 2][e & 3], cs, bias));
+        l[rt] += x;
+        p[rt][e] = (_Float16)x;
+      }
+    }
+
+    // outputs
+    const float vscale = kv_pow2(ev - vref);
+    bool bad = false;
+    if (!whole) {
+      unsigned f = 0;
+#pragma unroll
+      for (int c = 0; c < kVc; ++c)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) f |= nan_bytes(cur.v[c][d]);
+      bad = __any(f != 0);
+    }
+    if (!bad) {
+#pragma unroll
+      for (int c = 0; c < kVc; ++c)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const f16x8 vf = Fp16::widen(cur.v[c][2 * f], cur.v[c][2 * f + 1], vscale);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            o[rt][c][f] = Fp16::mfma(vf, p[rt], o[rt][c][f]);
+        }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kVc; ++c)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const unsigned w0 = cur.v[c][2 * f], w1 = cur.v[c][2 * f + 1];
+          // 0x80 flags widened to whole bytes; 0x38 is the code of 1
+          const unsigned n0 = (nan_bytes(w0) >> 7) * 255u, n1 = (nan_bytes(w1) >> 7) * 255u;
+          const f16x8 vf = Fp16::widen(w0 & ~n0, w1 & ~n1, vscale);
+          const f16x8 nf = Fp16::widen(n0 & 0x38383838u, n1 & 0x38383838u, 1.f);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            f16x8 see;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              see[e] = (seen[rt] >> e & 1) ? (_Float16)1.f : (_Float16)0.f;
+            f32x4 x = Fp16::mfma(vf, p[rt], o[rt][c][f]);
+            const f32x4 hit = Fp16::mfma(nf, see, f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = hit[e] > 0.f ? __builtin_nanf("") : x[e];
+            o[rt][c][f] = x;
+          }
+        }
+    }
+    cur = nxt;
+  }
+
+  // The four wavefronts' sums, brought to one maximum per row and to the values' own unit.
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    l[rt] = group_sum(l[rt]);
+    if (g == 0) {
+      sm[wave][rt * 16 + n] = mx[rt];
+      sl[wave][rt * 16 + n] = l[rt];
+    }
+  }
+  __syncthreads();
+  const float unit = kv_pow2(vref);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    float m = sm[0][rt * 16 + n];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sm[w][rt * 16 + n]);
+    const float f = __builtin_amdgcn_exp2f(mx[rt] - m) * unit;
+#pragma unroll
+    for (int c0 = 0; c0 < kVc; c0 += kPiece / 32) {
+#pragma unroll
+      for (int c = 0; c < kPiece / 32; ++c) {
+        f32x4 lo, hi;  // dims 32 c + 8 g + 0..7: element i of half f is dim 2 i + f
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          lo[e] = o[rt][c0 + c][e & 1][e >> 1] * f;
+          hi[e] = o[rt][c0 + c][e & 1][2 + (e >> 1)] * f;
+        }
+        *(f32x4*)&red[wave][n][32 * c + 8 * g] = lo;
+        *(f32x4*)&red[wave][n][32 * c + 8 * g + 4] = hi;
+      }
+      __syncthreads();
+      constexpr int kPer = kPiece / 16;  // dims of one thread
+      const int rr = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * kPer;
+      const int row = r0 + rt * 16 + rr;
+      if (row < all_rows) {
+        float mm = sm[0][rt * 16 + rr], ll = 0.f;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, sm[w][rt * 16 + rr]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+          ll += sl[w][rt * 16 + rr] * __builtin_amdgcn_exp2f(sm[w][rt * 16 + rr] - mm);
+        float x[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; e += 4) {
+          f32x4 v = *(const f32x4*)&red[0][rr][d0 + e];
+#pragma unroll
+          for (int w = 1; w < kWaves; ++w) v += *(const f32x4*)&red[w][rr][d0 + e];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[e + k] = v[k];
+        }
+        const bool none = ll == 0.f || row >= s.rows;  // sees nothing, or past q_len
+        const float inv = 1.f / ll;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[e] = none ? 0.f : x[e] * inv;
+        const int d = c0 * 32 + d0;
+        if (active > 1) {
+          const int64_t rows = (int64_t)a.B * a.c.heads * all_rows;
+          const int64_t at = split * rows + ((int64_t)b * a.c.heads + h) * all_rows + row;
+#pragma unroll
+          for (int e = 0; e < kPer; e += 4)
+            *(f32x4*)(a.part_o + at * D + d + e) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+          if (d == 0)
+            a.part_lse[at] = none ? -__builtin_inff() : mm + __builtin_amdgcn_logf(ll);
+        } else {
+          const int64_t at =
+              ((int64_t)b * a.T + row / a.group) * a.c.heads * a.group + h * a.group +
+              row % a.group;
+          unsigned* p = (unsigned*)((char*)a.out + (at * D + d) * 2);
+#pragma unroll
+          for (int e = 0; e < kPer; e += 2) p[e / 2] = T::pack(x[e], x[e + 1]);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Joins the splits of the rows that had more than one: one wavefront per row.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chunk_rows) {
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int all_rows = a.T * a.group;
+  const int64_t rows = (int64_t)a.B * a.c.heads * all_rows;
+  if (at >= rows) return;
+  const int row = (int)(at % all_rows);
+  const int h = (int)(at / all_rows % a.c.heads);
+  const int b = (int)(at / all_rows / a.c.heads);
+  const Span s = span_of(a, b, row / chunk_rows * chunk_rows, chunk_rows);
+  const int active = (s.tiles + a.tiles_per_split - 1) / a.tiles_per_split;
+  if (active <= 1) return;
+  float m = -__builtin_inff();
+  for (int i = 0; i < active; ++i) m = fmaxf(m, a.part_lse[i * rows + at]);
+  constexpr int kPer = D / 64;
+  float x[kPer] = {}, l = 0.f;
+  for (int i = 0; i < active; ++i) {
+    const float e = a.part_lse[i * rows + at];
+    const float w = e == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(e - m);
+    l += w;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      x[k] += w * a.part_o[(i * rows + at) * D + lane * kPer + k];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t out =
+      ((int64_t)b * a.T + row / a.group) * a.c.heads * a.group + h * a.group + row % a.group;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const unsigned short v = (unsigned short)T::pack(x[k] * inv, 0.f);
+    ((unsigned short*)a.out)[out * D + lane * kPer + k] = v;
+  }
+}
+
+int max_row_tiles(int dim) { return dim > 128 ? 2 : 4; }
+
+int row_tiles(const KvAttentionArgs& a, int dim, int* chunks) {
+  const int64_t tiles = ((int64_t)a.T * a.group + 15) / 16;
+  const int most = max_row_tiles(dim);
+  *chunks = (int)((tiles + most - 1) / most);
+  return (int)((tiles + *chunks - 1) / *chunks);
+}
+
+}  // namespace
+
+size_t kv_attention_plan(KvAttentionArgs* a, int dim) {
+  row_tiles(*a, dim, &a->chunks);
+  const int64_t cap = (int64_t)a->max_pages * a->c.page_size;
+  if (a->window >= cap + a->T) a->window = 0;
+  int64_t tiles = (cap + kKvBlock - 1) / kKvBlock;
+  if (a->window > 0) {
+    const int64_t seen = ((int64_t)a->window + a->T) / kKvBlock + 2 +
+                         ((int64_t)a->sinks + kKvBlock - 1) / kKvBlock;
+    tiles = seen < tiles ? seen : tiles;
+  }
+  // Enough workgroups for the 256 CUs twice over, and at least four tiles a wavefront.
+  const int64_t pairs = (int64_t)a->B * a->c.heads * a->chunks;
+  int64_t splits = pairs > 0 ? (512 + pairs - 1) / pairs : 1;
+  const int64_t most = tiles / (4 * kWaves);
+  splits = splits > most ? most : splits;
+  splits = splits < 1 ? 1 : splits;
+  a->tiles_per_split = (int)((tiles + splits - 1) / splits);
+  if (a->tiles_per_split < 1) a->tiles_per_split = 1;
+  a->splits = (int)splits;
+  if (splits == 1) return 0;
+  const size_t rows = (size_t)a->B * a->c.heads * a->T * a->group;
+  return (size_t)splits * rows * (dim + 1) * sizeof(float);
+}
+
+void kv_attention_place(KvAttentionArgs* a, int dim, void* workspace) {
+  const size_t rows = (size_t)a->B * a->c.heads * a->T * a->group;
+  a->part_o = (float*)workspace;
+  a->part_lse = a->part_o + (size_t)a->splits * rows * dim;
+}
+
+namespace {
+
+template <typename T, int D>
+hipError_t launch_dim(const KvAttentionArgs& a, hipStream_t st) {
+  int chunks = 0;
+  const int rt = row_tiles(a, D, &chunks);
+  const int64_t groups = (int64_t)a.B * a.c.heads * a.splits;
+  const dim3 grid((unsigned)((groups + 7) / 8 * 8 * a.chunks));
+  const dim3 block(64 * kWaves);
+  if (rt == 1)
+    hipLaunchKernelGGL((kv_attention_kernel<T, D, 1>), grid, block, 0, st, a);
+  else if (rt == 2)
+    hipLaunchKernelGGL((kv_attention_kernel<T, D, 2>), grid, block, 0, st, a);
+  if constexpr (D <= 128) {
+    if (rt == 3)
+      hipLaunchKernelGGL((kv_attention_kernel<T, D, 3>), grid, block, 0, st, a);
+    else if (rt == 4)
+      hipLaunchKernelGGL((kv_attention_kernel<T, D, 4>), grid, block, 0, st, a);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t rows = (int64_t)a.B * a.c.heads * a.T * a.group;
+  hipLaunchKernelGGL((kv_join_kernel<T, D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a,
+                     rt * 16);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_type(const KvAttentionArgs& a, int dim, hipStream_t st) {
+  if (dim == 64) return launch_dim<T, 64>(a, st);
+  if (dim == 128) return launch_dim<T, 128>(a, st);
+  return launch_dim<T, 256>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_kv_attention(const KvAttentionArgs& a, int dim, KvType type, hipStream_t st) {
+  if (a.B <= 0 || a.T <= 0) return hipSuccess;
+  return type == kFp16 ? launch_type<Fp16>(a, dim, st) : launch_type<Bf16>(a, dim, st);
+}
+
+}  // namespace sfx

@@ -22,6 +22,7 @@
 #include "call_forms.h"
 #include "checks.h"
 #include "delta_index.h"
+#include "errors.h"
 #include "noalloc.h"
 #include "propose.h"
 #include "sa_build.h"
@@ -29,8 +30,10 @@
 using namespace sfx;
 
 namespace {
-
 thread_local std::string g_err = "no error";
+}
+
+namespace sfx {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -46,11 +49,9 @@ int hip_fail(hipError_t e, const char* what) {
   return fail(SFX_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-#define HIP_OR_RETURN(expr, what)                  \
-  do {                                             \
-    hipError_t e_ = (expr);                        \
-    if (e_ != hipSuccess) return hip_fail(e_, what); \
-  } while (0)
+}  // namespace sfx
+
+namespace {
 
 constexpr int kIngestChunk = 65536;  // documents per ingest launch
 

@@ -1,0 +1,243 @@
+"""Draft verification against the model in 64 bits (tests/kv_model.py): tokens and counts are
+compared exactly."""
+import numpy as np
+import pytest
+
+from tests import kv_model as M
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def S():
+    import torch
+
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    import suffix_match_drafter_amd as sfx
+
+    sfx.load()
+    return sfx
+
+
+def dev(a):
+    import torch
+
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def case(rng, B, k, V, dtype, take=0.6):
+    """Logits [B, k + 1, V] in `dtype`, drafts that the target likes with chance `take`."""
+    import torch
+
+    x = rng.standard_normal((B, k + 1, V)) * 2
+    draft = rng.integers(0, V, size=(B, k)).astype(np.int32)
+    like = rng.random((B, k)) < take
+    for b in range(B):
+        for i in range(k):
+            if like[b, i]:
+                x[b, i, draft[b, i]] = np.log(V) + 3
+    t = torch.from_numpy(x).to(getattr(torch, dtype))
+    return t.cuda(), draft, rng.integers(0, k + 1, size=B).astype(np.int32), \
+        rng.random((B, k)).astype(np.float32), rng.random(B).astype(np.float32), \
+        rng.uniform(0.3, 2.0, B).astype(np.float32)
+
+
+def check(S, logits, draft, nv, ua, us, temp):
+    import torch
+
+    out, na = S.verify(logits, dev(draft), None if nv is None else dev(nv), dev(ua), dev(us),
+                       None if temp is None else dev(temp))
+    torch.cuda.synchronize()
+    x = logits.double().cpu().numpy()
+    B, k1 = x.shape[:2]
+    for b in range(B):
+        s, n = M.verify(x[b], draft[b], k1 - 1 if nv is None else nv[b], ua[b], us[b],
+                        1.0 if temp is None else float(temp[b]))
+        assert na[b].item() == n and np.array_equal(out[b].cpu().numpy(), s), \
+            (b, out[b].tolist(), s, na[b].item(), n)
+    return out, na
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("B,k,V", [(1, 1, 1), (3, 2, 2), (5, 4, 7), (8, 8, 1000), (4, 32, 513),
+                                   (16, 3, 4099), (2, 16, 40001), (1, 5, 151936)])
+def test_against_model(S, B, k, V, dtype):
+    rng = np.random.default_rng(B * 100 + V)
+    check(S, *case(rng, B, k, V, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_greedy(S, dtype):
+    """T = 0, below 0 and NaN; ties go to the lowest index, also across the row's parts."""
+    rng = np.random.default_rng(1)
+    x, draft, nv, ua, us, temp = case(rng, 8, 4, 40000, dtype)
+    temp[:] = [0.0, -1.0, np.nan, -np.inf, 0.0, 0.0, 1.0, -0.0]
+    x[4, :, 39990] = 50.0
+    x[4, :, 17] = 50.0
+    x[5, 0] = 1.0
+    draft[5, 0], nv[5] = 0, 4
+    check(S, x, draft, nv, ua, us, temp)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+def test_masked_logits(S, dtype):
+    """-inf and the type's lowest value as masks, NaN, +inf, rows that leave nothing or one."""
+    import torch
+
+    rng = np.random.default_rng(2)
+    x, draft, nv, ua, us, temp = case(rng, 12, 3, 300, dtype)
+    low = torch.finfo(x.dtype).min
+    nv[:] = 3
+    x[0, :, 50:] = -float("inf")
+    x[1, :, 50:] = low
+    x[2] = -float("inf")
+    x[3] = float("nan")
+    x[4, :, 5] = float("nan")
+    x[5, 0, [7, 9]] = float("inf")
+    draft[5, 0] = 9
+    x[6] = -float("inf")
+    x[6, :, 123] = 0.0
+    draft[6] = [123, 5, 123]
+    x[7] = low
+    x[8] = 1.0
+    x[9, 0, :] = float("inf")
+    temp[8:10] = [np.inf, 1e-30]
+    x[10] = -float("inf")
+    x[10, :, 40] = 3.0
+    draft[10] = [40, 40, 40]
+    temp[10] = 0.0
+    x[11] = float("nan")
+    temp[11] = 0.0
+    check(S, x, draft, nv, ua, us, temp)
+    temp[:] = np.inf
+    check(S, x, draft, nv, ua, us, temp)
+    temp[:] = np.float32(1e-42)
+    check(S, x, draft, nv, ua, us, temp)
+
+
+def test_borders(S):
+    """Tests and draws whose two sides are equal in exact arithmetic, or one float apart."""
+    import torch
+
+    V, k, B = 8, 2, 64
+    x = torch.zeros((B, k + 1, V), device="cuda")       # every weight is exactly 1
+    draft = np.tile(np.arange(2, dtype=np.int32), (B, 1))
+    nv = np.full(B, k, np.int32)
+    ua, us = np.zeros((B, k), np.float32), np.zeros(B, np.float32)
+    eighth = np.float32(0.125)
+    ua[:16] = eighth                                     # u Z = w: not accepted
+    ua[16:32] = np.nextafter(eighth, np.float32(0))      # accepted
+    ua[32:48] = np.nextafter(eighth, np.float32(1))
+    for b in range(B):
+        # running sums of 7 (a rejected draft) or 8 equal weights: their borders exactly
+        us[b] = np.float32(b % 8) * eighth
+    us[-1] = np.nextafter(np.float32(1), np.float32(0))
+    check(S, x, draft, nv, ua, us, None)
+    check(S, x, draft, None, ua, us, np.full(B, 0.7, np.float32))
+
+
+def test_drafts_outside_the_vocabulary(S):
+    rng = np.random.default_rng(3)
+    x, draft, nv, ua, us, temp = case(rng, 6, 3, 100, "float32")
+    nv[:] = [3, 3, 3, 7, -2, 0]
+    draft[0, 0], draft[1, 0], draft[2, 1] = -1, 100, 2 ** 31 - 1
+    draft[3] = -2 ** 31
+    ua[:] = 0.0
+    check(S, x, draft, nv, ua, us, temp)
+    temp[:] = 0.0
+    check(S, x, draft, nv, ua, us, temp)
+
+
+def test_flat_and_peaked_rows(S):
+    """Draws along a flat large row (every border is within a float's rounding of the next) and
+    from rows with one heavy token; all random numbers, 0 and the largest below 1."""
+    import torch
+
+    V, B = 100003, 48
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x = torch.randn((B, 1, V), generator=g, device="cuda") * 0.01
+    x[24:, :, 77777] = 14.0
+    us = np.linspace(0, 1, B, endpoint=False).astype(np.float32)
+    us[23] = us[47] = np.nextafter(np.float32(1), np.float32(0))
+    empty = np.zeros((B, 0), np.int32)
+    check(S, x, empty, None, empty.astype(np.float32), us, None)
+    check(S, x.to(torch.bfloat16), empty, np.full(B, 5, np.int32), empty.astype(np.float32), us,
+          np.full(B, 0.8, np.float32))
+
+
+def test_strides_and_outputs(S):
+    """Rows of a wider buffer at odd offsets; given outputs; nothing past num_valid is read."""
+    import torch
+
+    rng = np.random.default_rng(5)
+    B, k, V = 5, 6, 1001
+    x, draft, nv, ua, us, temp = case(rng, B, k, V, "bfloat16")
+    wide = torch.full((k + 1, B, V + 7), float("nan"), dtype=torch.bfloat16, device="cuda")
+    view = wide[:, :, 3:3 + V].transpose(0, 1)
+    view.copy_(x)
+    a = check(S, view, draft, nv, ua, us, temp)
+    out = torch.full((B, k + 1), 9, dtype=torch.int32, device="cuda")
+    na = torch.full((B,), 9, dtype=torch.int32, device="cuda")
+    got = S.verify(x, dev(draft), dev(nv), dev(ua), dev(us), dev(temp), sampled=out,
+                   num_accepted=na)
+    assert got[0] is out and got[1] is na
+    assert torch.equal(out, a[0]) and torch.equal(na, a[1])
+    for b in range(B):
+        x[b, nv[b] + 1:] = float("inf")
+    assert torch.equal(S.verify(x, dev(draft), dev(nv), dev(ua), dev(us), dev(temp))[0], out)
+    assert S.verify(x[:0], dev(draft)[:0], None, dev(ua)[:0], dev(us)[:0])[0].shape == (0, k + 1)
+
+
+def test_graph_and_stream(S):
+    import torch
+
+    rng = np.random.default_rng(6)
+    B, k, V = 7, 4, 30011
+    x, draft, nv, ua, us, temp = case(rng, B, k, V, "float16")
+    bufs = [x.clone(), dev(draft), dev(nv), dev(ua), dev(us), dev(temp)]
+    out = torch.empty((B, k + 1), dtype=torch.int32, device="cuda")
+    na = torch.empty((B,), dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        S.verify(*bufs, sampled=out, num_accepted=na, stream=s)
+    for step in range(4):
+        new = case(rng, B, k, V, "float16")
+        for b, n in zip(bufs, new):
+            b.copy_(n if isinstance(n, torch.Tensor) else dev(n))
+        out.fill_(-7)
+        g.replay()
+        want = check(S, *new)
+        assert torch.equal(out, want[0]) and torch.equal(na, want[1]), step
+        s.wait_stream(torch.cuda.current_stream())
+        mine = S.verify(*bufs, stream=s)
+        s.synchronize()
+        assert torch.equal(mine[0], want[0]) and torch.equal(mine[1], want[1])
+
+
+def test_step_with_the_drafter(S):
+    """propose -> verify -> feedback and update: the verifier's outputs are the drafter's next
+    inputs, and a greedy target that repeats the draft accepts all of it."""
+    import torch
+
+    rng = np.random.default_rng(8)
+    B, Sq, V, k = 4, 64, 50, 8
+    d = S.Drafter(S.Config(k=k, max_tree_depth=8, max_batch=B, max_seq=Sq, max_sampled=k + 1))
+    period = rng.integers(0, V, size=(B, 5)).astype(np.int32)
+    tok = dev(np.tile(period, (1, 13))[:, :Sq])
+    n = dev(np.full(B, 20, np.int32))
+    samp = torch.full((B, k + 1), -1, dtype=torch.int32, device="cuda")
+    samp[:, 0] = tok[:, 20]
+    draft, nv = d.propose(n, tok, samp)
+    logits = torch.zeros((B, k + 1, V), device="cuda")
+    want = torch.from_numpy(np.tile(period, (1, 13))[:, 21:21 + k + 1]).cuda()
+    logits.scatter_(2, want.long()[:, :, None], 5.0)
+    zero = torch.zeros((B,), device="cuda")
+    out, na = S.verify(logits, draft, nv, torch.zeros((B, k), device="cuda"), zero, zero)
+    assert na.tolist() == nv.tolist() == [k] * B and torch.equal(out, want)
+    d.accept_feedback(na)
+    after = S.update_state(tok.clone(), S.update_state(tok, n, samp), out)
+    assert after.tolist() == [21 + k + 1] * B
+    d.close()
