@@ -232,7 +232,7 @@ int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batc
   a.u_sample = u_sample;
   a.sampled = sampled;
   a.num_accepted = num_accepted;
-  a.part = (VerifyPart*)workspace;
+  verify_place(&a, workspace);
   HIP_OR_RETURN(launch_verify(a, kv_type(type), (hipStream_t)stream), "verify launch");
   return SFX_OK;
 }

@@ -9,7 +9,7 @@
 
 namespace sfx {
 
-// What one workgroup saw of its part of a row.
+// What one workgroup saw of its part of a row (or of all of it).
 struct VerifyPart {
   float m;     // largest logit (-inf: none)
   float s;     // sum of 2^((l - m) / (T ln 2))
@@ -28,13 +28,20 @@ struct VerifyArgs {
   const float* u_sample;
   int32_t* sampled;
   int32_t* num_accepted;
-  // plan
+  // plan (verify_plan)
+  bool in_order;      // one workgroup per row, in slot order, rows past a rejection left out
   int32_t parts;      // workgroups of one row
   int32_t part_size;  // its logits
   VerifyPart* part;   // [B][k + 1][parts]
+  int32_t* stop;      // [B] lowest slot known to be rejected (in_order), else NULL
 };
 
+// Fills the plan from the shapes; returns the workspace bytes it needs.
 size_t verify_plan(VerifyArgs* a);
+
+// Places the plan's buffers in the workspace.
+void verify_place(VerifyArgs* a, void* workspace);
+
 hipError_t launch_verify(const VerifyArgs& a, KvType type, hipStream_t st);
 
 }  // namespace sfx

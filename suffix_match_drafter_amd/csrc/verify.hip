@@ -10,10 +10,15 @@
 // T = 0 (or less, or NaN) is greedy: a draft is accepted when it is the row's largest logit (the
 // lowest index of equals), which is also what is drawn.  A NaN logit counts as -inf.
 //
-// Precision.  The statistics of all rows come from one pass in fp32 (memory-bound).  Both
-// comparisons decide a token, so neither is left to rounding: a test whose two sides are within
-// the fp32 pass's error bound is redone in fp64, and the row that is drawn from is summed
-// and searched in fp64.
+// Precision.  A row's statistics (maximum, sum) come from one pass in fp32, bounded by the
+// reading of the logits.  Both comparisons decide a token, so neither is left to rounding: a
+// test whose two sides are within the fp32 pass's error bound is redone in fp64, and the row that
+// is drawn from is summed and searched in fp64.
+//
+// Work.  Rows past the first rejection decide nothing.  Large calls take one workgroup per row in
+// slot order: a row of a request that is known to have been rejected earlier is not read (the
+// dispatch order makes the look-ahead about one slot of the batch).  Small calls, which do not
+// fill the card with whole rows, read all rows in parts at once.
 #include "verify.h"
 
 #include <hip/hip_bf16.h>
@@ -23,10 +28,10 @@ namespace sfx {
 
 namespace {
 
-constexpr int kStatThreads = 256;
-constexpr int kPickThreads = 1024;
-constexpr int kPickWaves = kPickThreads / 64;
-constexpr int kMaxRows = 33;  // k + 1
+constexpr int kPartThreads = 256;   // workgroup of a part of a row
+constexpr int kRowThreads = 1024;   // workgroup of a whole row, and of a request's draw
+constexpr int kRowWaves = kRowThreads / 64;
+constexpr int kMaxRows = 33;        // k + 1
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
@@ -38,10 +43,10 @@ __device__ __forceinline__ float from_half(unsigned short b) {
   return (float)h;
 }
 
-// A logit as the sums take it: NaN is -inf; +inf becomes the largest float, so that equal
-// infinities differ by 0 and share the row.
+// A logit as the sums take it: NaN is -inf (a maximum drops it); +inf becomes the largest float,
+// so that equal infinities differ by 0 and share the row.
 __device__ __forceinline__ float clean(float x) {
-  return x == x ? fminf(x, 3.402823466e38f) : -__builtin_inff();
+  return fminf(fmaxf(x, -__builtin_inff()), 3.402823466e38f);
 }
 
 struct Bf16 {
@@ -105,30 +110,15 @@ __device__ __forceinline__ float fmerge(float m, float s, float m2, float s2, fl
   return s * __builtin_amdgcn_exp2f((m - z) * c) + s2 * __builtin_amdgcn_exp2f((m2 - z) * c);
 }
 
-// One part of one row: largest logit, its lowest index, sum of exponentials.  Memory-bound.
-template <typename T>
-__global__ __launch_bounds__(kStatThreads) void verify_stats_kernel(VerifyArgs a) {
-  const int part = (int)(blockIdx.x % a.parts);
-  const int64_t rowid = blockIdx.x / a.parts;  // slot-major
-  const int slot = (int)(rowid / a.B), b = (int)(rowid % a.B);
-  if (slot > clamp_valid(a, b)) return;
-  const char* row = (const char*)a.logits +
-                    ((int64_t)b * a.batch_stride + slot * a.slot_stride) * T::kBytes;
-  const float temp = temperature(a, b);
-  const bool greedy = !(temp > 0.f);
-  const float c = greedy ? 1.f : inv_log2(temp);
-  const int j0 = part * a.part_size;
-  const int j1 = a.V - j0 < a.part_size ? a.V : j0 + a.part_size;
+// Largest logit, its lowest index and the sum of exponentials of logits [j0, j1) of a row, by a
+// workgroup of N threads; the result is thread 0's.  Four 16-byte loads a thread are in flight.
+template <typename T, int N>
+__device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, float c) {
+  __shared__ VerifyPart w[N / 64];
+  constexpr int kBatch = 4;
   float m = -__builtin_inff(), s = 0.f;
   int at = 0x7fffffff;
-  for (int j = j0 + (int)threadIdx.x * 8; j < j1; j += kStatThreads * 8) {
-    float x[8];
-    if (j + 8 <= j1) {
-      T::get8(row, j, x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = j + e < j1 ? T::get(row, j + e) : -__builtin_inff();
-    }
+  auto take = [&](const float (&x)[8], int j) {
     float t = x[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) t = fmaxf(t, x[e]);
@@ -144,6 +134,24 @@ __global__ __launch_bounds__(kStatThreads) void verify_stats_kernel(VerifyArgs a
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((x[e] - z) * c);
     }
+  };
+  int j = j0 + (int)threadIdx.x * 8;
+  for (; j + (kBatch - 1) * N * 8 + 8 <= j1; j += kBatch * N * 8) {
+    float x[kBatch][8];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) T::get8(row, j + k * N * 8, x[k]);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) take(x[k], j + k * N * 8);
+  }
+  for (; j < j1; j += N * 8) {
+    float x[8];
+    if (j + 8 <= j1) {
+      T::get8(row, j, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = j + e < j1 ? T::get(row, j + e) : -__builtin_inff();
+    }
+    take(x, j);
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
@@ -154,18 +162,68 @@ __global__ __launch_bounds__(kStatThreads) void verify_stats_kernel(VerifyArgs a
     at = m2 > m || (m2 == m && at2 < at) ? at2 : at;
     m = mm;
   }
-  __shared__ VerifyPart w[kStatThreads / 64];
   if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = VerifyPart{m, s, at, 0};
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kStatThreads / 64; ++i) {
+  if (threadIdx.x == 0)
+    for (int i = 1; i < N / 64; ++i) {
       const float mm = fmaxf(m, w[i].m);
       s = fmerge(m, s, w[i].m, w[i].s, c, mm);
       at = w[i].m > m || (w[i].m == m && w[i].at < at) ? w[i].at : at;
       m = mm;
     }
-    a.part[((int64_t)b * (a.k + 1) + slot) * a.parts + part] = VerifyPart{m, s, at, 0};
-  }
+  return VerifyPart{m, s, at, 0};
+}
+
+__device__ __forceinline__ const char* row_ptr(const VerifyArgs& a, int b, int slot, int bytes) {
+  return (const char*)a.logits + ((int64_t)b * a.batch_stride + slot * a.slot_stride) * bytes;
+}
+
+// ---------------------------------------------------------------- fp64 weights
+// exp by a table of 2^(i/32) and a polynomial over 1/32 of an octave, |z| <= ln 2 / 64:
+//   2^(n/32 + f/32) = 2^(n div 32) T[n mod 32] (1 + z + ... + z^5 / 120),  z = f ln 2 / 32,
+// within 2^-48 of the function; about half the instructions of a full-precision exp, and the
+// search for the drawn token is bounded by them.
+constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer
+constexpr double kZ = 0.69314718055994530942 / 32;
+
+struct Weights64 {
+  const double* table;  // 32 entries in LDS
+  double k;             // 32 log2(e) / T
+  double m;
+  float lo;             // logits below it weigh nothing (under e^-700)
+};
+
+__device__ __forceinline__ void fill_table(double* table) {
+  if (threadIdx.x < 32) table[threadIdx.x] = exp2((double)threadIdx.x / 32.0);
+}
+
+__device__ __forceinline__ Weights64 weights64(const double* table, float m, float temp,
+                                               bool greedy) {
+  const double inv = greedy ? 1.0 : inv64(temp);
+  const double lo = fmax((double)m - 700.0 / inv, -3.402823466e38);
+  float f = (float)lo;
+  if ((double)f < lo) f = nextafterf(f, 3.402823466e38f);  // up: exponents stay within fp64's
+  return Weights64{table, inv * (32 * 1.4426950408889634074), (double)m, f};
+}
+
+__device__ __forceinline__ double weight64(const Weights64& w, float x) {
+  const double d = (double)fmaxf(x, w.lo) - w.m;
+  const double t = fma(d, w.k, kMagic);
+  const int n = (int)__double_as_longlong(t);  // low word: the integer
+  const double f = fma(d, w.k, -(t - kMagic));
+  double p = fma(f, kZ * kZ * kZ * kZ * kZ / 120, kZ * kZ * kZ * kZ / 24);
+  p = fma(f, p, kZ * kZ * kZ / 6);
+  p = fma(f, p, kZ * kZ / 2);
+  p = fma(f, p, kZ);
+  p *= f;
+  const double s = w.table[n & 31];
+  const double ts = __hiloint2double(__double2hiint(s) + ((n >> 5) << 20), __double2loint(s));
+  return x >= w.lo ? fma(ts, p, ts) : 0.0;
+}
+
+// The same to the last weight above 0 that fp64 has: for draws at the very start of a row.
+__device__ __forceinline__ double weight64_full(float x, float m, double inv) {
+  return exp(((double)x - (double)m) * inv);
 }
 
 __device__ __forceinline__ double wave_sum64(double x) {
@@ -174,16 +232,22 @@ __device__ __forceinline__ double wave_sum64(double x) {
   return x;
 }
 
-__device__ __forceinline__ double weight64(float x, float m, double inv) {
-  return exp(((double)x - (double)m) * inv);
-}
-
-// Sum of the weights of [j0, j1), one wavefront, `skip` left out.
+// Sum of the weights of [j0, j1) but `skip`, one wavefront.
 template <typename T>
-__device__ double wave_range64(const char* row, int j0, int j1, float m, double inv, int skip,
+__device__ double wave_range64(const char* row, int j0, int j1, const Weights64& w, int skip,
                                int lane) {
   double s = 0.0;
-  for (int j = j0 + lane * 8; j < j1; j += 512) {
+  int j = j0 + lane * 8;
+  for (; j + 520 <= j1; j += 1024) {  // two loads at a time
+    float x[2][8];
+    T::get8(row, j, x[0]);
+    T::get8(row, j + 512, x[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += weight64(w, x[k][e]);
+  }
+  for (; j < j1; j += 512) {
     float x[8];
     if (j + 8 <= j1) {
       T::get8(row, j, x);
@@ -192,180 +256,326 @@ __device__ double wave_range64(const char* row, int j0, int j1, float m, double 
       for (int e = 0; e < 8; ++e) x[e] = j + e < j1 ? T::get(row, j + e) : -__builtin_inff();
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += j + e == skip ? 0.0 : weight64(x[e], m, inv);
+    for (int e = 0; e < 8; ++e) s += weight64(w, x[e]);
   }
-  return wave_sum64(s);
+  s = wave_sum64(s);
+  // the weight left out is subtracted as it was added, unless it is most of the sum
+  if (skip >= j0 && skip < j1) {
+    const double d = weight64(w, T::get(row, skip));
+    if (d < 0.5 * s) return s - d;
+    s = 0.0;
+    for (int i = j0 + lane; i < j1; i += 64)
+      if (i != skip) s += weight64(w, T::get(row, i));
+    s = wave_sum64(s);
+  }
+  return s;
 }
 
-// Segment w of [j0, j1) in kPickWaves equal ones.
-__device__ __forceinline__ int seg_at(int j0, int j1, int w) {
-  const int len = (j1 - j0 + kPickWaves - 1) / kPickWaves;
+// Segment w of [j0, j1) in `of` equal ones.
+__device__ __forceinline__ int seg_at(int j0, int j1, int w, int of) {
+  const int len = (j1 - j0 + of - 1) / of;
   const int64_t j = (int64_t)j0 + (int64_t)len * w;
   return j < j1 ? (int)j : j1;
 }
 
-// One workgroup per request: the tests in order, then the draw from the row they end at.
+// ---------------------------------------------------------------- tests
+enum { kReject = 0, kAccept = 1, kClose = 2 };
+
+// The test of slot `slot` from its row's fp32 statistics.
 template <typename T>
-__global__ __launch_bounds__(kPickThreads) void verify_pick_kernel(VerifyArgs a) {
-  __shared__ float row_m[kMaxRows];
-  __shared__ int row_at[kMaxRows], verdict[kMaxRows];
-  __shared__ double seg[kPickWaves];
-  __shared__ int token;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int nv = clamp_valid(a, b);
+__device__ int test_slot(const VerifyArgs& a, int b, int slot, const VerifyPart& p, bool greedy,
+                         float c) {
+  if (!(p.m > -__builtin_inff())) return kReject;
+  const int d = a.draft[(int64_t)b * a.k + slot];
+  if (d < 0 || d >= a.V) return kReject;
+  if (greedy) return p.at == d ? kAccept : kReject;
+  const float w =
+      __builtin_amdgcn_exp2f((T::get(row_ptr(a, b, slot, T::kBytes), d) - p.m) * c);
+  const float uz = a.u_accept[(int64_t)b * a.k + slot] * p.s;
+  // Either side's fp32 error is below 2^-15 of it (an exponent of up to 126 octaves, rounded
+  // twice, is off by 2^-16.4 of the weight) or below 2^-60 where a weight underflows.
+  if (fabsf(uz - w) <= (uz + w) * 0x1p-14f + 0x1p-60f) return kClose;
+  return uz < w ? kAccept : kReject;
+}
+
+// The same in fp64, by a whole workgroup of kRowThreads; seg: kRowWaves doubles of LDS.
+template <typename T>
+__device__ bool test_close(const VerifyArgs& a, int b, int slot, const Weights64& w, float m,
+                           double inv, double* seg) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const char* row = row_ptr(a, b, slot, T::kBytes);
+  const double s = wave_range64<T>(row, seg_at(0, a.V, wave, kRowWaves),
+                                   seg_at(0, a.V, wave + 1, kRowWaves), w, -1, lane);
+  __syncthreads();
+  if (lane == 0) seg[wave] = s;
+  __syncthreads();
+  double z = 0.0;
+  for (int i = 0; i < kRowWaves; ++i) z += seg[i];
+  const int d = a.draft[(int64_t)b * a.k + slot];
+  return (double)a.u_accept[(int64_t)b * a.k + slot] * z < weight64_full(T::get(row, d), m, inv);
+}
+
+// ---------------------------------------------------------------- kernels
+// Small calls: one part of one row.
+template <typename T>
+__global__ __launch_bounds__(kPartThreads) void verify_part_kernel(VerifyArgs a) {
+  const int part = (int)(blockIdx.x % a.parts);
+  const int64_t rowid = blockIdx.x / a.parts;
+  const int slot = (int)(rowid / a.B), b = (int)(rowid % a.B);
+  if (slot > clamp_valid(a, b)) return;
+  const float temp = temperature(a, b);
+  const bool greedy = !(temp > 0.f);
+  const int j0 = part * a.part_size;
+  const int j1 = a.V - j0 < a.part_size ? a.V : j0 + a.part_size;
+  const VerifyPart p = row_stats<T, kPartThreads>(row_ptr(a, b, slot, T::kBytes), j0, j1, greedy,
+                                                  greedy ? 1.f : inv_log2(temp));
+  if (threadIdx.x == 0) a.part[((int64_t)b * (a.k + 1) + slot) * a.parts + part] = p;
+}
+
+__global__ void verify_begin_kernel(VerifyArgs a) {
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b < a.B) a.stop[b] = clamp_valid(a, b);
+}
+
+// Large calls: one row, its test included; stop[b] is the lowest slot known to be rejected.
+template <typename T>
+__global__ __launch_bounds__(kRowThreads) void verify_row_kernel(VerifyArgs a) {
+  __shared__ VerifyPart whole;
+  __shared__ int verdict;
+  __shared__ double seg[kRowWaves], table[32];
+  const int slot = (int)(blockIdx.x / a.B), b = (int)(blockIdx.x % a.B);
+  if (slot > __hip_atomic_load(&a.stop[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) return;
   const float temp = temperature(a, b);
   const bool greedy = !(temp > 0.f);
   const float c = greedy ? 1.f : inv_log2(temp);
-  const double inv = greedy ? 1.0 : inv64(temp);
-  const char* rows = (const char*)a.logits + (int64_t)b * a.batch_stride * T::kBytes;
-  auto row_of = [&](int i) { return rows + i * a.slot_stride * T::kBytes; };
+  const VerifyPart p =
+      row_stats<T, kRowThreads>(row_ptr(a, b, slot, T::kBytes), 0, a.V, greedy, c);
+  const bool last = slot >= clamp_valid(a, b);
+  if (threadIdx.x == 0) {
+    a.part[(int64_t)b * (a.k + 1) + slot] = p;
+    whole = p;
+    verdict = last ? kAccept : test_slot<T>(a, b, slot, p, greedy, c);
+  }
+  __syncthreads();
+  if (verdict == kClose) {
+    fill_table(table);
+    __syncthreads();
+    const bool ok = test_close<T>(a, b, slot, weights64(table, whole.m, temp, greedy), whole.m,
+                                  inv64(temp), seg);
+    __syncthreads();
+    if (threadIdx.x == 0) verdict = ok ? kAccept : kReject;
+  }
+  if (threadIdx.x == 0 && verdict == kReject) atomicMin(&a.stop[b], slot);
+}
+
+// What a request's draw starts from: the number accepted and the row's statistics.
+struct Drawn {
+  int n;
+  float m;
+  int at;
+};
+
+template <typename T>
+__device__ Drawn accepted(const VerifyArgs& a, int b, float temp, bool greedy, double* seg,
+                          const double* table) {
+  if (a.stop) {
+    const int n = a.stop[b];
+    const VerifyPart p = a.part[(int64_t)b * (a.k + 1) + n];
+    return Drawn{n, p.m, p.at};
+  }
+  __shared__ float row_m[kMaxRows];
+  __shared__ int row_at[kMaxRows], verdict[kMaxRows];
+  const int nv = clamp_valid(a, b), tid = threadIdx.x;
+  const float c = greedy ? 1.f : inv_log2(temp);
   if (tid <= nv) {
     const VerifyPart* p = a.part + ((int64_t)b * (a.k + 1) + tid) * a.parts;
-    float m = p[0].m;
-    int at = p[0].at;
+    VerifyPart r = p[0];
     for (int i = 1; i < a.parts; ++i)
-      if (p[i].m > m) {
-        m = p[i].m;
-        at = p[i].at;
+      if (p[i].m > r.m) {
+        r.m = p[i].m;
+        r.at = p[i].at;
       }
-    row_m[tid] = m;
-    row_at[tid] = at;
-    int v = 0;
-    if (tid < nv && m > -__builtin_inff()) {
-      const int d = a.draft[(int64_t)b * a.k + tid];
-      if (d >= 0 && d < a.V) {
-        if (greedy) {
-          v = at == d;
-        } else {
-          float z = 0.f;
-          for (int i = 0; i < a.parts; ++i)
-            z += p[i].s * __builtin_amdgcn_exp2f((p[i].m - m) * c);
-          const float w = __builtin_amdgcn_exp2f((T::get(row_of(tid), d) - m) * c);
-          const float uz = a.u_accept[(int64_t)b * a.k + tid] * z;
-          // the fp32 sides are off by less than 2^-16 of themselves where w is not tiny
-          v = fabsf(uz - w) <= (uz + w) * 0x1p-14f + 0x1p-60f ? 2 : (uz < w ? 1 : 0);
-        }
-      }
-    }
-    verdict[tid] = v;
+    r.s = 0.f;
+    if (r.m > -__builtin_inff())
+      for (int i = 0; i < a.parts; ++i)
+        r.s += p[i].s * __builtin_amdgcn_exp2f((p[i].m - r.m) * c);
+    row_m[tid] = r.m;
+    row_at[tid] = r.at;
+    verdict[tid] = tid < nv ? test_slot<T>(a, b, tid, r, greedy, c) : kReject;
   }
   __syncthreads();
   int n = 0;
   for (; n < nv; ++n) {
-    int v = verdict[n];
-    if (v == 2) {
-      const double s = wave_range64<T>(row_of(n), seg_at(0, a.V, wave), seg_at(0, a.V, wave + 1),
-                                       row_m[n], inv, -1, lane);
-      if (lane == 0) seg[wave] = s;
-      __syncthreads();
-      double z = 0.0;
-      for (int w = 0; w < kPickWaves; ++w) z += seg[w];
-      __syncthreads();
-      const int d = a.draft[(int64_t)b * a.k + n];
-      v = (double)a.u_accept[(int64_t)b * a.k + n] * z <
-          weight64(T::get(row_of(n), d), row_m[n], inv);
-    }
-    if (!v) break;
+    bool ok = verdict[n] == kAccept;
+    if (verdict[n] == kClose)
+      ok = test_close<T>(a, b, n, weights64(table, row_m[n], temp, greedy), row_m[n],
+                         inv64(temp), seg);
+    if (!ok) break;
   }
+  return Drawn{n, row_m[n], row_at[n]};
+}
+
+// One workgroup per request: the tests in order (small calls), then the draw from the row they
+// end at.  The row is summed in segments, the segment that holds the draw in turn, until 1024
+// logits are left, which are scanned one a thread.
+template <typename T>
+__global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) {
+  __shared__ double seg[kRowWaves], table[32];
+  __shared__ int found;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const float temp = temperature(a, b);
+  const bool greedy = !(temp > 0.f);
+  fill_table(table);
+  __syncthreads();
+  const Drawn r = accepted<T>(a, b, temp, greedy, seg, table);
   int pick = -1;
-  if (row_m[n] > -__builtin_inff()) {
-    pick = row_at[n];
+  if (r.m > -__builtin_inff()) {
+    pick = r.at;
     if (!greedy) {
-      const int d = n < nv ? a.draft[(int64_t)b * a.k + n] : -1;
-      const char* row = row_of(n);
-      const float m = row_m[n];
+      const int d = r.n < clamp_valid(a, b) ? a.draft[(int64_t)b * a.k + r.n] : -1;
+      const char* row = row_ptr(a, b, r.n, T::kBytes);
+      const Weights64 w = weights64(table, r.m, temp, false);
+      const double inv = inv64(temp);
       int j0 = 0, j1 = a.V;
       double base = 0.0, t = 0.0;
       bool none = false;
-      for (int level = 0; level < 2; ++level) {
-        const double s = wave_range64<T>(row, seg_at(j0, j1, wave), seg_at(j0, j1, wave + 1), m,
-                                         inv, d, lane);
+      while (j1 - j0 > kRowThreads) {
+        const double s = wave_range64<T>(row, seg_at(j0, j1, wave, kRowWaves),
+                                         seg_at(j0, j1, wave + 1, kRowWaves), w, d, lane);
+        __syncthreads();
         if (lane == 0) seg[wave] = s;
         __syncthreads();
-        if (level == 0) {
+        if (j0 == 0 && j1 == a.V) {
           double z = 0.0;
-          for (int w = 0; w < kPickWaves; ++w) z += seg[w];
+          for (int i = 0; i < kRowWaves; ++i) z += seg[i];
           t = (double)a.u_sample[b] * z;
-          none = !(z > 0.0);  // the rejected draft was all there was
+          none = !(z > 0.0);
         }
         // the segment whose sums pass t; the last that holds anything if rounding hides it
-        int at = -1;
+        int at = 0;
         double before = base, run = base;
-        for (int w = 0; w < kPickWaves; ++w) {
-          if (seg[w] > 0.0) {
-            at = w;
+        for (int i = 0; i < kRowWaves; ++i)
+          if (seg[i] > 0.0) {
+            at = i;
             before = run;
-            run += seg[w];
+            run += seg[i];
             if (run > t) break;
           }
-        }
-        __syncthreads();
-        if (at < 0) at = 0;
         base = before;
-        const int s0 = seg_at(j0, j1, at), s1 = seg_at(j0, j1, at + 1);
+        const int s0 = seg_at(j0, j1, at, kRowWaves), s1 = seg_at(j0, j1, at + 1, kRowWaves);
         j0 = s0;
         j1 = s1;
       }
-      if (none) {
-        pick = row_at[n];
-      } else {
+      const bool whole = j0 == 0 && j1 == a.V;
+      // one logit a thread: running sums of the wavefront, then of those before it
+      const int j = j0 + tid;
+      double x = 0.0;
+      if (j < j1 && j != d)
+        x = whole ? weight64_full(T::get(row, j), r.m, inv) : weight64(w, T::get(row, j));
+      double inc = x;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const double y = __shfl_up(inc, o);
+        if (lane >= o) inc += y;
+      }
+      __syncthreads();
+      if (lane == 63) seg[wave] = inc;
+      if (tid == 0) found = 0x7fffffff;
+      __syncthreads();
+      double before = base, z = 0.0;
+      for (int i = 0; i < kRowWaves; ++i) {
+        if (i < wave) before += seg[i];
+        z += seg[i];
+      }
+      if (whole) {
+        t = (double)a.u_sample[b] * z;
+        none = !(z > 0.0);
+      }
+      const unsigned long long hit = __ballot(x > 0.0 && before + inc > t);
+      if (hit && lane == 0) atomicMin(&found, j + __ffsll((long long)hit) - 1);
+      __syncthreads();
+      if (found == 0x7fffffff) {  // rounding hid it: the last that weighs anything
+        const unsigned long long some = __ballot(x > 0.0);
+        __syncthreads();
+        if (tid == 0) found = -1;
+        __syncthreads();
+        if (some && lane == 0) atomicMax(&found, j + 63 - __clzll(some));
+        __syncthreads();
+      }
+      if (!none) pick = found;
+      if (!whole && t < 0x1p-900 && !none) {
+        // A draw this close to 0 can land on weights that the fast ones leave out.
         if (wave == 0) {
-          int found = -1;
-          for (int j = j0; j < j1; j += 64) {
-            double w = 0.0;
-            if (j + lane < j1 && j + lane != d) w = weight64(T::get(row, j + lane), m, inv);
-            double inc = w;
+          double run = 0.0;
+          int last = -1;
+          for (int i = 0; i < a.V; i += 64) {
+            double y = 0.0;
+            if (i + lane < a.V && i + lane != d)
+              y = weight64_full(T::get(row, i + lane), r.m, inv);
+            double sum = y;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
-              const double y = __shfl_up(inc, o);
-              if (lane >= o) inc += y;
+              const double v = __shfl_up(sum, o);
+              if (lane >= o) sum += v;
             }
-            const unsigned long long some = __ballot(w > 0.0);
-            const unsigned long long hit = __ballot(w > 0.0 && base + inc > t);
-            if (some) found = j + 63 - __clzll(some);
-            if (hit) {
-              found = j + __ffsll((long long)hit) - 1;
+            const unsigned long long h = __ballot(y > 0.0 && run + sum > t);
+            if (h) {
+              last = i + __ffsll((long long)h) - 1;
               break;
             }
-            base += __shfl(inc, 63);
+            run += __shfl(sum, 63);
           }
-          if (lane == 0) token = found;
+          if (lane == 0) found = last;
         }
         __syncthreads();
-        pick = token;
+        pick = found;
       }
     }
   }
   if (tid <= a.k)
     a.sampled[(int64_t)b * (a.k + 1) + tid] =
-        tid < n ? a.draft[(int64_t)b * a.k + tid] : (tid == n ? pick : -1);
-  if (tid == 0) a.num_accepted[b] = n;
+        tid < r.n ? a.draft[(int64_t)b * a.k + tid] : (tid == r.n ? pick : -1);
+  if (tid == 0) a.num_accepted[b] = r.n;
 }
 
 template <typename T>
 hipError_t launch_type(const VerifyArgs& a, hipStream_t st) {
-  const int64_t groups = (int64_t)a.B * (a.k + 1) * a.parts;
-  hipLaunchKernelGGL(verify_stats_kernel<T>, dim3((unsigned)groups), dim3(kStatThreads), 0, st, a);
+  const int64_t rows = (int64_t)a.B * (a.k + 1);
+  if (a.stop) {
+    hipLaunchKernelGGL(verify_begin_kernel, dim3((unsigned)((a.B + 255) / 256)), dim3(256), 0, st,
+                       a);
+    hipLaunchKernelGGL(verify_row_kernel<T>, dim3((unsigned)rows), dim3(kRowThreads), 0, st, a);
+  } else {
+    hipLaunchKernelGGL(verify_part_kernel<T>, dim3((unsigned)(rows * a.parts)),
+                       dim3(kPartThreads), 0, st, a);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(verify_pick_kernel<T>, dim3((unsigned)a.B), dim3(kPickThreads), 0, st, a);
+  hipLaunchKernelGGL(verify_draw_kernel<T>, dim3((unsigned)a.B), dim3(kRowThreads), 0, st, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t verify_plan(VerifyArgs* a) {
-  // parts of at least 16K logits, enough of them to fill 256 CUs four times over
   const int64_t rows = (int64_t)a->B * (a->k + 1);
+  a->in_order = rows >= 512 && a->V >= 16384;
+  // else parts of at least 16K logits, enough of them to fill 256 CUs four times over
   int64_t parts = rows > 0 ? (1024 + rows - 1) / rows : 1;
   const int64_t most = ((int64_t)a->V + 16383) / 16384;
   parts = parts > most ? most : parts;
-  parts = parts < 1 ? 1 : parts;
+  parts = parts < 1 || a->in_order ? 1 : parts;
   const int64_t size = (a->V + parts - 1) / parts;
   a->part_size = (int32_t)((size + 7) / 8 * 8);
   a->parts = (int32_t)((a->V + a->part_size - 1) / a->part_size);
   if (a->parts < 1) a->parts = 1;
-  return (size_t)rows * a->parts * sizeof(VerifyPart);
+  return (size_t)rows * a->parts * sizeof(VerifyPart) +
+         (a->in_order ? (size_t)a->B * sizeof(int32_t) : 0);
+}
+
+void verify_place(VerifyArgs* a, void* workspace) {
+  a->part = (VerifyPart*)workspace;
+  a->stop = a->in_order ? (int32_t*)(a->part + (size_t)a->B * (a->k + 1) * a->parts) : nullptr;
 }
 
 hipError_t launch_verify(const VerifyArgs& a, KvType type, hipStream_t st) {
