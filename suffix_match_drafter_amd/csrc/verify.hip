@@ -15,10 +15,10 @@
 // test whose two sides are within the fp32 pass's error bound is redone in fp64, and the row that
 // is drawn from is summed and searched in fp64.
 //
-// Work.  Rows past the first rejection decide nothing.  Large calls take one workgroup per row in
-// slot order: a row of a request that is known to have been rejected earlier is not read (the
-// dispatch order makes the look-ahead about one slot of the batch).  Small calls, which do not
-// fill the card with whole rows, read all rows in parts at once.
+// Work.  Rows past the first rejection decide nothing.  Large calls take the first slot of every
+// request, then the other slots in order with one workgroup per CU, and leave out rows of requests
+// that are known by then to have been rejected earlier.  Small calls, which do not fill the card
+// with whole rows, read all rows in parts at once.
 #include "verify.h"
 
 #include <hip/hip_bf16.h>
@@ -49,47 +49,113 @@ __device__ __forceinline__ float clean(float x) {
   return fminf(fmaxf(x, -__builtin_inff()), 3.402823466e38f);
 }
 
+// One logit, and eight as they lie in memory (any alignment of their type) and as floats.
 struct Bf16 {
   static constexpr int kBytes = 2;
+  struct Raw {
+    u32x4 w;
+  };
   static __device__ float get(const void* p, int64_t i) {
-    return clean(__uint_as_float((unsigned)((const unsigned short*)p)[i] << 16));
+    return __uint_as_float((unsigned)((const unsigned short*)p)[i] << 16);
   }
-  static __device__ void get8(const void* p, int64_t i, float (&x)[8]) {
-    const u32x4 w = *(const u32x4_a2*)((const unsigned short*)p + i);
+  static __device__ Raw raw8(const void* p, int64_t i) {
+    return Raw{*(const u32x4_a2*)((const unsigned short*)p + i)};
+  }
+  static __device__ void floats(const Raw& r, float (&x)[8]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[2 * e] = clean(__uint_as_float(w[e] << 16));
-      x[2 * e + 1] = clean(__uint_as_float(w[e] & 0xffff0000u));
+      x[2 * e] = __uint_as_float(r.w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(r.w[e] & 0xffff0000u);
     }
   }
 };
 struct Fp16 {
   static constexpr int kBytes = 2;
+  struct Raw {
+    u32x4 w;
+  };
   static __device__ float get(const void* p, int64_t i) {
-    return clean(from_half(((const unsigned short*)p)[i]));
+    return from_half(((const unsigned short*)p)[i]);
   }
-  static __device__ void get8(const void* p, int64_t i, float (&x)[8]) {
-    const u32x4 w = *(const u32x4_a2*)((const unsigned short*)p + i);
+  static __device__ Raw raw8(const void* p, int64_t i) {
+    return Raw{*(const u32x4_a2*)((const unsigned short*)p + i)};
+  }
+  static __device__ void floats(const Raw& r, float (&x)[8]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[2 * e] = clean(from_half((unsigned short)w[e]));
-      x[2 * e + 1] = clean(from_half((unsigned short)(w[e] >> 16)));
+      x[2 * e] = from_half((unsigned short)r.w[e]);
+      x[2 * e + 1] = from_half((unsigned short)(r.w[e] >> 16));
     }
   }
 };
 struct Fp32 {
   static constexpr int kBytes = 4;
-  static __device__ float get(const void* p, int64_t i) { return clean(((const float*)p)[i]); }
-  static __device__ void get8(const void* p, int64_t i, float (&x)[8]) {
-    const u32x4 w = *(const u32x4_a4*)((const float*)p + i);
-    const u32x4 v = *(const u32x4_a4*)((const float*)p + i + 4);
+  struct Raw {
+    u32x4 w, v;
+  };
+  static __device__ float get(const void* p, int64_t i) { return ((const float*)p)[i]; }
+  static __device__ Raw raw8(const void* p, int64_t i) {
+    return Raw{*(const u32x4_a4*)((const float*)p + i),
+               *(const u32x4_a4*)((const float*)p + i + 4)};
+  }
+  static __device__ void floats(const Raw& r, float (&x)[8]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[e] = clean(__uint_as_float(w[e]));
-      x[4 + e] = clean(__uint_as_float(v[e]));
+      x[e] = __uint_as_float(r.w[e]);
+      x[4 + e] = __uint_as_float(r.v[e]);
     }
   }
 };
+
+template <typename T>
+__device__ __forceinline__ float logit(const void* row, int64_t j) {
+  return clean(T::get(row, j));
+}
+
+// Calls f(eight logits, index of the first) for j, j + step, ... below j1; missing ones are -inf.
+// Loads run a batch ahead of the work on them, in two sets of registers that take turns (a copy
+// from one to the other would wait for the loads).
+template <typename T, int kBatch, typename F>
+__device__ __forceinline__ void each8(const char* row, int j, int j1, int step, F&& f) {
+  const int batch = kBatch * step, reach = (kBatch - 1) * step + 8;
+  float x[8];
+  if (j + reach <= j1) {
+    typename T::Raw a[kBatch], b[kBatch];
+    auto load = [&](typename T::Raw (&r)[kBatch], int at) {
+      // past the end: any place inside, not used
+      const int from = at + reach <= j1 ? at : j;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) r[k] = T::raw8(row, from + k * step);
+    };
+    auto work = [&](const typename T::Raw (&r)[kBatch], int at) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        T::floats(r[k], x);
+        f(x, at + k * step);
+      }
+    };
+    load(a, j);
+    for (;;) {
+      load(b, j + batch);
+      work(a, j);
+      j += batch;
+      if (j + reach > j1) break;
+      load(a, j + batch);
+      work(b, j);
+      j += batch;
+      if (j + reach > j1) break;
+    }
+  }
+  for (; j < j1; j += step) {
+    if (j + 8 <= j1) {
+      T::floats(T::raw8(row, j), x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = j + e < j1 ? T::get(row, j + e) : -__builtin_inff();
+    }
+    f(x, j);
+  }
+}
 
 __device__ __forceinline__ int clamp_valid(const VerifyArgs& a, int b) {
   const int nv = a.num_valid ? a.num_valid[b] : a.k;
@@ -111,14 +177,17 @@ __device__ __forceinline__ float fmerge(float m, float s, float m2, float s2, fl
 }
 
 // Largest logit, its lowest index and the sum of exponentials of logits [j0, j1) of a row, by a
-// workgroup of N threads; the result is thread 0's.  Four 16-byte loads a thread are in flight.
-template <typename T, int N>
-__device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, float c) {
-  __shared__ VerifyPart w[N / 64];
-  constexpr int kBatch = 4;
+// workgroup of N threads; the result is every thread's.  Taken as they come, a NaN or +inf makes
+// the sum a NaN; then, and only then, they are cleaned and summed again.
+template <typename T, int N, bool kClean>
+__device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, float c,
+                                VerifyPart* w) {
   float m = -__builtin_inff(), s = 0.f;
   int at = 0x7fffffff;
-  auto take = [&](const float (&x)[8], int j) {
+  each8<T, 4>(row, j0 + (int)threadIdx.x * 8, j1, N * 8, [&](float (&x)[8], int j) {
+    if (kClean)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = clean(x[e]);
     float t = x[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) t = fmaxf(t, x[e]);
@@ -132,27 +201,10 @@ __device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, fl
     if (!greedy) {
       const float z = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((x[e] - z) * c);
+      for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f((x[e] - z) * c);
+      s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
     }
-  };
-  int j = j0 + (int)threadIdx.x * 8;
-  for (; j + (kBatch - 1) * N * 8 + 8 <= j1; j += kBatch * N * 8) {
-    float x[kBatch][8];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) T::get8(row, j + k * N * 8, x[k]);
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) take(x[k], j + k * N * 8);
-  }
-  for (; j < j1; j += N * 8) {
-    float x[8];
-    if (j + 8 <= j1) {
-      T::get8(row, j, x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = j + e < j1 ? T::get(row, j + e) : -__builtin_inff();
-    }
-    take(x, j);
-  }
+  });
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
     const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
@@ -162,16 +214,27 @@ __device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, fl
     at = m2 > m || (m2 == m && at2 < at) ? at2 : at;
     m = mm;
   }
+  __syncthreads();
   if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = VerifyPart{m, s, at, 0};
   __syncthreads();
-  if (threadIdx.x == 0)
-    for (int i = 1; i < N / 64; ++i) {
-      const float mm = fmaxf(m, w[i].m);
-      s = fmerge(m, s, w[i].m, w[i].s, c, mm);
-      at = w[i].m > m || (w[i].m == m && w[i].at < at) ? w[i].at : at;
-      m = mm;
-    }
-  return VerifyPart{m, s, at, 0};
+  VerifyPart r = w[0];
+  for (int i = 1; i < N / 64; ++i) {
+    const VerifyPart p = w[i];
+    const float mm = fmaxf(r.m, p.m);
+    r.s = fmerge(r.m, r.s, p.m, p.s, c, mm);
+    r.at = p.m > r.m || (p.m == r.m && p.at < r.at) ? p.at : r.at;
+    r.m = mm;
+  }
+  return r;
+}
+
+template <typename T, int N>
+__device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, float c) {
+  __shared__ VerifyPart w[N / 64];
+  VerifyPart r = row_stats<T, N, false>(row, j0, j1, greedy, c, w);
+  if (!(r.s < __builtin_inff()) || r.m == __builtin_inff())
+    r = row_stats<T, N, true>(row, j0, j1, greedy, c, w);
+  return r;
 }
 
 __device__ __forceinline__ const char* row_ptr(const VerifyArgs& a, int b, int slot, int bytes) {
@@ -179,22 +242,27 @@ __device__ __forceinline__ const char* row_ptr(const VerifyArgs& a, int b, int s
 }
 
 // ---------------------------------------------------------------- fp64 weights
-// exp by a table of 2^(i/32) and a polynomial over 1/32 of an octave, |z| <= ln 2 / 64:
-//   2^(n/32 + f/32) = 2^(n div 32) T[n mod 32] (1 + z + ... + z^5 / 120),  z = f ln 2 / 32,
-// within 2^-48 of the function; about half the instructions of a full-precision exp, and the
-// search for the drawn token is bounded by them.
+// exp by a table of 2^(i/256) and a polynomial over 1/256 of an octave, |z| <= ln 2 / 512:
+//   2^(n/256 + f/256) = 2^(n div 256) T[n mod 256] (1 + z + z^2/2 + z^3/6),  z = f ln 2 / 256,
+// within 2^-42 of the function.  The search for the drawn token is bounded by these instructions
+// (19 a logit; 27 with 32 entries, two more terms and a select took 49 us a row of 151936, not
+// 36).  Logits more than 700 T below the largest weigh e^-700 here, whatever they are: what they
+// add is far below a draw's resolution unless the draw is below kTiny, which is done again with
+// the exact function.
 constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer
-constexpr double kZ = 0.69314718055994530942 / 32;
+constexpr double kZ = 0.69314718055994530942 / 256;
+constexpr int kTable = 256;
+constexpr double kTiny = 0x1p-900;  // above 2^30 times e^-700
 
 struct Weights64 {
-  const double* table;  // 32 entries in LDS
-  double k;             // 32 log2(e) / T
+  const double* table;  // kTable entries in LDS
+  double k;             // 256 log2(e) / T
   double m;
-  float lo;             // logits below it weigh nothing (under e^-700)
+  float lo;             // m - 700 T
 };
 
 __device__ __forceinline__ void fill_table(double* table) {
-  if (threadIdx.x < 32) table[threadIdx.x] = exp2((double)threadIdx.x / 32.0);
+  if (threadIdx.x < kTable) table[threadIdx.x] = exp2((double)threadIdx.x / kTable);
 }
 
 __device__ __forceinline__ Weights64 weights64(const double* table, float m, float temp,
@@ -203,22 +271,30 @@ __device__ __forceinline__ Weights64 weights64(const double* table, float m, flo
   const double lo = fmax((double)m - 700.0 / inv, -3.402823466e38);
   float f = (float)lo;
   if ((double)f < lo) f = nextafterf(f, 3.402823466e38f);  // up: exponents stay within fp64's
-  return Weights64{table, inv * (32 * 1.4426950408889634074), (double)m, f};
+  return Weights64{table, inv * (kTable * 1.4426950408889634074), (double)m, f};
 }
 
-__device__ __forceinline__ double weight64(const Weights64& w, float x) {
-  const double d = (double)fmaxf(x, w.lo) - w.m;
-  const double t = fma(d, w.k, kMagic);
-  const int n = (int)__double_as_longlong(t);  // low word: the integer
-  const double f = fma(d, w.k, -(t - kMagic));
-  double p = fma(f, kZ * kZ * kZ * kZ * kZ / 120, kZ * kZ * kZ * kZ / 24);
-  p = fma(f, p, kZ * kZ * kZ / 6);
-  p = fma(f, p, kZ * kZ / 2);
-  p = fma(f, p, kZ);
-  p *= f;
-  const double s = w.table[n & 31];
-  const double ts = __hiloint2double(__double2hiint(s) + ((n >> 5) << 20), __double2loint(s));
-  return x >= w.lo ? fma(ts, p, ts) : 0.0;
+// Sum of four weights, stage by stage: each weight is one chain of dependent instructions.  The
+// median takes a NaN and -inf to lo and +inf to the largest float.
+__device__ __forceinline__ double weights4(const Weights64& w, const float* x) {
+  double f[4], p[4], ts[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const double d = (double)__builtin_amdgcn_fmed3f(x[e], w.lo, 3.402823466e38f) - w.m;
+    const double t = fma(d, w.k, kMagic);
+    const int n = (int)__double_as_longlong(t);  // low word: the integer
+    f[e] = fma(d, w.k, -(t - kMagic));
+    const double s = w.table[n & (kTable - 1)];
+    ts[e] = __hiloint2double(__double2hiint(s) + ((n & ~(kTable - 1)) << 12),
+                             __double2loint(s));
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) p[e] = fma(f[e], kZ * kZ * kZ / 6, kZ * kZ / 2);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) p[e] = fma(f[e], p[e], kZ);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) p[e] = fma(ts[e], p[e] * f[e], ts[e]);
+  return (p[0] + p[1]) + (p[2] + p[3]);
 }
 
 // The same to the last weight above 0 that fp64 has: for draws at the very start of a row.
@@ -232,43 +308,20 @@ __device__ __forceinline__ double wave_sum64(double x) {
   return x;
 }
 
-// Sum of the weights of [j0, j1) but `skip`, one wavefront.
+// Sum of the weights of [j0, j1) (as of weights4; `skip` counts as masked), one wavefront.
 template <typename T>
-__device__ double wave_range64(const char* row, int j0, int j1, const Weights64& w, int skip,
+__device__ __forceinline__ double wave_range64(const char* row, int j0, int j1, const Weights64& w, int skip,
                                int lane) {
   double s = 0.0;
-  int j = j0 + lane * 8;
-  for (; j + 520 <= j1; j += 1024) {  // two loads at a time
-    float x[2][8];
-    T::get8(row, j, x[0]);
-    T::get8(row, j + 512, x[1]);
+  each8<T, 4 / T::kBytes>(row, j0 + lane * 8, j1, 512, [&](float (&x)[8], int j) {
+    if ((unsigned)(skip - j) < 8u)
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += weight64(w, x[k][e]);
-  }
-  for (; j < j1; j += 512) {
-    float x[8];
-    if (j + 8 <= j1) {
-      T::get8(row, j, x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = j + e < j1 ? T::get(row, j + e) : -__builtin_inff();
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s += weight64(w, x[e]);
-  }
-  s = wave_sum64(s);
-  // the weight left out is subtracted as it was added, unless it is most of the sum
-  if (skip >= j0 && skip < j1) {
-    const double d = weight64(w, T::get(row, skip));
-    if (d < 0.5 * s) return s - d;
-    s = 0.0;
-    for (int i = j0 + lane; i < j1; i += 64)
-      if (i != skip) s += weight64(w, T::get(row, i));
-    s = wave_sum64(s);
-  }
-  return s;
+      for (int e = 0; e < 8; ++e)
+        if (j + e == skip) x[e] = -__builtin_inff();
+    s += weights4(w, x);
+    s += weights4(w, x + 4);
+  });
+  return wave_sum64(s);
 }
 
 // Segment w of [j0, j1) in `of` equal ones.
@@ -281,20 +334,25 @@ __device__ __forceinline__ int seg_at(int j0, int j1, int w, int of) {
 // ---------------------------------------------------------------- tests
 enum { kReject = 0, kAccept = 1, kClose = 2 };
 
-// The test of slot `slot` from its row's fp32 statistics.
+// The test of slot `slot` from its row's fp32 statistics; `groups`: groups of eight logits that
+// one thread of the pass added up in turn.
+//
+// Errors, in units of 2^-23: an exponent x is rounded three times, 1.04 |x| of its weight, and
+// the function's own 1; over a sum that averages to at most 1.04 log2 V (31).  Each group may add
+// a rounding and, when the maximum moved, a rescaling (3).  The joins of threads and parts fit the
+// rest of 64.  Weights below 2^-126 are lost: under 2^-60 of any sum.
 template <typename T>
 __device__ int test_slot(const VerifyArgs& a, int b, int slot, const VerifyPart& p, bool greedy,
-                         float c) {
+                         float c, int groups) {
   if (!(p.m > -__builtin_inff())) return kReject;
   const int d = a.draft[(int64_t)b * a.k + slot];
   if (d < 0 || d >= a.V) return kReject;
   if (greedy) return p.at == d ? kAccept : kReject;
-  const float w =
-      __builtin_amdgcn_exp2f((T::get(row_ptr(a, b, slot, T::kBytes), d) - p.m) * c);
+  const float x = (logit<T>(row_ptr(a, b, slot, T::kBytes), d) - p.m) * c;
+  const float w = __builtin_amdgcn_exp2f(x);
   const float uz = a.u_accept[(int64_t)b * a.k + slot] * p.s;
-  // Either side's fp32 error is below 2^-15 of it (an exponent of up to 126 octaves, rounded
-  // twice, is off by 2^-16.4 of the weight) or below 2^-60 where a weight underflows.
-  if (fabsf(uz - w) <= (uz + w) * 0x1p-14f + 0x1p-60f) return kClose;
+  const float off = uz * (3 * groups + 64) + w * (1.04f * fminf(-x, 200.f) + 4);
+  if (fabsf(uz - w) <= off * 0x1p-23f + 0x1p-60f) return kClose;
   return uz < w ? kAccept : kReject;
 }
 
@@ -312,7 +370,7 @@ __device__ bool test_close(const VerifyArgs& a, int b, int slot, const Weights64
   double z = 0.0;
   for (int i = 0; i < kRowWaves; ++i) z += seg[i];
   const int d = a.draft[(int64_t)b * a.k + slot];
-  return (double)a.u_accept[(int64_t)b * a.k + slot] * z < weight64_full(T::get(row, d), m, inv);
+  return (double)a.u_accept[(int64_t)b * a.k + slot] * z < weight64_full(logit<T>(row, d), m, inv);
 }
 
 // ---------------------------------------------------------------- kernels
@@ -332,40 +390,61 @@ __global__ __launch_bounds__(kPartThreads) void verify_part_kernel(VerifyArgs a)
   if (threadIdx.x == 0) a.part[((int64_t)b * (a.k + 1) + slot) * a.parts + part] = p;
 }
 
-__global__ void verify_begin_kernel(VerifyArgs a) {
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b < a.B) a.stop[b] = clamp_valid(a, b);
-}
-
-// Large calls: one row, its test included; stop[b] is the lowest slot known to be rejected.
+// One whole row of a large call: its statistics and its test (one too close for fp32 is left to the
+// draw).  Returns whether the slot is rejected, in thread 0.
 template <typename T>
-__global__ __launch_bounds__(kRowThreads) void verify_row_kernel(VerifyArgs a) {
-  __shared__ VerifyPart whole;
-  __shared__ int verdict;
-  __shared__ double seg[kRowWaves], table[32];
-  const int slot = (int)(blockIdx.x / a.B), b = (int)(blockIdx.x % a.B);
-  if (slot > __hip_atomic_load(&a.stop[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) return;
+__device__ __forceinline__ bool take_row(const VerifyArgs& a, int slot, int b) {
   const float temp = temperature(a, b);
   const bool greedy = !(temp > 0.f);
   const float c = greedy ? 1.f : inv_log2(temp);
   const VerifyPart p =
       row_stats<T, kRowThreads>(row_ptr(a, b, slot, T::kBytes), 0, a.V, greedy, c);
-  const bool last = slot >= clamp_valid(a, b);
-  if (threadIdx.x == 0) {
-    a.part[(int64_t)b * (a.k + 1) + slot] = p;
-    whole = p;
-    verdict = last ? kAccept : test_slot<T>(a, b, slot, p, greedy, c);
-  }
-  __syncthreads();
-  if (verdict == kClose) {
-    fill_table(table);
+  if (threadIdx.x != 0) return false;
+  a.part[(int64_t)b * (a.k + 1) + slot] = p;
+  return slot < clamp_valid(a, b) &&
+         test_slot<T>(a, b, slot, p, greedy, c, a.V / (8 * kRowThreads) + 1) == kReject;
+}
+
+// Large calls, slot 0: also sets stop[b], the lowest slot known to be rejected (num_valid: none).
+template <typename T>
+__global__ __launch_bounds__(kRowThreads) void verify_first_kernel(VerifyArgs a) {
+  const int b = blockIdx.x;
+  const bool reject = take_row<T>(a, 0, b);
+  if (threadIdx.x == 0) a.stop[b] = reject ? 0 : clamp_valid(a, b);
+}
+
+// Large calls, the other slots: row t of the slot-major list is request (t + 37 slot) mod B, so
+// that a workgroup, which takes every gridDim.x-th, meets other requests in each slot.  It looks
+// at its next 64 rows at a time and goes to the first that still counts.
+template <typename T>
+__global__ __launch_bounds__(kRowThreads) void verify_rest_kernel(VerifyArgs a) {
+  __shared__ int64_t next;
+  const int64_t rows = (int64_t)a.B * a.k;
+  auto slot_of = [&](int64_t t) { return (int)(t / a.B) + 1; };
+  auto request_of = [&](int64_t t) { return (int)((t + 37 * (t / a.B)) % a.B); };
+  for (int64_t t = blockIdx.x; t < rows;) {
+    if (threadIdx.x < 64) {
+      const int64_t mine = t + (int64_t)threadIdx.x * gridDim.x;
+      const bool live =
+          mine < rows && slot_of(mine) <= __hip_atomic_load(&a.stop[request_of(mine)],
+                                                            __ATOMIC_RELAXED,
+                                                            __HIP_MEMORY_SCOPE_AGENT);
+      const unsigned long long any = __ballot(live);
+      if (threadIdx.x == 0)
+        next = any ? t + (int64_t)(__ffsll((long long)any) - 1) * gridDim.x
+                   : -(t + 64 * (int64_t)gridDim.x);
+    }
     __syncthreads();
-    const bool ok = test_close<T>(a, b, slot, weights64(table, whole.m, temp, greedy), whole.m,
-                                  inv64(temp), seg);
+    const int64_t at = next;
     __syncthreads();
-    if (threadIdx.x == 0) verdict = ok ? kAccept : kReject;
+    if (at < 0) {
+      t = -at;
+      continue;
+    }
+    const int slot = slot_of(at), b = request_of(at);
+    if (take_row<T>(a, slot, b)) atomicMin(&a.stop[b], slot);
+    t = at + gridDim.x;
   }
-  if (threadIdx.x == 0 && verdict == kReject) atomicMin(&a.stop[b], slot);
 }
 
 // What a request's draw starts from: the number accepted and the row's statistics.
@@ -378,16 +457,12 @@ struct Drawn {
 template <typename T>
 __device__ Drawn accepted(const VerifyArgs& a, int b, float temp, bool greedy, double* seg,
                           const double* table) {
-  if (a.stop) {
-    const int n = a.stop[b];
-    const VerifyPart p = a.part[(int64_t)b * (a.k + 1) + n];
-    return Drawn{n, p.m, p.at};
-  }
   __shared__ float row_m[kMaxRows];
   __shared__ int row_at[kMaxRows], verdict[kMaxRows];
-  const int nv = clamp_valid(a, b), tid = threadIdx.x;
+  // rows past `end` have no statistics, and slot `end` is known to be rejected or past the draft
+  const int end = a.stop ? a.stop[b] : clamp_valid(a, b), tid = threadIdx.x;
   const float c = greedy ? 1.f : inv_log2(temp);
-  if (tid <= nv) {
+  if (tid <= end) {
     const VerifyPart* p = a.part + ((int64_t)b * (a.k + 1) + tid) * a.parts;
     VerifyPart r = p[0];
     for (int i = 1; i < a.parts; ++i)
@@ -401,11 +476,14 @@ __device__ Drawn accepted(const VerifyArgs& a, int b, float temp, bool greedy, d
         r.s += p[i].s * __builtin_amdgcn_exp2f((p[i].m - r.m) * c);
     row_m[tid] = r.m;
     row_at[tid] = r.at;
-    verdict[tid] = tid < nv ? test_slot<T>(a, b, tid, r, greedy, c) : kReject;
+    verdict[tid] =
+        tid < end ? test_slot<T>(a, b, tid, r, greedy, c, a.stop ? a.V / (8 * kRowThreads) + 1
+                                                                 : a.part_size / (8 * kPartThreads) + 1)
+                  : kReject;
   }
   __syncthreads();
   int n = 0;
-  for (; n < nv; ++n) {
+  for (; n < end; ++n) {
     bool ok = verdict[n] == kAccept;
     if (verdict[n] == kClose)
       ok = test_close<T>(a, b, n, weights64(table, row_m[n], temp, greedy), row_m[n],
@@ -420,7 +498,7 @@ __device__ Drawn accepted(const VerifyArgs& a, int b, float temp, bool greedy, d
 // logits are left, which are scanned one a thread.
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) {
-  __shared__ double seg[kRowWaves], table[32];
+  __shared__ double seg[kRowWaves], table[kTable];
   __shared__ int found;
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const float temp = temperature(a, b);
@@ -449,13 +527,13 @@ __global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) 
           double z = 0.0;
           for (int i = 0; i < kRowWaves; ++i) z += seg[i];
           t = (double)a.u_sample[b] * z;
-          none = !(z > 0.0);
+          none = !(z > kTiny);
         }
         // the segment whose sums pass t; the last that holds anything if rounding hides it
         int at = 0;
         double before = base, run = base;
         for (int i = 0; i < kRowWaves; ++i)
-          if (seg[i] > 0.0) {
+          if (seg[i] > kTiny) {
             at = i;
             before = run;
             run += seg[i];
@@ -471,7 +549,7 @@ __global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) 
       const int j = j0 + tid;
       double x = 0.0;
       if (j < j1 && j != d)
-        x = whole ? weight64_full(T::get(row, j), r.m, inv) : weight64(w, T::get(row, j));
+        x = weight64_full(logit<T>(row, j), r.m, inv);
       double inc = x;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -503,7 +581,7 @@ __global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) 
         __syncthreads();
       }
       if (!none) pick = found;
-      if (!whole && t < 0x1p-900 && !none) {
+      if (!whole && t < kTiny && !none) {
         // A draw this close to 0 can land on weights that the fast ones leave out.
         if (wave == 0) {
           double run = 0.0;
@@ -511,7 +589,7 @@ __global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) 
           for (int i = 0; i < a.V; i += 64) {
             double y = 0.0;
             if (i + lane < a.V && i + lane != d)
-              y = weight64_full(T::get(row, i + lane), r.m, inv);
+              y = weight64_full(logit<T>(row, i + lane), r.m, inv);
             double sum = y;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
@@ -542,9 +620,11 @@ template <typename T>
 hipError_t launch_type(const VerifyArgs& a, hipStream_t st) {
   const int64_t rows = (int64_t)a.B * (a.k + 1);
   if (a.stop) {
-    hipLaunchKernelGGL(verify_begin_kernel, dim3((unsigned)((a.B + 255) / 256)), dim3(256), 0, st,
-                       a);
-    hipLaunchKernelGGL(verify_row_kernel<T>, dim3((unsigned)rows), dim3(kRowThreads), 0, st, a);
+    hipLaunchKernelGGL(verify_first_kernel<T>, dim3((unsigned)a.B), dim3(kRowThreads), 0, st, a);
+    const int64_t rest = rows - a.B;
+    if (rest > 0)
+      hipLaunchKernelGGL(verify_rest_kernel<T>, dim3((unsigned)(rest < 256 ? rest : 256)),
+                         dim3(kRowThreads), 0, st, a);
   } else {
     hipLaunchKernelGGL(verify_part_kernel<T>, dim3((unsigned)(rows * a.parts)),
                        dim3(kPartThreads), 0, st, a);
