@@ -503,7 +503,7 @@ int sfx_kv_attention(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t q_
  *   num_accepted [B] the number accepted.  A row with no token above -inf draws -1.
  * Comparisons are decided as in exact arithmetic up to fp64 rounding.  k within [0, 32].
  * workspace: sfx_verify_workspace_bytes, aligned to 16 bytes. */
-int sfx_verify_workspace_bytes(int32_t B, int32_t k, int32_t V, size_t* bytes);
+int sfx_verify_workspace_bytes(int32_t B, int32_t k, int32_t V, int32_t type, size_t* bytes);
 int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batch_stride,
                int64_t slot_stride, int32_t type, const float* temperature, const int32_t* draft,
                const int32_t* num_valid, const float* u_accept, const float* u_sample,

@@ -182,7 +182,7 @@ def load(path: str = LIB_PATH):
         "sfx_kv_attention": (ctypes.c_int, [_V, _I32, _I32, _I32, _I32, _V, _V, _V, _V, _V, _V,
                                             _I32, ctypes.c_float, _I32, _I32, _V,
                                             ctypes.c_size_t, _V]),
-        "sfx_verify_workspace_bytes": (ctypes.c_int, [_I32, _I32, _I32, _SIZE_P]),
+        "sfx_verify_workspace_bytes": (ctypes.c_int, [_I32, _I32, _I32, _I32, _SIZE_P]),
         "sfx_verify": (ctypes.c_int, [_I32, _I32, _I32, _V, _I64, _I64, _I32, _V, _V, _V, _V,
                                       _V, _V, _V, _V, ctypes.c_size_t, _V]),
     }
@@ -728,10 +728,11 @@ def verify(logits, draft, num_valid, u_accept, u_sample, temperature=None, sampl
         raise ValueError(f"sampled must be [{B}, {k1}] on {dev}")
     _vec(num_accepted, "num_accepted", B, torch.int32, dev)
     L, n = load(), ctypes.c_size_t(0)
-    _check(L.sfx_verify_workspace_bytes(B, k1 - 1, V, ctypes.byref(n)))
+    ty = _TYPES[logits.dtype]
+    _check(L.sfx_verify_workspace_bytes(B, k1 - 1, V, ty, ctypes.byref(n)))
     ws = _empty((n.value,), torch.uint8, dev, stream) if n.value else None
     _check(L.sfx_verify(B, k1 - 1, V, _ptr(logits), logits.stride(0), logits.stride(1),
-                        _TYPES[logits.dtype], _ptr(tp), _ptr(dr), _ptr(nv), _ptr(u_accept),
+                        ty, _ptr(tp), _ptr(dr), _ptr(nv), _ptr(u_accept),
                         _ptr(us), _ptr(sampled), _ptr(num_accepted), _ptr(ws), n.value,
                         _stream(stream)))
     return sampled, num_accepted

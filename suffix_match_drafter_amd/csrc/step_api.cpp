@@ -119,14 +119,16 @@ int attention_plan(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t q_he
   return SFX_OK;
 }
 
-int verify_shape(int32_t B, int32_t k, int32_t V, VerifyArgs* a, size_t* bytes) {
+int verify_shape(int32_t B, int32_t k, int32_t V, int32_t type, VerifyArgs* a, size_t* bytes) {
+  int rc = check_type(type, true);
+  if (rc) return rc;
   if (B < 0) return fail(SFX_EINVAL, "negative B=%d", B);
   if (k < 0 || k > 32) return fail(SFX_EINVAL, "k=%d outside [0,32]", k);
   if (V < 1 || V > (1 << 30)) return fail(SFX_EINVAL, "V=%d outside [1,2^30]", V);
   a->B = B;
   a->k = k;
   a->V = V;
-  *bytes = verify_plan(a);
+  *bytes = verify_plan(a, kv_type(type));
   if ((int64_t)B * (k + 1) * a->parts > kMaxGroups)
     return fail(SFX_ECAPACITY, "B=%d k=%d V=%d is too large for one call", B, k, V);
   return SFX_OK;
@@ -201,10 +203,10 @@ int sfx_kv_attention(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t q_
   return SFX_OK;
 }
 
-int sfx_verify_workspace_bytes(int32_t B, int32_t k, int32_t V, size_t* bytes) {
+int sfx_verify_workspace_bytes(int32_t B, int32_t k, int32_t V, int32_t type, size_t* bytes) {
   if (!bytes) return fail(SFX_EINVAL, "bytes is NULL");
   VerifyArgs a{};
-  return verify_shape(B, k, V, &a, bytes);
+  return verify_shape(B, k, V, type, &a, bytes);
 }
 
 int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batch_stride,
@@ -214,8 +216,7 @@ int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batc
                void* stream) {
   VerifyArgs a{};
   size_t bytes = 0;
-  int rc = verify_shape(B, k, V, &a, &bytes);
-  if (!rc) rc = check_type(type, true);
+  int rc = verify_shape(B, k, V, type, &a, &bytes);
   if (rc || B == 0) return rc;
   if (!logits || !u_sample || !sampled || !num_accepted || (k > 0 && (!draft || !u_accept)))
     return fail(SFX_EINVAL, "NULL array argument");

@@ -29,15 +29,19 @@ struct VerifyArgs {
   int32_t* sampled;
   int32_t* num_accepted;
   // plan (verify_plan)
-  bool in_order;      // one workgroup per row, in slot order, rows past a rejection left out
-  int32_t parts;      // workgroups of one row
-  int32_t part_size;  // its logits
+  bool in_order;      // slots in phases, rows past a rejection left out
+  int32_t parts;      // parts of one row (in_order: the most)
+  int32_t part_size;  // its logits (not in_order)
   VerifyPart* part;   // [B][k + 1][parts]
-  int32_t* stop;      // [B] lowest slot known to be rejected (in_order), else NULL
+  int32_t* stop;      // [phases][B] lowest slot known to be rejected (in_order, else NULL)
+  int32_t* phase_parts;  // [phases] parts of a row (in_order, else NULL)
 };
 
+constexpr int kVerifyMaxParts = 16;      // of a row, in_order
+constexpr int kVerifyMaxOrdered = 2048;  // requests of an in_order call (a list in LDS)
+
 // Fills the plan from the shapes; returns the workspace bytes it needs.
-size_t verify_plan(VerifyArgs* a);
+size_t verify_plan(VerifyArgs* a, KvType type);
 
 // Places the plan's buffers in the workspace.
 void verify_place(VerifyArgs* a, void* workspace);

@@ -15,10 +15,10 @@
 // test whose two sides are within the fp32 pass's error bound is redone in fp64, and the row that
 // is drawn from is summed and searched in fp64.
 //
-// Work.  Rows past the first rejection decide nothing.  Large calls take the first slot of every
-// request, then the other slots in order with one workgroup per CU, and leave out rows of requests
-// that are known by then to have been rejected earlier.  Small calls, which do not fill the card
-// with whole rows, read all rows in parts at once.
+// Work.  Rows past the first rejection decide nothing.  Large calls go through the slots in four
+// launches (0, 1-2, 3-6, 7-k), each over the requests that are still undecided, so that few rows are
+// read in vain and each launch fills the card.  Small calls, where four launches would cost more
+// than the rows they save, read all rows in parts at once.
 #include "verify.h"
 
 #include <hip/hip_bf16.h>
@@ -32,6 +32,8 @@ constexpr int kPartThreads = 256;   // workgroup of a part of a row
 constexpr int kRowThreads = 1024;   // workgroup of a whole row, and of a request's draw
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kMaxRows = 33;        // k + 1
+constexpr int kPhaseThreads = 512;  // workgroup of a phase after the first
+constexpr int kPhaseGroups = 512;   // two on each of 256 CUs
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
@@ -171,9 +173,12 @@ __device__ __forceinline__ float inv_log2(float t) {
 }
 __device__ __forceinline__ double inv64(float t) { return fmax(1.0 / (double)t, 1e-300); }
 
-__device__ __forceinline__ float fmerge(float m, float s, float m2, float s2, float c, float mm) {
-  const float z = mm == -__builtin_inff() ? 0.f : mm;
-  return s * __builtin_amdgcn_exp2f((m - z) * c) + s2 * __builtin_amdgcn_exp2f((m2 - z) * c);
+// Two parts of a row as one; of equal largest logits the lowest index.
+__device__ __forceinline__ VerifyPart join(const VerifyPart& p, const VerifyPart& q, float c) {
+  const float m = fmaxf(p.m, q.m), z = m == -__builtin_inff() ? 0.f : m;
+  return VerifyPart{m, p.s * __builtin_amdgcn_exp2f((p.m - z) * c) +
+                           q.s * __builtin_amdgcn_exp2f((q.m - z) * c),
+                    q.m > p.m || (q.m == p.m && q.at < p.at) ? q.at : p.at, 0};
 }
 
 // Largest logit, its lowest index and the sum of exponentials of logits [j0, j1) of a row, by a
@@ -205,26 +210,15 @@ __device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, fl
       s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
     }
   });
+  VerifyPart r{m, s, at, 0};
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
-    const int at2 = __shfl_xor(at, o);
-    const float mm = fmaxf(m, m2);
-    s = fmerge(m, s, m2, s2, c, mm);
-    at = m2 > m || (m2 == m && at2 < at) ? at2 : at;
-    m = mm;
-  }
+  for (int o = 32; o >= 1; o >>= 1)
+    r = join(r, VerifyPart{__shfl_xor(r.m, o), __shfl_xor(r.s, o), __shfl_xor(r.at, o), 0}, c);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = VerifyPart{m, s, at, 0};
+  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = r;
   __syncthreads();
-  VerifyPart r = w[0];
-  for (int i = 1; i < N / 64; ++i) {
-    const VerifyPart p = w[i];
-    const float mm = fmaxf(r.m, p.m);
-    r.s = fmerge(r.m, r.s, p.m, p.s, c, mm);
-    r.at = p.m > r.m || (p.m == r.m && p.at < r.at) ? p.at : r.at;
-    r.m = mm;
-  }
+  r = w[0];
+  for (int i = 1; i < N / 64; ++i) r = join(r, w[i], c);
   return r;
 }
 
@@ -245,7 +239,7 @@ __device__ __forceinline__ const char* row_ptr(const VerifyArgs& a, int b, int s
 // exp by a table of 2^(i/256) and a polynomial over 1/256 of an octave, |z| <= ln 2 / 512:
 //   2^(n/256 + f/256) = 2^(n div 256) T[n mod 256] (1 + z + z^2/2 + z^3/6),  z = f ln 2 / 256,
 // within 2^-42 of the function.  The search for the drawn token is bounded by these instructions
-// (19 a logit; 27 with 32 entries, two more terms and a select took 49 us a row of 151936, not
+// (20 a logit; 27 with 32 entries, two more terms and a select took 49 us a row of 151936, not
 // 36).  Logits more than 700 T below the largest weigh e^-700 here, whatever they are: what they
 // add is far below a draw's resolution unless the draw is below kTiny, which is done again with
 // the exact function.
@@ -258,7 +252,7 @@ struct Weights64 {
   const double* table;  // kTable entries in LDS
   double k;             // 256 log2(e) / T
   double m;
-  float lo;             // m - 700 T
+  double lo;            // -700 T
 };
 
 __device__ __forceinline__ void fill_table(double* table) {
@@ -268,19 +262,17 @@ __device__ __forceinline__ void fill_table(double* table) {
 __device__ __forceinline__ Weights64 weights64(const double* table, float m, float temp,
                                                bool greedy) {
   const double inv = greedy ? 1.0 : inv64(temp);
-  const double lo = fmax((double)m - 700.0 / inv, -3.402823466e38);
-  float f = (float)lo;
-  if ((double)f < lo) f = nextafterf(f, 3.402823466e38f);  // up: exponents stay within fp64's
-  return Weights64{table, inv * (kTable * 1.4426950408889634074), (double)m, f};
+  return Weights64{table, inv * (kTable * 1.4426950408889634074), (double)m, -700.0 / inv};
 }
 
 // Sum of four weights, stage by stage: each weight is one chain of dependent instructions.  The
-// median takes a NaN and -inf to lo and +inf to the largest float.
+// median takes a NaN and -inf to the lowest float and +inf to the largest.
 __device__ __forceinline__ double weights4(const Weights64& w, const float* x) {
   double f[4], p[4], ts[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const double d = (double)__builtin_amdgcn_fmed3f(x[e], w.lo, 3.402823466e38f) - w.m;
+    const double d = fmax(
+        (double)__builtin_amdgcn_fmed3f(x[e], -3.402823466e38f, 3.402823466e38f) - w.m, w.lo);
     const double t = fma(d, w.k, kMagic);
     const int n = (int)__double_as_longlong(t);  // low word: the integer
     f[e] = fma(d, w.k, -(t - kMagic));
@@ -390,60 +382,121 @@ __global__ __launch_bounds__(kPartThreads) void verify_part_kernel(VerifyArgs a)
   if (threadIdx.x == 0) a.part[((int64_t)b * (a.k + 1) + slot) * a.parts + part] = p;
 }
 
-// One whole row of a large call: its statistics and its test (one too close for fp32 is left to the
-// draw).  Returns whether the slot is rejected, in thread 0.
-template <typename T>
-__device__ __forceinline__ bool take_row(const VerifyArgs& a, int slot, int b) {
-  const float temp = temperature(a, b);
-  const bool greedy = !(temp > 0.f);
-  const float c = greedy ? 1.f : inv_log2(temp);
-  const VerifyPart p =
-      row_stats<T, kRowThreads>(row_ptr(a, b, slot, T::kBytes), 0, a.V, greedy, c);
-  if (threadIdx.x != 0) return false;
-  a.part[(int64_t)b * (a.k + 1) + slot] = p;
-  return slot < clamp_valid(a, b) &&
-         test_slot<T>(a, b, slot, p, greedy, c, a.V / (8 * kRowThreads) + 1) == kReject;
+// ---------------------------------------------------------------- phases of a large call
+// Phase 0 is slot 0, 1: slots 1-2, 2: 3-6, 3: the rest.
+constexpr int kPhases = 4;
+__device__ __host__ __forceinline__ int phase_begin(int phase) {
+  return phase == 0 ? 0 : (1 << phase) - 1;
+}
+__device__ __host__ __forceinline__ int phase_end(int phase, int k) {
+  const int e = phase == kPhases - 1 ? k : (2 << phase) - 2;
+  return e < k ? e : k;
+}
+__device__ __host__ __forceinline__ int last_phase(int k) {
+  return k == 0 ? 0 : (k < 3 ? 1 : (k < 7 ? 2 : 3));
+}
+__device__ __forceinline__ int phase_of(int slot) {
+  return slot == 0 ? 0 : (slot < 3 ? 1 : (slot < 7 ? 2 : 3));
 }
 
-// Large calls, slot 0: also sets stop[b], the lowest slot known to be rejected (num_valid: none).
+// Logits of one of `parts` parts of a row.
+__device__ __forceinline__ int phase_part(int V, int parts) {
+  return ((V + parts - 1) / parts + 7) / 8 * 8;
+}
+
+// A row's parts, `parts` of them, as one.
+__device__ __forceinline__ VerifyPart join_row(const VerifyArgs& a, int64_t row, int parts,
+                                               float c) {
+  VerifyPart r = a.part[row * a.parts];
+  for (int i = 1; i < parts; ++i) r = join(r, a.part[row * a.parts + i], c);
+  return r;
+}
+
+// Slot 0: one workgroup per request.  stop[phase][b] is the lowest slot of request b that phase
+// knows to be rejected; none yet (num_valid).
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void verify_first_kernel(VerifyArgs a) {
   const int b = blockIdx.x;
-  const bool reject = take_row<T>(a, 0, b);
-  if (threadIdx.x == 0) a.stop[b] = reject ? 0 : clamp_valid(a, b);
+  const float temp = temperature(a, b);
+  const bool greedy = !(temp > 0.f);
+  const VerifyPart p = row_stats<T, kRowThreads>(row_ptr(a, b, 0, T::kBytes), 0, a.V, greedy,
+                                                 greedy ? 1.f : inv_log2(temp));
+  if (threadIdx.x == 0) {
+    a.part[(int64_t)b * (a.k + 1) * a.parts] = p;
+    a.stop[b] = clamp_valid(a, b);
+    if (b == 0) a.phase_parts[0] = 1;
+  }
 }
 
-// Large calls, the other slots: row t of the slot-major list is request (t + 37 slot) mod B, so
-// that a workgroup, which takes every gridDim.x-th, meets other requests in each slot.  It looks
-// at its next 64 rows at a time and goes to the first that still counts.
+// A later phase.  Every workgroup first makes the tests of the phase before (a few loads a thread;
+// joining the workgroups through memory instead took fences that cost more than the rows), which
+// gives them all the same list of requests that are undecided, and then takes its share of the
+// parts of their rows.
 template <typename T>
-__global__ __launch_bounds__(kRowThreads) void verify_rest_kernel(VerifyArgs a) {
-  __shared__ int64_t next;
-  const int64_t rows = (int64_t)a.B * a.k;
-  auto slot_of = [&](int64_t t) { return (int)(t / a.B) + 1; };
-  auto request_of = [&](int64_t t) { return (int)((t + 37 * (t / a.B)) % a.B); };
-  for (int64_t t = blockIdx.x; t < rows;) {
-    if (threadIdx.x < 64) {
-      const int64_t mine = t + (int64_t)threadIdx.x * gridDim.x;
-      const bool live =
-          mine < rows && slot_of(mine) <= __hip_atomic_load(&a.stop[request_of(mine)],
-                                                            __ATOMIC_RELAXED,
-                                                            __HIP_MEMORY_SCOPE_AGENT);
-      const unsigned long long any = __ballot(live);
-      if (threadIdx.x == 0)
-        next = any ? t + (int64_t)(__ffsll((long long)any) - 1) * gridDim.x
-                   : -(t + 64 * (int64_t)gridDim.x);
+__global__ __launch_bounds__(kPhaseThreads) void verify_phase_kernel(VerifyArgs a, int phase) {
+  __shared__ int stop[kVerifyMaxOrdered], live[kVerifyMaxOrdered], count;
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int b = tid; b < a.B; b += kPhaseThreads) stop[b] = a.stop[(phase - 1) * a.B + b];
+  __syncthreads();
+  {
+    const int q0 = phase_begin(phase - 1), q1 = phase_end(phase - 1, a.k);
+    const int parts = a.phase_parts[phase - 1];
+    const int groups = phase == 1 ? a.V / (8 * kRowThreads) + 1
+                                  : phase_part(a.V, parts) / (8 * kPhaseThreads) + 1;
+    for (int i = tid; i < a.B * (q1 - q0 + 1); i += kPhaseThreads) {
+      const int b = i % a.B, slot = q0 + i / a.B;
+      if (slot >= stop[b]) continue;  // not read, known, or past the draft
+      const float temp = temperature(a, b);
+      const bool greedy = !(temp > 0.f);
+      const float c = greedy ? 1.f : inv_log2(temp);
+      const VerifyPart p = join_row(a, (int64_t)b * (a.k + 1) + slot, parts, c);
+      if (test_slot<T>(a, b, slot, p, greedy, c, groups) == kReject) atomicMin(&stop[b], slot);
     }
-    __syncthreads();
-    const int64_t at = next;
-    __syncthreads();
-    if (at < 0) {
-      t = -at;
-      continue;
+  }
+  __syncthreads();
+  const int s0 = phase_begin(phase), s1 = phase_end(phase, a.k);
+  if (tid < 64) {
+    int n = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+      const int b = b0 + lane;
+      const bool in = b < a.B && stop[b] >= s0;
+      const unsigned long long any = __ballot(in);
+      if (in) live[n + __popcll(any & ((1ull << lane) - 1))] = b;
+      n += __popcll(any);
     }
-    const int slot = slot_of(at), b = request_of(at);
-    if (take_row<T>(a, slot, b)) atomicMin(&a.stop[b], slot);
-    t = at + gridDim.x;
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int n = count;
+  // The number of parts that makes the busiest workgroup's time least: its rounds, each a part of
+  // a row and about 1/8 of one besides (starting the loads, joining the threads).
+  const int64_t rows = (int64_t)n * (s1 - s0 + 1);
+  int parts = 1;
+  float least = 3.4e38f;
+  for (int p = 1; p <= a.parts && p * 4096 <= a.V; ++p) {
+    const float t = (float)((rows * p + kPhaseGroups - 1) / kPhaseGroups) * (1.f / p + 0.125f);
+    if (t < least) {
+      least = t;
+      parts = p;
+    }
+  }
+  if (blockIdx.x == 0) {
+    for (int b = tid; b < a.B; b += kPhaseThreads) a.stop[phase * a.B + b] = stop[b];
+    if (tid == 0) a.phase_parts[phase] = parts;
+  }
+  const int size = phase_part(a.V, parts);
+  for (int64_t i = blockIdx.x; i < rows * parts; i += gridDim.x) {
+    const int part = (int)(i % parts);
+    const int64_t r = i / parts;
+    const int slot = s0 + (int)(r / n), b = live[r % n];
+    if (slot > stop[b]) continue;  // past num_valid
+    const float temp = temperature(a, b);
+    const bool greedy = !(temp > 0.f);
+    const int j0 = part * size < a.V ? part * size : a.V;
+    const int j1 = a.V - j0 < size ? a.V : j0 + size;
+    const VerifyPart p = row_stats<T, kPhaseThreads>(row_ptr(a, b, slot, T::kBytes), j0, j1,
+                                                     greedy, greedy ? 1.f : inv_log2(temp));
+    if (tid == 0) a.part[((int64_t)b * (a.k + 1) + slot) * a.parts + part] = p;
   }
 }
 
@@ -459,27 +512,21 @@ __device__ Drawn accepted(const VerifyArgs& a, int b, float temp, bool greedy, d
                           const double* table) {
   __shared__ float row_m[kMaxRows];
   __shared__ int row_at[kMaxRows], verdict[kMaxRows];
-  // rows past `end` have no statistics, and slot `end` is known to be rejected or past the draft
-  const int end = a.stop ? a.stop[b] : clamp_valid(a, b), tid = threadIdx.x;
+  // rows past `end` have no statistics; slot `end` is past the draft or known to be rejected
+  const int tid = threadIdx.x;
+  const int end = a.stop ? a.stop[last_phase(a.k) * a.B + b] : clamp_valid(a, b);
   const float c = greedy ? 1.f : inv_log2(temp);
   if (tid <= end) {
-    const VerifyPart* p = a.part + ((int64_t)b * (a.k + 1) + tid) * a.parts;
-    VerifyPart r = p[0];
-    for (int i = 1; i < a.parts; ++i)
-      if (p[i].m > r.m) {
-        r.m = p[i].m;
-        r.at = p[i].at;
-      }
-    r.s = 0.f;
-    if (r.m > -__builtin_inff())
-      for (int i = 0; i < a.parts; ++i)
-        r.s += p[i].s * __builtin_amdgcn_exp2f((p[i].m - r.m) * c);
+    const int64_t row = (int64_t)b * (a.k + 1) + tid;
+    const int phase = phase_of(tid);
+    const int parts = a.stop ? a.phase_parts[phase] : a.parts;
+    const VerifyPart r = join_row(a, row, parts, c);
+    const int groups = 1 + (!a.stop ? a.part_size / (8 * kPartThreads)
+                                    : phase == 0 ? a.V / (8 * kRowThreads)
+                                                 : phase_part(a.V, parts) / (8 * kPhaseThreads));
     row_m[tid] = r.m;
     row_at[tid] = r.at;
-    verdict[tid] =
-        tid < end ? test_slot<T>(a, b, tid, r, greedy, c, a.stop ? a.V / (8 * kRowThreads) + 1
-                                                                 : a.part_size / (8 * kPartThreads) + 1)
-                  : kReject;
+    verdict[tid] = tid < end ? test_slot<T>(a, b, tid, r, greedy, c, groups) : kReject;
   }
   __syncthreads();
   int n = 0;
@@ -621,10 +668,9 @@ hipError_t launch_type(const VerifyArgs& a, hipStream_t st) {
   const int64_t rows = (int64_t)a.B * (a.k + 1);
   if (a.stop) {
     hipLaunchKernelGGL(verify_first_kernel<T>, dim3((unsigned)a.B), dim3(kRowThreads), 0, st, a);
-    const int64_t rest = rows - a.B;
-    if (rest > 0)
-      hipLaunchKernelGGL(verify_rest_kernel<T>, dim3((unsigned)(rest < 256 ? rest : 256)),
-                         dim3(kRowThreads), 0, st, a);
+    for (int phase = 1; phase <= last_phase(a.k); ++phase)
+      hipLaunchKernelGGL(verify_phase_kernel<T>, dim3(kPhaseGroups), dim3(kPhaseThreads), 0, st, a,
+                         phase);
   } else {
     hipLaunchKernelGGL(verify_part_kernel<T>, dim3((unsigned)(rows * a.parts)),
                        dim3(kPartThreads), 0, st, a);
@@ -637,25 +683,28 @@ hipError_t launch_type(const VerifyArgs& a, hipStream_t st) {
 
 }  // namespace
 
-size_t verify_plan(VerifyArgs* a) {
+size_t verify_plan(VerifyArgs* a, KvType type) {
+  const int bytes = type == kFp32 ? 4 : 2;
   const int64_t rows = (int64_t)a->B * (a->k + 1);
-  a->in_order = rows >= 512 && a->V >= 16384;
+  a->in_order = a->B <= kVerifyMaxOrdered && (double)rows * a->V * bytes >= 2e8;
   // else parts of at least 16K logits, enough of them to fill 256 CUs four times over
   int64_t parts = rows > 0 ? (1024 + rows - 1) / rows : 1;
   const int64_t most = ((int64_t)a->V + 16383) / 16384;
   parts = parts > most ? most : parts;
-  parts = parts < 1 || a->in_order ? 1 : parts;
+  parts = parts < 1 ? 1 : parts;
   const int64_t size = (a->V + parts - 1) / parts;
   a->part_size = (int32_t)((size + 7) / 8 * 8);
   a->parts = (int32_t)((a->V + a->part_size - 1) / a->part_size);
-  if (a->parts < 1) a->parts = 1;
+  if (a->in_order) a->parts = kVerifyMaxParts;
   return (size_t)rows * a->parts * sizeof(VerifyPart) +
-         (a->in_order ? (size_t)a->B * sizeof(int32_t) : 0);
+         (a->in_order ? (size_t)kPhases * (a->B + 1) * sizeof(int32_t) : 0);
 }
 
 void verify_place(VerifyArgs* a, void* workspace) {
+  const size_t rows = (size_t)a->B * (a->k + 1);
   a->part = (VerifyPart*)workspace;
-  a->stop = a->in_order ? (int32_t*)(a->part + (size_t)a->B * (a->k + 1) * a->parts) : nullptr;
+  a->stop = a->in_order ? (int32_t*)(a->part + rows * a->parts) : nullptr;
+  a->phase_parts = a->in_order ? a->stop + (size_t)kPhases * a->B : nullptr;
 }
 
 hipError_t launch_verify(const VerifyArgs& a, KvType type, hipStream_t st) {

@@ -95,9 +95,10 @@ def test_bad_verify():
     assert verify(B=0, logits=None, us=None, ws=None) == sfx.OK
     n = ctypes.c_size_t()
     L = sfx.load()
-    assert L.sfx_verify_workspace_bytes(4, 8, 1000, None) == sfx.EINVAL
-    assert L.sfx_verify_workspace_bytes(4, 33, 1000, ctypes.byref(n)) == sfx.EINVAL
-    assert L.sfx_verify_workspace_bytes(4, 8, 1000, ctypes.byref(n)) == sfx.OK and n.value > 0
+    assert L.sfx_verify_workspace_bytes(4, 8, 1000, 0, None) == sfx.EINVAL
+    assert L.sfx_verify_workspace_bytes(4, 33, 1000, 0, ctypes.byref(n)) == sfx.EINVAL
+    assert L.sfx_verify_workspace_bytes(4, 8, 1000, 3, ctypes.byref(n)) == sfx.EINVAL
+    assert L.sfx_verify_workspace_bytes(4, 8, 1000, 2, ctypes.byref(n)) == sfx.OK and n.value > 0
 
 
 def test_python_refusals():

@@ -241,3 +241,45 @@ def test_step_with_the_drafter(S):
     after = S.update_state(tok.clone(), S.update_state(tok, n, samp), out)
     assert after.tolist() == [21 + k + 1] * B
     d.close()
+
+
+@pytest.mark.parametrize("dtype,B,k,V", [("float32", 26, 16, 120011), ("bfloat16", 150, 32, 20481),
+                                         ("float16", 2048, 3, 12345), ("float16", 2049, 3, 12345)])
+def test_large_calls(S, dtype, B, k, V):
+    """Calls large enough to go through the slots in phases (and one too wide for that): all
+    accepted, none, greedy, masked rows, counts of 0 and k, and a second pass over one workspace's
+    worth of memory."""
+    rng = np.random.default_rng(V)
+    import torch
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    x = torch.randn((B, k + 1, V), generator=g, device="cuda").mul_(2).to(getattr(torch, dtype))
+    draft = rng.integers(0, V, size=(B, k)).astype(np.int32)
+    nv = rng.integers(0, k + 1, size=B).astype(np.int32)
+    like = rng.random((B, k)) < 0.85
+    like[:4] = True
+    nv[:4] = k
+    like[4:8] = False
+    at = np.where(like, draft, rng.integers(0, V, size=(B, k)))
+    x[:, :k].scatter_(2, dev(at)[:, :, None], 16.0)
+    temp = rng.uniform(0.5, 1.3, B).astype(np.float32)
+    temp[[1, 5, 9, 10]] = 0.0
+    ua = rng.random((B, k)).astype(np.float32)
+    us = rng.random(B).astype(np.float32)
+    ua[0] = 0.0
+    x[11, 0] = -float("inf")
+    x[12, 1, ::2] = -float("inf")
+    x[13, 0, 5] = float("nan")
+    x[14, 0, [7, V - 1]] = float("inf")
+    nv[11:15] = k
+    rows = list(range(15)) + list(range(15, B, max(1, B // 12)))
+    for step in range(2):
+        out, na = S.verify(x, dev(draft), dev(nv), dev(ua), dev(us), dev(temp))
+        torch.cuda.synchronize()
+        for b in rows:
+            s, n = M.verify(x[b].double().cpu().numpy(), draft[b], nv[b], ua[b], us[b],
+                            float(temp[b]))
+            assert na[b].item() == n and np.array_equal(out[b].cpu().numpy(), s), (b, n)
+        us = rng.random(B).astype(np.float32)
+        ua = rng.random((B, k)).astype(np.float32)
