@@ -142,15 +142,6 @@ __device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int r0,
   return s;
 }
 
-// One tile's codes and scales as they come from memory.
-template <int D>
-struct Tile {
-  u32x4 k[D / 32];
-  u32x4 v[D / 32];
-  float ks, vs;
-  bool mapped;
-};
-
 // Block number of list entry i; its page id (-1: unmapped), read through the scalar cache.
 __device__ __forceinline__ int block_of(const Span& s, int i) {
   return __builtin_amdgcn_readfirstlane(i < s.nsink ? i : s.first + i - s.nsink);
@@ -159,32 +150,51 @@ __device__ __forceinline__ int page_id(const KvAttentionArgs& a, const int32_t* 
   return __builtin_amdgcn_readfirstlane(table[kv_page_of(a.c, block)]);
 }
 
+// Where a tile lies: its (page, head) and its block there.
+struct Place {
+  int64_t ph;
+  int sub;
+  bool mapped;
+};
+__device__ __forceinline__ Place place_of(const KvAttentionArgs& a, int h, int block, int page) {
+  const int per_page = a.c.page_size / kKvBlock;
+  const bool mapped = page >= 0 && page < a.c.num_pages;
+  return Place{(int64_t)(mapped ? page : 0) * a.c.heads + h,
+               block - kv_page_of(a.c, block) * per_page, mapped};
+}
+
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D>& t, const KvAttentionArgs& a, int h, int block,
-                                          int page, int lane) {
-  t.mapped = page >= 0 && page < a.c.num_pages;
-  if (!t.mapped) {
+__device__ __forceinline__ void load_k(u32x4 (&k)[D / 32], float& scale, const KvAttentionArgs& a,
+                                       const Place& p, int off) {
+  if (!p.mapped) {
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) t.k[c] = t.v[c] = u32x4{0, 0, 0, 0};
-    t.ks = t.vs = 1.f;
+    for (int c = 0; c < D / 32; ++c) k[c] = u32x4{0, 0, 0, 0};
+    scale = 1.f;
     return;
   }
-  const int per_page = a.c.page_size / kKvBlock;
-  const int sub = block - kv_page_of(a.c, block) * per_page;
-  const int64_t ph = (int64_t)page * a.c.heads + h;
-  const uint8_t* kb = a.c.k + ph * a.c.page_size * D + (int64_t)sub * kKvBlock * 64;
-  const uint8_t* vb = a.c.v + ph * a.c.page_size * D + (int64_t)sub * kKvBlock * D;
-  const int off = (lane & 15) * 64 + (lane >> 4) * 16;
+  const uint8_t* base = a.c.k + p.ph * a.c.page_size * D + (int64_t)p.sub * kKvBlock * 64;
 #pragma unroll
   for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
     for (int j = 0; j < D / 64; ++j)
-      t.k[tt * (D / 64) + j] =
-          *(const u32x4*)(kb + (int64_t)j * a.c.page_size * 64 + tt * 1024 + off);
+      k[tt * (D / 64) + j] =
+          *(const u32x4*)(base + (int64_t)j * a.c.page_size * 64 + tt * 1024 + off);
+  scale = a.c.k_scale[p.ph * (a.c.page_size / kKvBlock) + p.sub];
+}
+
+template <int D>
+__device__ __forceinline__ void load_v(u32x4 (&v)[D / 32], float& scale, const KvAttentionArgs& a,
+                                       const Place& p, int off) {
+  if (!p.mapped) {
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) t.v[c] = *(const u32x4*)(vb + c * 1024 + off);
-  t.ks = a.c.k_scale[ph * per_page + sub];
-  t.vs = a.c.v_scale[ph * per_page + sub];
+    for (int c = 0; c < D / 32; ++c) v[c] = u32x4{0, 0, 0, 0};
+    scale = 1.f;
+    return;
+  }
+  const uint8_t* base = a.c.v + p.ph * a.c.page_size * D + (int64_t)p.sub * kKvBlock * D;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) v[c] = *(const u32x4*)(base + c * 1024 + off);
+  scale = a.c.v_scale[p.ph * (a.c.page_size / kKvBlock) + p.sub];
 }
 
 // Bytes of a dword that are e4m3 NaNs, as 0x80 flags.
@@ -192,9 +202,12 @@ __device__ __forceinline__ unsigned nan_bytes(unsigned w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// Wavefronts of a SIMD that the registers of a variant leave room for.
+constexpr int waves_per_simd(int D, int RT) { return D * RT <= 128 ? 3 : (D * RT <= 384 ? 2 : 1); }
+
 // One (chunk, split): RT 16-row tiles by the split's tokens.
 template <typename T, int D, int RT>
-__global__ __launch_bounds__(64 * kWaves) void kv_attention_kernel(KvAttentionArgs a) {
+__global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attention_kernel(KvAttentionArgs a) {
   constexpr int kSlabs = D / 64, kVc = D / 32;
   constexpr int kPiece = D < 128 ? D : 128;  // dims of one pass of the final reduction
   __shared__ float red[kWaves][16][kPiece + 4];
@@ -253,31 +266,29 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_kernel(KvAttentionAr
   float cs = a.scale_log2;
   bool first_tile = true;
 
+  // A tile's codes stay in one set of registers: the next keys are loaded as soon as the scores
+  // are made, the next values as soon as the outputs are, each behind the other's work.
   const int32_t* table = a.page_table + (int64_t)b * a.max_pages;
-  Tile<D> cur;
-  int i = i0 + wave;
-  int nblock = 0, npage = -1;
+  const int off = n * 64 + g * 16;
+  u32x4 kc[kVc], vc[kVc];
+  float ks = 1.f, vs = 1.f;
+  Place here{};
+  int i = i0 + wave, block = 0, next_block = 0, next_page = -1;
   if (i < i1) {
-    const int blk = block_of(s, i);
-    load_tile<D>(cur, a, h, blk, page_id(a, table, blk), lane);
+    block = block_of(s, i);
+    here = place_of(a, h, block, page_id(a, table, block));
+    load_k<D>(kc, ks, a, here, off);
+    load_v<D>(vc, vs, a, here, off);
     if (i + kWaves < i1) {
-      nblock = block_of(s, i + kWaves);
-      npage = page_id(a, table, nblock);
+      next_block = block_of(s, i + kWaves);
+      next_page = page_id(a, table, next_block);
     }
   }
   for (; i < i1; i += kWaves) {
-    const int block = block_of(s, i);
-    Tile<D> nxt;
-    if (i + kWaves < i1) {
-      load_tile<D>(nxt, a, h, nblock, npage, lane);
-      if (i + 2 * kWaves < i1) {
-        nblock = block_of(s, i + 2 * kWaves);
-        npage = page_id(a, table, nblock);
-      }
-    }
+    const bool more = i + kWaves < i1;
     // reference exponents
-    const int ek = __builtin_amdgcn_readfirstlane(kv_exp_of(cur.ks));
-    const int ev = __builtin_amdgcn_readfirstlane(kv_exp_of(cur.vs));
+    const int ek = __builtin_amdgcn_readfirstlane(kv_exp_of(ks));
+    const int ev = __builtin_amdgcn_readfirstlane(kv_exp_of(vs));
     if (first_tile || ek - kref < kRefLo || ek - kref > kRefHi) {
       kref = ek - 1;
       cs = a.scale_log2 * kv_pow2(kref);
@@ -301,32 +312,66 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_kernel(KvAttentionAr
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) sc[rt][0] = sc[rt][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int tt = 0; tt < 2; ++tt)
+    for (int m = 0; m < 2 * kSlabs; ++m)
 #pragma unroll
-      for (int m = 0; m < 2 * kSlabs; ++m) {
-        const u32x4 w = cur.k[tt * kSlabs + (m >> 1)];
+      for (int tt = 0; tt < 2; ++tt) {
+        const u32x4 w = kc[tt * kSlabs + (m >> 1)];
         const auto kf = T::widen(w[2 * (m & 1)], w[2 * (m & 1) + 1], kscale);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) sc[rt][tt] = T::mfma(kf, q[rt][m], sc[rt][tt]);
       }
+    Place next{};
+    if (more) {
+      next = place_of(a, h, next_block, next_page);
+      load_k<D>(kc, ks, a, next, off);
+    }
 
     // masks: only where some row does not see the whole tile
     const int j0 = block * kKvBlock;
-    const bool whole = cur.mapped && j0 + kKvBlock - 1 <= s.lo_pos &&
+    const bool whole = here.mapped && j0 + kKvBlock - 1 <= s.lo_pos &&
                        (a.window == 0 || s.hi_pos - j0 < a.window || j0 + kKvBlock <= a.sinks);
-    unsigned seen[RT];  // bit 4 tt + i: the lane's row sees token 16 tt + 4 g + i
     if (!whole) {
+      unsigned seen[RT];  // bit 4 tt + i: the lane's row sees token 16 tt + 4 g + i
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         seen[rt] = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int j = j0 + 16 * (e >> 2) + 4 * g + (e & 3);
-          const bool see = cur.mapped && j <= pos[rt] &&
+          const bool see = here.mapped && j <= pos[rt] &&
                            (a.window == 0 || pos[rt] - j < a.window || j < a.sinks);
           if (see) seen[rt] |= 1u << e;
           sc[rt][e >> 2][e & 3] = see ? sc[rt][e >> 2][e & 3] : -__builtin_inff();
         }
+      }
+      unsigned f = 0;
+#pragma unroll
+      for (int c = 0; c < kVc; ++c)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) f |= nan_bytes(vc[c][d]);
+      if (__any(f != 0)) {
+#pragma unroll
+        for (int c = 0; c < kVc; ++c)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            // 0x80 flags widened to whole bytes; 0x38 is the code of 1
+            const unsigned n0 = (nan_bytes(vc[c][2 * f]) >> 7) * 255u;
+            const unsigned n1 = (nan_bytes(vc[c][2 * f + 1]) >> 7) * 255u;
+            vc[c][2 * f] &= ~n0;
+            vc[c][2 * f + 1] &= ~n1;
+            const f16x8 nf = Fp16::widen(n0 & 0x38383838u, n1 & 0x38383838u, 1.f);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              f16x8 see;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                see[e] = (seen[rt] >> e & 1) ? (_Float16)1.f : (_Float16)0.f;
+              const f32x4 hit = Fp16::mfma(nf, see, f32x4{0, 0, 0, 0});
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[rt][c][f][e] = hit[e] > 0.f ? __builtin_nanf("") : o[rt][c][f][e];
+            }
+          }
       }
     }
 
@@ -369,50 +414,23 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_kernel(KvAttentionAr
 
     // outputs
     const float vscale = kv_pow2(ev - vref);
-    bool bad = false;
-    if (!whole) {
-      unsigned f = 0;
 #pragma unroll
-      for (int c = 0; c < kVc; ++c)
+    for (int c = 0; c < kVc; ++c)
 #pragma unroll
-        for (int d = 0; d < 4; ++d) f |= nan_bytes(cur.v[c][d]);
-      bad = __any(f != 0);
+      for (int f = 0; f < 2; ++f) {
+        const f16x8 vf = Fp16::widen(vc[c][2 * f], vc[c][2 * f + 1], vscale);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) o[rt][c][f] = Fp16::mfma(vf, p[rt], o[rt][c][f]);
+      }
+    if (more) {
+      load_v<D>(vc, vs, a, next, off);
+      here = next;
+      block = next_block;
+      if (i + 2 * kWaves < i1) {
+        next_block = block_of(s, i + 2 * kWaves);
+        next_page = page_id(a, table, next_block);
+      }
     }
-    if (!bad) {
-#pragma unroll
-      for (int c = 0; c < kVc; ++c)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const f16x8 vf = Fp16::widen(cur.v[c][2 * f], cur.v[c][2 * f + 1], vscale);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-            o[rt][c][f] = Fp16::mfma(vf, p[rt], o[rt][c][f]);
-        }
-    } else {
-#pragma unroll
-      for (int c = 0; c < kVc; ++c)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const unsigned w0 = cur.v[c][2 * f], w1 = cur.v[c][2 * f + 1];
-          // 0x80 flags widened to whole bytes; 0x38 is the code of 1
-          const unsigned n0 = (nan_bytes(w0) >> 7) * 255u, n1 = (nan_bytes(w1) >> 7) * 255u;
-          const f16x8 vf = Fp16::widen(w0 & ~n0, w1 & ~n1, vscale);
-          const f16x8 nf = Fp16::widen(n0 & 0x38383838u, n1 & 0x38383838u, 1.f);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            f16x8 see;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              see[e] = (seen[rt] >> e & 1) ? (_Float16)1.f : (_Float16)0.f;
-            f32x4 x = Fp16::mfma(vf, p[rt], o[rt][c][f]);
-            const f32x4 hit = Fp16::mfma(nf, see, f32x4{0, 0, 0, 0});
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = hit[e] > 0.f ? __builtin_nanf("") : x[e];
-            o[rt][c][f] = x;
-          }
-        }
-    }
-    cur = nxt;
   }
 
   // The four wavefronts' sums, brought to one maximum per row and to the values' own unit.
