@@ -91,6 +91,13 @@ struct Fp16 {
   }
 };
 
+// Three-way maximum of scores as they come from the matrix unit (fmaxf would first quiet each).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // Largest / sum over the four lane groups g of a row (lanes n, n + 16, n + 32, n + 48).
 __device__ __forceinline__ float group_max(float x) {
   const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
@@ -212,7 +219,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
   constexpr int kPiece = D < 128 ? D : 128;  // dims of one pass of the final reduction
   __shared__ float red[kWaves][16][kPiece + 4];
   __shared__ float sm[kWaves][RT * 16], sl[kWaves][RT * 16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // a scalar to the compiler
   const int n = lane & 15, g = lane >> 4;
 
   // Workgroups of one (request, head, split) share its keys and values: their ids are 8 apart, so
@@ -380,11 +388,9 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
     float top[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      float t = sc[rt][0][0];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) t = fmaxf(t, sc[rt][e >> 2][e & 3]);
-      top[rt] = t;
-      move |= fmaf(t, cs, kPShift - mx[rt]) > kPLimit;
+      const f32x4 x = sc[rt][0], y = sc[rt][1];
+      top[rt] = max3(max3(x[0], x[1], x[2]), max3(x[3], y[0], y[1]), max3(y[2], y[3], y[3]));
+      move |= fmaf(top[rt], cs, kPShift - mx[rt]) > kPLimit;
     }
     if (__any(move)) {
 #pragma unroll
