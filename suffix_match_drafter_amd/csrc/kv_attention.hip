@@ -516,11 +516,13 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
   }
 }
 
-// Joins the splits of the rows that had more than one: one wavefront per row.
+// Joins the splits of the rows that had more than one, D / 4 lanes a row; the loads of up to eight
+// splits are in flight together.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chunk_rows) {
-  const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  constexpr int kLanes = D / 4;
+  const int d = (threadIdx.x % kLanes) * 4;
+  const int64_t at = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
   const int all_rows = a.T * a.group;
   const int64_t rows = (int64_t)a.B * a.c.heads * all_rows;
   if (at >= rows) return;
@@ -531,25 +533,24 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chu
   const int active = (s.tiles + a.tiles_per_split - 1) / a.tiles_per_split;
   if (active <= 1) return;
   float m = -__builtin_inff();
+#pragma unroll 8
   for (int i = 0; i < active; ++i) m = fmaxf(m, a.part_lse[i * rows + at]);
-  constexpr int kPer = D / 64;
-  float x[kPer] = {}, l = 0.f;
+  f32x4 x{0, 0, 0, 0};
+  float l = 0.f;
+#pragma unroll 8
   for (int i = 0; i < active; ++i) {
     const float e = a.part_lse[i * rows + at];
+    const f32x4 o = *(const f32x4*)(a.part_o + (i * rows + at) * D + d);
     const float w = e == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(e - m);
     l += w;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      x[k] += w * a.part_o[(i * rows + at) * D + lane * kPer + k];
+    x += w * o;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t out =
       ((int64_t)b * a.T + row / a.group) * a.c.heads * a.group + h * a.group + row % a.group;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const unsigned short v = (unsigned short)T::pack(x[k] * inv, 0.f);
-    ((unsigned short*)a.out)[out * D + lane * kPer + k] = v;
-  }
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  *(u32x2*)((char*)a.out + (out * D + d) * 2) =
+      u32x2{T::pack(x[0] * inv, x[1] * inv), T::pack(x[2] * inv, x[3] * inv)};
 }
 
 int max_row_tiles(int dim) { return dim > 128 ? 2 : 4; }
@@ -558,13 +559,14 @@ int row_tiles(const KvAttentionArgs& a, int dim, int* chunks) {
   const int64_t tiles = ((int64_t)a.T * a.group + 15) / 16;
   const int most = max_row_tiles(dim);
   *chunks = (int)((tiles + most - 1) / most);
+  if (*chunks < 1) *chunks = 1;
   return (int)((tiles + *chunks - 1) / *chunks);
 }
 
 }  // namespace
 
 size_t kv_attention_plan(KvAttentionArgs* a, int dim) {
-  row_tiles(*a, dim, &a->chunks);
+  const int rt = row_tiles(*a, dim, &a->chunks);
   const int64_t cap = (int64_t)a->max_pages * a->c.page_size;
   if (a->window >= cap + a->T) a->window = 0;
   int64_t tiles = (cap + kKvBlock - 1) / kKvBlock;
@@ -573,9 +575,11 @@ size_t kv_attention_plan(KvAttentionArgs* a, int dim) {
                          ((int64_t)a->sinks + kKvBlock - 1) / kKvBlock;
     tiles = seen < tiles ? seen : tiles;
   }
-  // Enough workgroups for the 256 CUs twice over, and at least four tiles a wavefront.
+  // As many splits as find a place on the card at once (a few more would make a second round of
+  // the whole), of at least four tiles a wavefront.
   const int64_t pairs = (int64_t)a->B * a->c.heads * a->chunks;
-  int64_t splits = pairs > 0 ? (512 + pairs - 1) / pairs : 1;
+  const int64_t places = 256 * waves_per_simd(dim, rt);
+  int64_t splits = pairs > 0 ? places / pairs : 1;
   const int64_t most = tiles / (4 * kWaves);
   splits = splits > most ? most : splits;
   splits = splits < 1 ? 1 : splits;
@@ -615,8 +619,8 @@ hipError_t launch_dim(const KvAttentionArgs& a, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t rows = (int64_t)a.B * a.c.heads * a.T * a.group;
-  hipLaunchKernelGGL((kv_join_kernel<T, D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a,
-                     rt * 16);
+  hipLaunchKernelGGL((kv_join_kernel<T, D>), dim3((unsigned)((rows * (D / 4) + 255) / 256)),
+                     dim3(256), 0, st, a, rt * 16);
   return hipGetLastError();
 }
 
