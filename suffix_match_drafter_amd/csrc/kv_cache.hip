@@ -32,118 +32,74 @@ typedef unsigned u32_a2 __attribute__((aligned(2)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
 
-struct Bf16 {};
-struct Fp16 {};
-struct Fp32 {};
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ float half_bits_to_float(unsigned short b) {
-  _Float16 h;
-  __builtin_memcpy(&h, &b, 2);
-  return (float)h;
-}
-__device__ __forceinline__ unsigned short float_to_half_bits(float x) {
-  const _Float16 h = (_Float16)x;
-  unsigned short b;
-  __builtin_memcpy(&b, &h, 2);
-  return b;
-}
-__device__ __forceinline__ unsigned short float_to_bf16_bits(float x) {
-  const __bf16 h = (__bf16)x;
-  unsigned short b;
-  __builtin_memcpy(&b, &h, 2);
-  return b;
-}
-
-template <typename T> struct Elem;
-template <> struct Elem<Bf16> {
+// Elements travel in words: a pair of 16-bit ones or one of 32 bits.
+//   codes: two words' (16-bit) or four words' (32-bit) values over a power of two as four codes,
+//   without saturation; widen: the reverse, half `hi` of a word of codes; floats: as fp32.
+struct Bf16 {
   static constexpr int kBytes = 2;
-  static __device__ float lo(unsigned w) { return __uint_as_float(w << 16); }
-  static __device__ float hi(unsigned w) { return __uint_as_float(w & 0xffff0000u); }
-  static __device__ unsigned pack(float a, float b) {
-    return float_to_bf16_bits(a) | ((unsigned)float_to_bf16_bits(b) << 16);
+  static constexpr unsigned kInf = 0x7f80;
+  static __device__ float value(unsigned bits) { return __uint_as_float(bits << 16); }
+  static __device__ unsigned codes(const unsigned* w, float scale) {
+    i16x2 r{0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, w[0]), scale,
+                                                  false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, w[1]), scale,
+                                                  true);
+    return __builtin_bit_cast(unsigned, r);
+  }
+  static __device__ f32x2 floats(unsigned w) {
+    return f32x2{__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+  }
+  template <bool kHi> static __device__ unsigned widen(unsigned codes, float scale) {
+    return __builtin_bit_cast(unsigned,
+                              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, kHi));
   }
 };
-template <> struct Elem<Fp16> {
+struct Fp16 {
   static constexpr int kBytes = 2;
-  static __device__ float lo(unsigned w) { return half_bits_to_float((unsigned short)w); }
-  static __device__ float hi(unsigned w) { return half_bits_to_float((unsigned short)(w >> 16)); }
-  static __device__ unsigned pack(float a, float b) {
-    return float_to_half_bits(a) | ((unsigned)float_to_half_bits(b) << 16);
+  static constexpr unsigned kInf = 0x7c00;
+  static __device__ float value(unsigned bits) {
+    return (float)__builtin_bit_cast(_Float16, (unsigned short)bits);
+  }
+  static __device__ unsigned codes(const unsigned* w, float scale) {
+    i16x2 r{0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(f16x2, w[0]), scale,
+                                                 false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(f16x2, w[1]), scale, true);
+    return __builtin_bit_cast(unsigned, r);
+  }
+  static __device__ f32x2 floats(unsigned w) {
+    const f16x2 h = __builtin_bit_cast(f16x2, w);
+    return f32x2{(float)h[0], (float)h[1]};
+  }
+  // by way of fp32: a value may be outside fp16's normal range
+  template <bool kHi> static __device__ unsigned widen(unsigned codes, float scale) {
+    const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8(codes, kHi);
+    return __builtin_bit_cast(unsigned, f16x2{(_Float16)(x[0] * scale), (_Float16)(x[1] * scale)});
   }
 };
-template <> struct Elem<Fp32> {
+struct Fp32 {
   static constexpr int kBytes = 4;
+  static constexpr unsigned kInf = 0x7f800000;
+  static __device__ float value(unsigned bits) { return __uint_as_float(bits); }
+  static __device__ unsigned codes(const unsigned* w, float scale) {
+    i16x2 r{0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(w[0]), __uint_as_float(w[1]),
+                                                 scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(w[2]), __uint_as_float(w[3]),
+                                                 scale, true);
+    return __builtin_bit_cast(unsigned, r);
+  }
 };
 
-// 16 consecutive elements as floats.
 template <typename T>
-__device__ __forceinline__ void load16(const char* p, float (&x)[16]) {
-  if constexpr (Elem<T>::kBytes == 2) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const u32x4 w = *(const u32x4_a2*)(p + 16 * i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[8 * i + 2 * e] = Elem<T>::lo(w[e]);
-        x[8 * i + 2 * e + 1] = Elem<T>::hi(w[e]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x4 w = *(const u32x4_a4*)(p + 16 * i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[4 * i + e] = __uint_as_float(w[e]);
-    }
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void store16(char* p, const float (&x)[16]) {
-  if constexpr (Elem<T>::kBytes == 2) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      u32x4 w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = Elem<T>::pack(x[8 * i + 2 * e], x[8 * i + 2 * e + 1]);
-      *(u32x4_a2*)(p + 16 * i) = w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u32x4 w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(x[4 * i + e]);
-      *(u32x4_a4*)(p + 16 * i) = w;
-    }
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void load2(const char* p, float& a, float& b) {
-  if constexpr (Elem<T>::kBytes == 2) {
-    const unsigned w = *(const u32_a2*)p;
-    a = Elem<T>::lo(w);
-    b = Elem<T>::hi(w);
-  } else {
-    const u32x2 w = *(const u32x2_a4*)p;
-    a = __uint_as_float(w[0]);
-    b = __uint_as_float(w[1]);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void store2(char* p, float a, float b) {
-  if constexpr (Elem<T>::kBytes == 2) {
-    *(u32_a2*)p = Elem<T>::pack(a, b);
-  } else {
-    u32x2 w;
-    w[0] = __float_as_uint(a);
-    w[1] = __float_as_uint(b);
-    *(u32x2_a4*)p = w;
-  }
-}
+constexpr int kWords = T::kBytes * 4;  // of 16 elements
 
 // Saturates to e4m3's range; a NaN stays one.
 __device__ __forceinline__ float saturate(float y) {
@@ -151,19 +107,61 @@ __device__ __forceinline__ float saturate(float y) {
   return y < -448.f ? -448.f : y;
 }
 
-// Four codes of four scaled values.
+// Four codes of four values that may not fit.
 __device__ __forceinline__ unsigned codes4(float a, float b, float c, float d) {
   unsigned w = __builtin_amdgcn_cvt_pk_fp8_f32(saturate(a), saturate(b), 0, false);
   return __builtin_amdgcn_cvt_pk_fp8_f32(saturate(c), saturate(d), w, true);
 }
+template <typename T>
+__device__ __forceinline__ unsigned codes_saturated(const unsigned* w, float inv) {
+  if constexpr (T::kBytes == 2) {
+    const f32x2 a = T::floats(w[0]), b = T::floats(w[1]);
+    return codes4(a[0] * inv, a[1] * inv, b[0] * inv, b[1] * inv);
+  } else {
+    return codes4(__uint_as_float(w[0]) * inv, __uint_as_float(w[1]) * inv,
+                  __uint_as_float(w[2]) * inv, __uint_as_float(w[3]) * inv);
+  }
+}
 
-__device__ __forceinline__ void values4(unsigned w, float (&x)[4]) {
-  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
-  const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
-  x[0] = lo[0];
-  x[1] = lo[1];
-  x[2] = hi[0];
-  x[3] = hi[1];
+// Largest magnitude, as bits, of m and the element(s) of w: with the sign cleared a float's bits
+// order as its value does, infinity and NaN last.
+template <typename T>
+__device__ __forceinline__ unsigned max_bits(unsigned m, unsigned w) {
+  if constexpr (T::kBytes == 2) {
+    const u16x2 a = __builtin_bit_cast(u16x2, m);
+    const u16x2 b = __builtin_bit_cast(u16x2, w & 0x7fff7fffu);
+    return __builtin_bit_cast(unsigned, __builtin_elementwise_max(a, b));
+  } else {
+    w &= 0x7fffffffu;
+    return m > w ? m : w;
+  }
+}
+// The same leaving infinities and NaN out.
+template <typename T>
+__device__ __forceinline__ unsigned max_bits_finite(unsigned m, unsigned w) {
+  if constexpr (T::kBytes == 2) {
+    unsigned lo = w & 0x7fff, hi = w >> 16 & 0x7fff;
+    lo = lo >= T::kInf ? 0 : lo;
+    hi = hi >= T::kInf ? 0 : hi;
+    return max_bits<T>(m, lo | hi << 16);
+  } else {
+    w &= 0x7fffffffu;
+    return max_bits<T>(m, w >= T::kInf ? 0 : w);
+  }
+}
+template <typename T>
+__device__ __forceinline__ unsigned wave_max_bits(unsigned m) {
+  if constexpr (T::kBytes == 2) {
+    const unsigned hi = m >> 16;
+    m &= 0xffff;
+    m = m > hi ? m : hi;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const unsigned x = __shfl_xor(m, o);
+    m = m > x ? m : x;
+  }
+  return __builtin_amdgcn_readfirstlane(m);
 }
 
 // Least e in range with m <= 448 * 2^e.  m = f * 2^x with f in [1, 2): 448 = 1.75 * 2^8.
@@ -172,12 +170,6 @@ __device__ __forceinline__ int needed_exp(float m) {
   int e = ((bits >> 23) & 255) - 127 - 8;
   if ((bits & 0x7fffff) > 0x600000) ++e;
   return e < kKvMinExp ? kKvMinExp : (e > kKvMaxExp ? kKvMaxExp : e);
-}
-
-__device__ __forceinline__ float wave_max(float m) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  return m;
 }
 
 // The element map of one 32-token block for lane (r, g): 16-byte chunk c of the block, element e.
@@ -197,13 +189,32 @@ struct Map {
   }
 };
 
+// A chunk's 16 elements in the codes' order from the words as loaded, and back.  Keys lie in that
+// order already; for values `raw` holds token e's (= (j, i)) dim pair: in 16 bits one word each,
+// in 32 bits words e and 8 + e.
+template <typename T, bool kVal>
+__device__ __forceinline__ void to_order(const unsigned (&raw)[kWords<T>],
+                                         unsigned (&w)[kWords<T>]) {
+  if constexpr (kVal && T::kBytes == 2) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      w[p] = __builtin_amdgcn_perm(raw[2 * (p & 3) + 1], raw[2 * (p & 3)],
+                                   p < 4 ? 0x05040100u : 0x07060302u);
+  } else {
+#pragma unroll
+    for (int p = 0; p < kWords<T>; ++p) w[p] = raw[p];
+  }
+}
+
 // One wavefront per (request, 32-token block, tensor, head).  The block's values stay in
-// registers between the maximum and the rounding, so the input is read once: the kernel is
-// bounded by that traffic (prompts), or by one dependent chain of loads (a few tokens).
+// registers between the maximum and the rounding, so the input is read once and the kernel is
+// bounded by that traffic (prompts: 1.5 vector instructions an element in 16 bits) or by one
+// dependent chain of loads (a few tokens: counts, page id, then inputs, old codes and scale
+// together).
 template <typename T, int D, bool kVal>
 __device__ void write_block(const KvMoveArgs& a, int b, int h, int block, int start, int count,
                             int lane) {
-  constexpr int kChunks = Map<D, kVal>::kChunks, kB = Elem<T>::kBytes;
+  constexpr int kChunks = Map<D, kVal>::kChunks, kB = T::kBytes, kW = kWords<T>;
   const KvCache& kc = a.c;
   const int per_page = kc.page_size / kKvBlock;
   const int pi = kv_page_of(kc, block);
@@ -218,169 +229,302 @@ __device__ void write_block(const KvMoveArgs& a, int b, int h, int block, int st
   const char* in = (const char*)(kVal ? a.v : a.k) + (b * s.batch + h * s.head) * kB;
   const int r = lane >> 2, g = lane & 3;
   const int rel = block * kKvBlock - start;  // input index of the block's first token
+  const bool full = rel >= 0 && rel + kKvBlock <= count, live_before = rel < 0;
   auto is_new = [&](int tok) { return rel + tok >= 0 && rel + tok < count; };
-  float x[kChunks][16];
-  float m = 0.f;
+  auto source = [&](int tok) {  // a row that can be read: one that is not new is cleared below
+    const int j = rel + tok;
+    return in + (int64_t)(j < 0 ? 0 : (j < count ? j : count - 1)) * s.token * kB;
+  };
+
+  // Old bytes: a 16-byte chunk of values mixes eight tokens and is read before it is written; one of
+  // keys is a single token's and is read only when it moves to another scale.
+  u32x4 old[kChunks];
+  float old_scale = 0.f;
+  if (kVal && !full)
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      old[c] = *(const u32x4*)(codes + Map<D, kVal>::offset(kc, c, r, g, tok0));
+  if (live_before) old_scale = *scale;
+  // the lane's eight tokens of values, the same in every chunk: their rows, which of them are new
+  const char* row[8];
+  unsigned fresh[8];
+  if constexpr (kVal)
+#pragma unroll
+    for (int ji = 0; ji < 8; ++ji) {
+      const int tok = Map<D, true>::token(0, ji, r, g);
+      row[ji] = source(tok) + 2 * r * kB;
+      fresh[ji] = full || is_new(tok) ? ~0u : 0;
+    }
+  unsigned w[kChunks][kW];
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
+    unsigned raw[kW];
     if constexpr (kVal) {
 #pragma unroll
       for (int ji = 0; ji < 8; ++ji) {
-        const int tok = Map<D, true>::token(c, ji, r, g);
-        x[c][ji] = x[c][8 + ji] = 0.f;
-        if (is_new(tok))
-          load2<T>(in + ((int64_t)(rel + tok) * s.token + 32 * c + 2 * r) * kB, x[c][ji],
-                   x[c][8 + ji]);
+        if constexpr (kB == 2) {
+          raw[ji] = *(const u32_a2*)(row[ji] + 32 * c * kB);
+        } else {
+          const u32x2 x = *(const u32x2_a4*)(row[ji] + 32 * c * kB);
+          raw[ji] = x[0];
+          raw[8 + ji] = x[1];
+        }
       }
+      if (!full)
+#pragma unroll
+        for (int e = 0; e < kW; ++e) raw[e] &= fresh[e & 7];
     } else {
       const int tok = Map<D, false>::token(c, 0, r, g);
+      const char* p = source(tok) + (64 * (c % (D / 64)) + 16 * g) * kB;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[c][e] = 0.f;
-      if (is_new(tok))
-        load16<T>(in + ((int64_t)(rel + tok) * s.token + 64 * (c % (D / 64)) + 16 * g) * kB,
-                  x[c]);
+      for (int i = 0; i < kW / 4; ++i) {
+        u32x4 x;
+        if constexpr (kB == 2)
+          x = *(const u32x4_a2*)(p + 16 * i);
+        else
+          x = *(const u32x4_a4*)(p + 16 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) raw[4 * i + e] = full || is_new(tok) ? x[e] : 0;
+      }
     }
+    to_order<T, kVal>(raw, w[c]);
   }
+  unsigned mb = 0;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float ax = fabsf(x[c][e]);
-      m = ax < __builtin_inff() ? fmaxf(m, ax) : m;  // NaN and infinities take no part
-    }
-  m = wave_max(m);
-  const bool live_before = rel < 0;
+    for (int e = 0; e < kW; ++e) mb = max_bits<T>(mb, w[c][e]);
+  mb = wave_max_bits<T>(mb);
+  const bool special = mb >= T::kInf;  // an infinity or a NaN: the maximum is over the others
+  if (special) {
+    mb = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int e = 0; e < kW; ++e) mb = max_bits_finite<T>(mb, w[c][e]);
+    mb = wave_max_bits<T>(mb);
+  }
+  const float m = T::value(mb);
   int e_new = needed_exp(m), e_old = e_new;
   if (live_before) {
-    e_old = kv_exp_of(*scale);
+    e_old = kv_exp_of(old_scale);
     e_new = e_old > e_new ? e_old : e_new;
   }
-  const float inv = kv_pow2(-e_new), move = kv_pow2(e_old - e_new);
-  const bool full = rel >= 0 && rel + kKvBlock <= count, moved = e_old != e_new;
+  const float sc = kv_pow2(e_new), inv = kv_pow2(-e_new), move = kv_pow2(e_old - e_new);
+  const bool moved = e_old != e_new;
+  const bool fits = !special && m <= 448.f * sc;
+  if (!kVal && moved)
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      old[c] = *(const u32x4*)(codes + Map<D, kVal>::offset(kc, c, r, g, tok0));
+  // Bytes to take from the new codes and, when the scale moved, from the old ones' new codes: of
+  // values' words 4 f + j by j (tokens 16 j + 4 g + i); of keys all or none.
+  unsigned take[2], carry[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    take[j] = carry[j] = 0;
+    if constexpr (kVal)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        take[j] |= fresh[4 * j + i] & 0xffu << (8 * i);
+        if (moved && rel + Map<D, true>::token(0, 4 * j + i, r, g) < 0) carry[j] |= 0xffu << (8 * i);
+      }
+  }
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
     u32x4* at = (u32x4*)(codes + Map<D, kVal>::offset(kc, c, r, g, tok0));
-    u32x4 w;
+    u32x4 q;
+    if (fits) {
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
-      w[d] = codes4(x[c][4 * d] * inv, x[c][4 * d + 1] * inv, x[c][4 * d + 2] * inv,
-                    x[c][4 * d + 3] * inv);
+      for (int d = 0; d < 4; ++d) q[d] = T::codes(&w[c][d * kW / 4], sc);
+    } else {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) q[d] = codes_saturated<T>(&w[c][d * kW / 4], inv);
+    }
     if (full) {
-      *at = w;
+      *at = q;
       continue;
     }
-    // part of the block: merge with the bytes that are there
-    unsigned fresh = 0, live = 0;  // per element of the chunk
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int tok = Map<D, kVal>::token(c, e, r, g);
-      if (is_new(tok)) fresh |= 1u << e;
-      if (rel + tok < 0 && moved) live |= 1u << e;
+    if constexpr (!kVal) {
+      const int tok = Map<D, false>::token(c, 0, r, g);
+      take[0] = take[1] = is_new(tok) ? ~0u : 0;
+      carry[0] = carry[1] = moved && rel + tok < 0 ? ~0u : 0;
     }
-    if (!(fresh | live)) continue;
-    const u32x4 old = *at;
+    if (moved) {
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      float y[4];
-      values4(old[d], y);
-      const unsigned q = codes4(y[0] * move, y[1] * move, y[2] * move, y[3] * move);
-      unsigned fm = 0, lm = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (fresh >> (4 * d + i) & 1) fm |= 0xffu << (8 * i);
-        if (live >> (4 * d + i) & 1) lm |= 0xffu << (8 * i);
+      for (int d = 0; d < 4; ++d) {
+        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(old[c][d], false);
+        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(old[c][d], true);
+        const unsigned y = codes4(lo[0] * move, lo[1] * move, hi[0] * move, hi[1] * move);
+        old[c][d] = (old[c][d] & ~carry[d & 1]) | (y & carry[d & 1]);
       }
-      w[d] = (w[d] & fm) | (q & lm) | (old[d] & ~(fm | lm));
     }
-    *at = w;
+    if (kVal || moved)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) q[d] = (q[d] & take[d & 1]) | (old[c][d] & ~take[d & 1]);
+    if (take[0] | take[1] | carry[0] | carry[1]) *at = q;
   }
-  if (lane == 0 && (!live_before || moved)) *scale = kv_pow2(e_new);
+  if (lane == 0 && (!live_before || moved)) *scale = sc;
 }
 
-// Unit u of the grid: head fastest (a token's heads are adjacent in the input), then tensor,
-// block and request.
+// Unit of the grid for one wavefront: head fastest (a token's heads are adjacent in the input),
+// then tensor, block and request.
+struct Unit {
+  int b, h, block;
+  bool val;
+};
+__device__ __forceinline__ Unit unit_of(int heads, int nb) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // a scalar to the compiler
+  unsigned u = blockIdx.x * kWavesPerGroup + wave;  // below 2^31 + 4
+  Unit r;
+  r.h = u % heads;
+  u /= heads;
+  r.val = u & 1;
+  u >>= 1;
+  r.block = u % nb;
+  r.b = u / nb;
+  return r;
+}
+
 template <typename T, int D>
 __global__ __launch_bounds__(64 * kWavesPerGroup) void kv_write_kernel(KvMoveArgs a, int nb) {
   const int lane = threadIdx.x & 63;
-  int64_t u = (int64_t)blockIdx.x * kWavesPerGroup + (threadIdx.x >> 6);
-  const int h = (int)(u % a.c.heads);
-  u /= a.c.heads;
-  const bool val = u & 1;
-  u >>= 1;
-  const int b = (int)(u / nb);
-  if (b >= a.B) return;
-  const int start = a.start[b];
-  int count = a.count ? a.count[b] : a.T;
+  const Unit u = unit_of(a.c.heads, nb);
+  if (u.b >= a.B) return;
+  const int start = a.start[u.b];
+  int count = a.count ? a.count[u.b] : a.T;
   count = count > a.T ? a.T : count;
   if (start < 0 || count <= 0) return;
-  const int64_t blk = (int64_t)start / kKvBlock + u % nb;
+  const int64_t blk = (int64_t)start / kKvBlock + u.block;
   if (blk * kKvBlock >= (int64_t)start + count || blk >= (1 << 26)) return;
-  const int block = (int)blk;
-  if (val)
-    write_block<T, D, true>(a, b, h, block, start, count, lane);
+  if (u.val)
+    write_block<T, D, true>(a, u.b, u.h, (int)blk, start, count, lane);
   else
-    write_block<T, D, false>(a, b, h, block, start, count, lane);
+    write_block<T, D, false>(a, u.b, u.h, (int)blk, start, count, lane);
 }
 
+// LDS of one wavefront of the read: 32 rows of up to 256 bytes, 16 apart so that the lanes' words of
+// four rows fall on different banks.
+template <typename T, int D>
+struct ReadLds {
+  static constexpr int kDims = D * T::kBytes < 256 ? D : 256 / T::kBytes;
+  static constexpr int kRow = kDims * T::kBytes + 16;
+  static constexpr int kVecs = kKvBlock * kRow / 16;
+};
+
 // The reverse: one wavefront per (request, 32-token block, tensor, head), zeros for rows past the
-// count or on an unmapped page.
+// count or on an unmapped page.  Bounded by the traffic, which is mostly the result's.
 template <typename T, int D, bool kVal>
 __device__ void read_block(const KvMoveArgs& a, int b, int h, int64_t block, int start, int count,
-                           int lane) {
-  constexpr int kChunks = Map<D, kVal>::kChunks, kB = Elem<T>::kBytes;
+                           int lane, u32x4* turn) {
+  constexpr int kChunks = Map<D, kVal>::kChunks, kB = T::kBytes;
   const KvCache& kc = a.c;
   const int per_page = kc.page_size / kKvBlock;
   const int64_t rel = block * kKvBlock - start;
   const int r = lane >> 2, g = lane & 3;
   const KvStrides& s = kVal ? a.vs : a.ks;
   char* out = (char*)(kVal ? a.v : a.k) + (b * s.batch + h * s.head) * kB;
-  bool mapped = false;
-  const uint8_t* codes = nullptr;
-  float scale = 0.f;
-  int tok0 = 0;
+  u32x4 w[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) w[c] = u32x4{0, 0, 0, 0};
+  float scale = 1.f;
   const int pi = block < (1 << 26) ? kv_page_of(kc, (int)block) : a.max_pages;
   if (rel < count && pi < a.max_pages) {
     const int page = a.page_table[(int64_t)b * a.max_pages + pi];
     if (page >= 0 && page < kc.num_pages) {
-      mapped = true;
       const int sub = (int)block - pi * per_page;
       const int64_t ph = (int64_t)page * kc.heads + h;
-      tok0 = sub * kKvBlock;
-      codes = (kVal ? kc.v : kc.k) + ph * kc.page_size * D;
+      const int tok0 = sub * kKvBlock;
+      const uint8_t* codes = (kVal ? kc.v : kc.k) + ph * kc.page_size * D;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        w[c] = *(const u32x4*)(codes + Map<D, kVal>::offset(kc, c, r, g, tok0));
       scale = kv_pow2(kv_exp_of((kVal ? kc.v_scale : kc.k_scale)[ph * per_page + sub]));
     }
   }
-  u32x4 w[kChunks];
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c)
-    w[c] = mapped ? *(const u32x4*)(codes + Map<D, kVal>::offset(kc, c, r, g, tok0))
-                  : u32x4{0, 0, 0, 0};
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
-    float x[16];
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      float y[4];
-      values4(w[c][d], y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[4 * d + i] = y[i] * scale;
-    }
     if constexpr (kVal) {
+      // A lane has two dims of eight tokens: the block turns in LDS, a piece of whole rows at a
+      // time, and goes out 16 bytes a lane.
+      constexpr int kPiece = ReadLds<T, D>::kDims, kRow = ReadLds<T, D>::kRow;
+      char* lds = (char*)turn;
 #pragma unroll
-      for (int ji = 0; ji < 8; ++ji) {
-        const int64_t j = rel + Map<D, true>::token(c, ji, r, g);
-        const bool in = j < count;
-        if (j >= 0 && j < a.T)
-          store2<T>(out + (j * s.token + 32 * c + 2 * r) * kB, in ? x[ji] : 0.f,
-                    in ? x[8 + ji] : 0.f);
+      for (int q = 0; q < 4; ++q) {  // tokens e = 2 q, 2 q + 1
+        u32x2 even, odd;             // their words
+        const unsigned lo = w[c][q >> 1], hi = w[c][2 + (q >> 1)];  // f = 0, 1
+        if constexpr (kB == 2) {
+          const unsigned x = q & 1 ? T::template widen<true>(lo, scale)
+                                   : T::template widen<false>(lo, scale);
+          const unsigned y = q & 1 ? T::template widen<true>(hi, scale)
+                                   : T::template widen<false>(hi, scale);
+          even[0] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+          odd[0] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        } else {
+          const f32x2 x = q & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(lo, true)
+                                : __builtin_amdgcn_cvt_pk_f32_fp8(lo, false);
+          const f32x2 y = q & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(hi, true)
+                                : __builtin_amdgcn_cvt_pk_f32_fp8(hi, false);
+          even = u32x2{__float_as_uint(x[0] * scale), __float_as_uint(y[0] * scale)};
+          odd = u32x2{__float_as_uint(x[1] * scale), __float_as_uint(y[1] * scale)};
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int tok = Map<D, true>::token(c, 2 * q + k, r, g);
+          char* p = lds + tok * kRow + (32 * c % kPiece + 2 * r) * kB;
+          if constexpr (kB == 2)
+            *(unsigned*)p = k ? odd[0] : even[0];
+          else
+            *(u32x2*)p = k ? odd : even;
+        }
+      }
+      if ((c + 1) * 32 % kPiece == 0) {
+        // one wavefront's own LDS: its accesses stay in order, the compiler must keep them so
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        constexpr int kLanes = kPiece * kB / 16;  // of a row
+#pragma unroll
+        for (int t = 0; t < kKvBlock; t += 64 / kLanes) {
+          const int tok = t + lane / kLanes, at = lane % kLanes * 16;
+          const int64_t j = rel + tok;
+          u32x4 v = *(const u32x4*)(lds + tok * kRow + at);
+          v = j < count ? v : u32x4{0, 0, 0, 0};
+          char* p = out + (j * s.token + 32 * (c + 1) - kPiece) * kB + at;
+          if (j >= 0 && j < a.T) {
+            if constexpr (kB == 2)
+              *(u32x4_a2*)p = v;
+            else
+              *(u32x4_a4*)p = v;
+          }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
     } else {
       const int64_t j = rel + Map<D, false>::token(c, 0, r, g);
-      if (j >= count)
+      char* p = out + (j * s.token + 64 * (c % (D / 64)) + 16 * g) * kB;
+      if (j < 0 || j >= a.T) continue;
+      const bool live = j < count;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0.f;
-      if (j >= 0 && j < a.T)
-        store16<T>(out + (j * s.token + 64 * (c % (D / 64)) + 16 * g) * kB, x);
+      for (int i = 0; i < kB; ++i) {
+        u32x4 v;
+        if constexpr (kB == 2) {
+          v = u32x4{T::template widen<false>(w[c][2 * i], scale),
+                    T::template widen<true>(w[c][2 * i], scale),
+                    T::template widen<false>(w[c][2 * i + 1], scale),
+                    T::template widen<true>(w[c][2 * i + 1], scale)};
+        } else {
+          const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8(w[c][i], false);
+          const f32x2 y = __builtin_amdgcn_cvt_pk_f32_fp8(w[c][i], true);
+          v = u32x4{__float_as_uint(x[0] * scale), __float_as_uint(x[1] * scale),
+                    __float_as_uint(y[0] * scale), __float_as_uint(y[1] * scale)};
+        }
+        v = live ? v : u32x4{0, 0, 0, 0};
+        if constexpr (kB == 2)
+          *(u32x4_a2*)(p + 16 * i) = v;
+        else
+          *(u32x4_a4*)(p + 16 * i) = v;
+      }
     }
   }
 }
@@ -388,23 +532,20 @@ __device__ void read_block(const KvMoveArgs& a, int b, int h, int64_t block, int
 template <typename T, int D>
 __global__ __launch_bounds__(64 * kWavesPerGroup) void kv_read_kernel(KvMoveArgs a, int nb) {
   const int lane = threadIdx.x & 63;
-  int64_t u = (int64_t)blockIdx.x * kWavesPerGroup + (threadIdx.x >> 6);
-  const int h = (int)(u % a.c.heads);
-  u /= a.c.heads;
-  const bool val = u & 1;
-  u >>= 1;
-  const int b = (int)(u / nb);
-  if (b >= a.B) return;
-  int start = a.start ? a.start[b] : 0;
-  int count = a.count ? a.count[b] : a.T;
+  __shared__ u32x4 turn[kWavesPerGroup][ReadLds<T, D>::kVecs];
+  const Unit u = unit_of(a.c.heads, nb);
+  if (u.b >= a.B) return;
+  u32x4* mine = turn[threadIdx.x >> 6];
+  int start = a.start[u.b];
+  int count = a.count ? a.count[u.b] : a.T;
   count = count > a.T ? a.T : count;
   if (start < 0) start = count = 0;  // no such token: zeros
-  const int64_t block = (int64_t)start / kKvBlock + u % nb;
+  const int64_t block = (int64_t)start / kKvBlock + u.block;
   if (block * kKvBlock >= (int64_t)start + a.T) return;
-  if (val)
-    read_block<T, D, true>(a, b, h, block, start, count, lane);
+  if (u.val)
+    read_block<T, D, true>(a, u.b, u.h, block, start, count, lane, mine);
   else
-    read_block<T, D, false>(a, b, h, block, start, count, lane);
+    read_block<T, D, false>(a, u.b, u.h, block, start, count, lane, mine);
 }
 
 // Blocks that T tokens can touch, whatever the start.
