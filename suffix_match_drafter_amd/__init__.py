@@ -521,13 +521,21 @@ def build_suffix_array(text: torch.Tensor, stream=None) -> torch.Tensor:
 
 
 # ------------------------------------------------------------------ the verification step
-def _on(device):
+# These calls are short (a few microseconds on the device), so their checks are written to be
+# cheap: device indexes instead of device objects, addresses as plain integers.
+def _on(index):
     """The kernels run on the current device: the tensors have to be there."""
-    if device.type != "cuda":
+    if index < 0:
         raise TypeError("tensors must be on a CUDA/HIP device")
     cur = torch.cuda.current_device()
-    if device.index is not None and device.index != cur:
-        raise ValueError(f"tensors are on {device}, the current device is {cur}")
+    if index != cur:
+        raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{cur}")
+
+
+def _raw_stream(stream, index):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _empty(shape, dtype, device, stream):
@@ -542,31 +550,30 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _vec(t, name, n, dtype, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
-        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous 1-D tensor of {n} entries")
-    return t
+def _array(t, name, shape, dtype, index):
+    """A contiguous tensor of this shape, type and device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{index}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got "
+                         f"{tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _heads(t, name, heads, dim, device=None):
+def _heads(t, name, heads, dim, index):
     """A [B, T, heads, dim] tensor of any batch, token and head strides."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES or not t.is_cuda or \
-            (device is not None and t.device != device):
-        raise TypeError(f"{name} must be a bfloat16, float16 or float32 CUDA/HIP tensor" +
-                        (f" on {device}" if device is not None else ""))
-    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != dim:
-        raise ValueError(f"{name} must be [B, T, {heads}, {dim}], got {tuple(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES or t.get_device() != index:
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor on cuda:{index}")
+    shape = t.shape
+    if len(shape) != 4 or shape[2] != heads or shape[3] != dim:
+        raise ValueError(f"{name} must be [B, T, {heads}, {dim}], got {tuple(shape)}")
     if t.stride(3) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t
+    return shape
 
 
 def _strides(t):
-    if t.is_contiguous():
-        return None
-    return (_I64 * 3)(t.stride(0), t.stride(1), t.stride(2))
+    return None if t.is_contiguous() else (_I64 * 3)(t.stride(0), t.stride(1), t.stride(2))
 
 
 class KVCache:
@@ -603,10 +610,12 @@ class KVCache:
         self.num_pages, self.page_size = int(num_pages), int(page_size)
         self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
         self.device = self.k.device
+        self._index = self.k.get_device()
         self._c = _KvCache(self.num_pages, self.page_size, self.kv_heads, self.head_dim,
                            self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
                            self.v_scale.data_ptr())
-        self._p = ctypes.byref(self._c)
+        self._p = ctypes.addressof(self._c)
+        self._bytes = {}  # workspace sizes of the attention's shapes
 
     @staticmethod
     def shapes(num_pages, page_size, kv_heads, head_dim):
@@ -617,49 +626,50 @@ class KVCache:
                             4)), s, s)
 
     def _table(self, page_table, B):
-        t = _i32(page_table, "page_table", 2)
-        if t.shape[0] != B or t.device != self.device:
-            raise ValueError(f"page_table must be [{B}, pages] on {self.device}")
-        return t
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table must be [B, pages]")
+        pages = page_table.shape[1]
+        return _array(page_table, "page_table", (B, pages), torch.int32, self._index), pages
 
     def write(self, k, v, page_table, start, count=None, stream=None):
         """sfx_kv_write: quantise k, v [B, T, kv_heads, head_dim] into positions start[b] .."""
-        _on(self.device)
-        k = _heads(k, "k", self.kv_heads, self.head_dim, self.device)
-        v = _heads(v, "v", self.kv_heads, self.head_dim, self.device)
-        if v.shape != k.shape or v.dtype != k.dtype:
+        i = self._index
+        _on(i)
+        shape = _heads(k, "k", self.kv_heads, self.head_dim, i)
+        if _heads(v, "v", self.kv_heads, self.head_dim, i) != shape or v.dtype is not k.dtype:
             raise ValueError("k and v differ in shape or type")
-        B, T = k.shape[:2]
-        tab = self._table(page_table, B)
-        st = _vec(start, "start", B, torch.int32, self.device)
-        ct = None if count is None else _vec(count, "count", B, torch.int32, self.device)
-        _check(load().sfx_kv_write(self._p, B, T, tab.shape[1], _ptr(tab), _ptr(st), _ptr(ct),
-                                   _ptr(k), _strides(k), _ptr(v), _strides(v),
-                                   _TYPES[k.dtype], _stream(stream)))
+        B = shape[0]
+        tab, pages = self._table(page_table, B)
+        st = _array(start, "start", (B,), torch.int32, i)
+        ct = None if count is None else _array(count, "count", (B,), torch.int32, i)
+        _check(load().sfx_kv_write(self._p, B, shape[1], pages, tab, st, ct, k.data_ptr(),
+                                   _strides(k), v.data_ptr(), _strides(v), _TYPES[k.dtype],
+                                   _raw_stream(stream, i)))
 
     def read(self, page_table, start, count, T, dtype=torch.bfloat16, k=None, v=None,
              stream=None):
         """sfx_kv_read: positions start[b] .. start[b] + T - 1 as k, v [B, T, kv_heads,
         head_dim]; zero past count[b]."""
-        _on(self.device)
+        i = self._index
+        _on(i)
         if dtype not in _TYPES:
             raise TypeError("dtype must be bfloat16, float16 or float32")
         B = page_table.shape[0]
-        tab = self._table(page_table, B)
-        st = _vec(start, "start", B, torch.int32, self.device)
-        ct = None if count is None else _vec(count, "count", B, torch.int32, self.device)
+        tab, pages = self._table(page_table, B)
+        st = _array(start, "start", (B,), torch.int32, i)
+        ct = None if count is None else _array(count, "count", (B,), torch.int32, i)
         shape = (B, int(T), self.kv_heads, self.head_dim)
         if k is None:
             k = _empty(shape, dtype, self.device, stream)
+        elif _heads(k, "k", self.kv_heads, self.head_dim, i) != shape or k.dtype is not dtype:
+            raise ValueError(f"k must be {shape} of {dtype}")
         if v is None:
             v = _empty(shape, dtype, self.device, stream)
-        k = _heads(k, "k", self.kv_heads, self.head_dim, self.device)
-        v = _heads(v, "v", self.kv_heads, self.head_dim, self.device)
-        if k.shape != shape or v.shape != shape or k.dtype != dtype or v.dtype != dtype:
-            raise ValueError(f"k and v must be {shape} of {dtype}")
-        _check(load().sfx_kv_read(self._p, B, int(T), tab.shape[1], _ptr(tab), _ptr(st),
-                                  _ptr(ct), _ptr(k), _strides(k), _ptr(v), _strides(v),
-                                  _TYPES[dtype], _stream(stream)))
+        elif _heads(v, "v", self.kv_heads, self.head_dim, i) != shape or v.dtype is not dtype:
+            raise ValueError(f"v must be {shape} of {dtype}")
+        _check(load().sfx_kv_read(self._p, B, shape[1], pages, tab, st, ct, k.data_ptr(),
+                                  _strides(k), v.data_ptr(), _strides(v), _TYPES[dtype],
+                                  _raw_stream(stream, i)))
         return k, v
 
     def attend(self, q, page_table, seq_lens, q_lens=None, scale=None, window=0, sinks=0,
@@ -667,32 +677,39 @@ class KVCache:
         """sfx_kv_attention: rows t < q_lens[b] of q [B, T, heads, head_dim] (bf16 or fp16), the
         newest tokens of seq_lens[b] cached ones, attend causally over the cache; window and
         sinks restrict what they see (0: everything).  scale defaults to head_dim ** -0.5."""
-        _on(self.device)
+        i = self._index
+        _on(i)
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError("q must be [B, T, heads, head_dim]")
-        B, T, H = q.shape[:3]
-        q = _heads(q, "q", H, self.head_dim, self.device)
-        if q.dtype == torch.float32:
+        B, T, H, _ = shape = _heads(q, "q", q.shape[2], self.head_dim, i)
+        if q.dtype is torch.float32:
             raise TypeError("q must be bfloat16 or float16")
-        tab = self._table(page_table, B)
-        sl = _vec(seq_lens, "seq_lens", B, torch.int32, self.device)
-        ql = None if q_lens is None else _vec(q_lens, "q_lens", B, torch.int32, self.device)
+        tab, pages = self._table(page_table, B)
+        sl = _array(seq_lens, "seq_lens", (B,), torch.int32, i)
+        ql = None if q_lens is None else _array(q_lens, "q_lens", (B,), torch.int32, i)
         if out is None:
-            out = _empty((B, T, H, self.head_dim), q.dtype, self.device, stream)
-        elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or \
-                not out.is_contiguous():
-            raise ValueError("out must be contiguous and like q")
-        L, n = load(), ctypes.c_size_t(0)
-        mp = tab.shape[1]
+            out = _empty(shape, q.dtype, self.device, stream)
+        to = _array(out, "out", shape, q.dtype, i)
+        L = load()
         window, sinks = int(window), int(sinks)
-        _check(L.sfx_kv_attention_workspace_bytes(self._p, B, T, H, mp, window, sinks,
-                                                  ctypes.byref(n)))
-        ws = _empty((n.value,), torch.uint8, self.device, stream) if n.value else None
-        _check(L.sfx_kv_attention(self._p, B, T, H, mp, _ptr(tab), _ptr(sl), _ptr(ql), _ptr(q),
-                                  _strides(q), _ptr(out), _TYPES[q.dtype],
+        key = (B, T, H, pages, window, sinks)
+        n = self._bytes.get(key)
+        if n is None:
+            size = ctypes.c_size_t(0)
+            _check(L.sfx_kv_attention_workspace_bytes(self._p, *key, ctypes.byref(size)))
+            if len(self._bytes) >= 1024:
+                self._bytes.clear()
+            n = self._bytes[key] = size.value
+        ws = _empty((n,), torch.uint8, self.device, stream) if n else None
+        _check(L.sfx_kv_attention(self._p, B, T, H, pages, tab, sl, ql, q.data_ptr(),
+                                  _strides(q), to, _TYPES[q.dtype],
                                   self.head_dim ** -0.5 if scale is None else float(scale),
-                                  window, sinks, _ptr(ws), n.value, _stream(stream)))
+                                  window, sinks, ws.data_ptr() if n else None, n,
+                                  _raw_stream(stream, i)))
         return out
+
+
+_verify_bytes = {}  # workspace sizes of verify's shapes
 
 
 def verify(logits, draft, num_valid, u_accept, u_sample, temperature=None, sampled=None,
@@ -706,33 +723,32 @@ def verify(logits, draft, num_valid, u_accept, u_sample, temperature=None, sampl
     if logits.dim() != 3 or logits.shape[1] < 1 or (logits.shape[2] > 1 and
                                                     logits.stride(2) != 1):
         raise ValueError("logits must be [B, k + 1, V] with V contiguous")
-    dev = logits.device
-    _on(dev)
+    i = logits.get_device()
+    _on(i)
     B, k1, V = logits.shape
-    dr = _i32(draft, "draft", 2)
-    if dr.shape != (B, k1 - 1) or dr.device != dev:
-        raise ValueError(f"draft must be [{B}, {k1 - 1}] on {dev}")
-    nv = None if num_valid is None else _vec(num_valid, "num_valid", B, torch.int32, dev)
-    if not isinstance(u_accept, torch.Tensor) or u_accept.dtype != torch.float32 or \
-            u_accept.device != dev:
-        raise TypeError(f"u_accept must be a float32 tensor on {dev}")
-    if u_accept.shape != dr.shape or not u_accept.is_contiguous():
-        raise ValueError(f"u_accept must be a contiguous [{B}, {k1 - 1}] tensor")
-    us = _vec(u_sample, "u_sample", B, torch.float32, dev)
-    tp = None if temperature is None else _vec(temperature, "temperature", B, torch.float32, dev)
+    dr = _array(draft, "draft", (B, k1 - 1), torch.int32, i)
+    nv = None if num_valid is None else _array(num_valid, "num_valid", (B,), torch.int32, i)
+    ua = _array(u_accept, "u_accept", (B, k1 - 1), torch.float32, i)
+    us = _array(u_sample, "u_sample", (B,), torch.float32, i)
+    tp = None if temperature is None else _array(temperature, "temperature", (B,),
+                                                 torch.float32, i)
     if sampled is None:
-        sampled = _empty((B, k1), torch.int32, dev, stream)
+        sampled = _empty((B, k1), torch.int32, logits.device, stream)
     if num_accepted is None:
-        num_accepted = _empty((B,), torch.int32, dev, stream)
-    if _i32(sampled, "sampled", 2).shape != (B, k1) or sampled.device != dev:
-        raise ValueError(f"sampled must be [{B}, {k1}] on {dev}")
-    _vec(num_accepted, "num_accepted", B, torch.int32, dev)
-    L, n = load(), ctypes.c_size_t(0)
-    ty = _TYPES[logits.dtype]
-    _check(L.sfx_verify_workspace_bytes(B, k1 - 1, V, ty, ctypes.byref(n)))
-    ws = _empty((n.value,), torch.uint8, dev, stream) if n.value else None
-    _check(L.sfx_verify(B, k1 - 1, V, _ptr(logits), logits.stride(0), logits.stride(1),
-                        ty, _ptr(tp), _ptr(dr), _ptr(nv), _ptr(u_accept),
-                        _ptr(us), _ptr(sampled), _ptr(num_accepted), _ptr(ws), n.value,
-                        _stream(stream)))
+        num_accepted = _empty((B,), torch.int32, logits.device, stream)
+    so = _array(sampled, "sampled", (B, k1), torch.int32, i)
+    no = _array(num_accepted, "num_accepted", (B,), torch.int32, i)
+    L = load()
+    key = (B, k1 - 1, V, _TYPES[logits.dtype])
+    n = _verify_bytes.get(key)
+    if n is None:
+        size = ctypes.c_size_t(0)
+        _check(L.sfx_verify_workspace_bytes(*key, ctypes.byref(size)))
+        if len(_verify_bytes) >= 1024:
+            _verify_bytes.clear()
+        n = _verify_bytes[key] = size.value
+    ws = _empty((n,), torch.uint8, logits.device, stream) if n else None
+    _check(L.sfx_verify(B, k1 - 1, V, logits.data_ptr(), logits.stride(0), logits.stride(1),
+                        key[3], tp, dr, nv, ua, us, so, no, ws.data_ptr() if n else None, n,
+                        _raw_stream(stream, i)))
     return sampled, num_accepted
