@@ -220,7 +220,7 @@ int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batc
   if (rc || B == 0) return rc;
   if (!logits || !u_sample || !sampled || !num_accepted || (k > 0 && (!draft || !u_accept)))
     return fail(SFX_EINVAL, "NULL array argument");
-  if (!workspace || workspace_bytes < bytes || ((uintptr_t)workspace & 15))
+  if (bytes > 0 && (!workspace || workspace_bytes < bytes || ((uintptr_t)workspace & 15)))
     return fail(SFX_EINVAL, "workspace of %zu bytes (16-byte aligned) needed, %zu given", bytes,
                 workspace ? workspace_bytes : (size_t)0);
   a.logits = logits;

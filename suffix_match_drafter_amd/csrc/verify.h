@@ -29,12 +29,16 @@ struct VerifyArgs {
   int32_t* sampled;
   int32_t* num_accepted;
   // plan (verify_plan)
+  bool small;         // one launch: a workgroup makes its request's statistics itself
   bool in_order;      // slots in phases, rows past a rejection left out
   int32_t parts;      // parts of one row (in_order: the most)
   int32_t part_size;  // its logits (not in_order)
   VerifyPart* part;   // [B][k + 1][parts]
   int32_t* stop;      // [phases][B] lowest slot known to be rejected (in_order, else NULL)
   int32_t* phase_parts;  // [phases] parts of a row (in_order, else NULL)
+  int32_t pieces;        // workgroups over the fp64 sums of a drawn row
+  VerifyPart* outcome;   // [B] m and at of the row drawn from, pad = its slot (pieces > 1)
+  double* sums;          // [B][pieces][16] (pieces > 1)
 };
 
 constexpr int kVerifyMaxParts = 16;      // of a row, in_order

@@ -32,8 +32,12 @@ constexpr int kPartThreads = 256;   // workgroup of a part of a row
 constexpr int kRowThreads = 1024;   // workgroup of a whole row, and of a request's draw
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kMaxRows = 33;        // k + 1
-constexpr int kPhaseThreads = 512;  // workgroup of a phase after the first
-constexpr int kPhaseGroups = 512;   // two on each of 256 CUs
+// Vocabularies up to this go in one launch: 12-14 us a call at B = 4, k = 8 and V = 1024-4096 where
+// two launches take 17, 25.6 against 37.1 at B = 256, k = 32, V = 4096; at V = 8192 17.4 against
+// 16.9 and 34.3 against 45.9, at 16384 25 against 17.
+constexpr int kSmallV = 4096;
+constexpr int kPhaseThreads = 256;  // workgroup of a phase after the first
+constexpr int kPhaseGroups = 1024;  // four on each of 256 CUs
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
@@ -181,15 +185,14 @@ __device__ __forceinline__ VerifyPart join(const VerifyPart& p, const VerifyPart
                     q.m > p.m || (q.m == p.m && q.at < p.at) ? q.at : p.at, 0};
 }
 
-// Largest logit, its lowest index and the sum of exponentials of logits [j0, j1) of a row, by a
-// workgroup of N threads; the result is every thread's.  Taken as they come, a NaN or +inf makes
-// the sum a NaN; then, and only then, they are cleaned and summed again.
-template <typename T, int N, bool kClean>
-__device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, float c,
-                                VerifyPart* w) {
+// Largest logit, its lowest index and the sum of exponentials of the logits that a wavefront's
+// lanes take: eight each at j, j + step, ... below j1.  The result is every lane's.
+template <typename T, int kBatch, bool kClean>
+__device__ __forceinline__ VerifyPart wave_stats(const char* row, int j, int j1, int step,
+                                                 bool greedy, float c) {
   float m = -__builtin_inff(), s = 0.f;
   int at = 0x7fffffff;
-  each8<T, 4>(row, j0 + (int)threadIdx.x * 8, j1, N * 8, [&](float (&x)[8], int j) {
+  each8<T, kBatch>(row, j, j1, step, [&](float (&x)[8], int j) {
     if (kClean)
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = clean(x[e]);
@@ -214,20 +217,34 @@ __device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, fl
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1)
     r = join(r, VerifyPart{__shfl_xor(r.m, o), __shfl_xor(r.s, o), __shfl_xor(r.at, o), 0}, c);
+  return r;
+}
+
+// Taken as they come, a NaN or +inf among the logits makes the sum a NaN or the maximum infinite;
+// then, and only then, they are cleaned and summed again.
+__device__ __forceinline__ bool to_clean(const VerifyPart& r) {
+  return !(r.s < __builtin_inff()) || r.m == __builtin_inff();
+}
+
+template <typename T, int N, bool kClean>
+__device__ __forceinline__ VerifyPart group_stats(const char* row, int j0, int j1, bool greedy, float c,
+                                  VerifyPart* w) {
+  const VerifyPart mine = wave_stats<T, 4, kClean>(row, j0 + (int)threadIdx.x * 8, j1, N * 8,
+                                                   greedy, c);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = r;
+  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = mine;
   __syncthreads();
-  r = w[0];
+  VerifyPart r = w[0];
   for (int i = 1; i < N / 64; ++i) r = join(r, w[i], c);
   return r;
 }
 
+// Logits [j0, j1) of a row by a workgroup of N threads; the result is every thread's.
 template <typename T, int N>
-__device__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, float c) {
+__device__ __forceinline__ VerifyPart row_stats(const char* row, int j0, int j1, bool greedy, float c) {
   __shared__ VerifyPart w[N / 64];
-  VerifyPart r = row_stats<T, N, false>(row, j0, j1, greedy, c, w);
-  if (!(r.s < __builtin_inff()) || r.m == __builtin_inff())
-    r = row_stats<T, N, true>(row, j0, j1, greedy, c, w);
+  VerifyPart r = group_stats<T, N, false>(row, j0, j1, greedy, c, w);
+  if (to_clean(r)) r = group_stats<T, N, true>(row, j0, j1, greedy, c, w);
   return r;
 }
 
@@ -404,11 +421,19 @@ __device__ __forceinline__ int phase_part(int V, int parts) {
   return ((V + parts - 1) / parts + 7) / 8 * 8;
 }
 
-// A row's parts, `parts` of them, as one.
+// A row's parts, `parts` of them, as one; eight loads are in flight together.
 __device__ __forceinline__ VerifyPart join_row(const VerifyArgs& a, int64_t row, int parts,
                                                float c) {
-  VerifyPart r = a.part[row * a.parts];
-  for (int i = 1; i < parts; ++i) r = join(r, a.part[row * a.parts + i], c);
+  const VerifyPart* p = a.part + row * a.parts;
+  VerifyPart r{-__builtin_inff(), 0.f, 0x7fffffff, 0};
+  for (int i = 0; i < parts; i += 8) {
+    VerifyPart q[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) q[k] = p[i + k < parts ? i + k : i];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i + k < parts) r = join(r, q[k], c);
+  }
   return r;
 }
 
@@ -507,16 +532,33 @@ struct Drawn {
   int at;
 };
 
-template <typename T>
+// kSmall: the rows' statistics are made here, a wavefront a row; otherwise they have been stored.
+template <typename T, bool kSmall>
 __device__ Drawn accepted(const VerifyArgs& a, int b, float temp, bool greedy, double* seg,
                           const double* table) {
   __shared__ float row_m[kMaxRows];
   __shared__ int row_at[kMaxRows], verdict[kMaxRows];
   // rows past `end` have no statistics; slot `end` is past the draft or known to be rejected
   const int tid = threadIdx.x;
-  const int end = a.stop ? a.stop[last_phase(a.k) * a.B + b] : clamp_valid(a, b);
+  const int end = !kSmall && a.stop ? a.stop[last_phase(a.k) * a.B + b] : clamp_valid(a, b);
   const float c = greedy ? 1.f : inv_log2(temp);
-  if (tid <= end) {
+  if constexpr (kSmall) {
+    __shared__ VerifyPart own[kMaxRows];
+    const int lane = tid & 63;
+    for (int slot = tid >> 6; slot <= end; slot += kRowWaves) {
+      const char* row = row_ptr(a, b, slot, T::kBytes);
+      VerifyPart r = wave_stats<T, 1, false>(row, lane * 8, a.V, 512, greedy, c);
+      if (to_clean(r)) r = wave_stats<T, 1, true>(row, lane * 8, a.V, 512, greedy, c);
+      if (lane == 0) own[slot] = r;
+    }
+    __syncthreads();
+    if (tid <= end) {
+      row_m[tid] = own[tid].m;
+      row_at[tid] = own[tid].at;
+      verdict[tid] = tid < end ? test_slot<T>(a, b, tid, own[tid], greedy, c, a.V / 512 + 1)
+                               : kReject;
+    }
+  } else if (tid <= end) {
     const int64_t row = (int64_t)b * (a.k + 1) + tid;
     const int phase = phase_of(tid);
     const int parts = a.stop ? a.phase_parts[phase] : a.parts;
@@ -540,41 +582,138 @@ __device__ Drawn accepted(const VerifyArgs& a, int b, float temp, bool greedy, d
   return Drawn{n, row_m[n], row_at[n]};
 }
 
-// One workgroup per request: the tests in order (small calls), then the draw from the row they
-// end at.  The row is summed in segments, the segment that holds the draw in turn, until 1024
-// logits are left, which are scanned one a thread.
-template <typename T>
-__global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) {
-  __shared__ double seg[kRowWaves], table[kTable];
+// One value a thread, in order: the first thread whose running sum (from `base`) passes t, or the
+// last that holds anything where rounding hides that one; -1 when all are nothing.  `before`: the
+// sum ahead of it; with `fresh`, t is first set to u times the whole sum.
+struct Found {
+  int at;
+  double before, t;
+};
+__device__ Found find_in_block(double x, double least, double base, double t, bool fresh, double u,
+                               double* seg) {
   __shared__ int found;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ double found_before;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  double inc = x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double y = __shfl_up(inc, o);
+    if (lane >= o) inc += y;
+  }
+  double exc = __shfl_up(inc, 1);
+  if (lane == 0) exc = 0.0;
+  __syncthreads();
+  if (lane == 63) seg[wave] = inc;
+  if (tid == 0) found = 0x7fffffff;
+  __syncthreads();
+  double before = base, z = 0.0;
+  for (int i = 0; i < kRowWaves; ++i) {
+    if (i < wave) before += seg[i];
+    z += seg[i];
+  }
+  if (fresh) t = u * z;
+  const unsigned long long some = __ballot(x > least);
+  const unsigned long long hit = __ballot(x > least && before + inc > t);
+  if (hit && lane == 0) atomicMin(&found, tid + __ffsll((long long)hit) - 1);
+  __syncthreads();
+  const bool hidden = found == 0x7fffffff;
+  __syncthreads();
+  if (hidden) {
+    if (tid == 0) found = -1;
+    __syncthreads();
+    if (some && lane == 0) atomicMax(&found, tid + 63 - __clzll(some));
+    __syncthreads();
+  }
+  const int at = found;
+  if (tid == at) found_before = before + exc;
+  __syncthreads();
+  const double ahead = at >= 0 ? found_before : base;
+  __syncthreads();
+  return Found{at, ahead, t};
+}
+
+// Few requests over a large vocabulary: the fp64 sums of a request's row, `pieces` workgroups of
+// kRowWaves segments each.  Every one makes the request's tests again; the first stores their
+// outcome.
+template <typename T>
+__global__ __launch_bounds__(kRowThreads) void verify_sums_kernel(VerifyArgs a) {
+  __shared__ double seg[kRowWaves], table[kTable];
+  const int b = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float temp = temperature(a, b);
   const bool greedy = !(temp > 0.f);
   fill_table(table);
   __syncthreads();
-  const Drawn r = accepted<T>(a, b, temp, greedy, seg, table);
+  const Drawn r = accepted<T, false>(a, b, temp, greedy, seg, table);
+  if (piece == 0 && threadIdx.x == 0) a.outcome[b] = VerifyPart{r.m, 0.f, r.at, r.n};
+  if (greedy || !(r.m > -__builtin_inff())) return;
+  const int d = r.n < clamp_valid(a, b) ? a.draft[(int64_t)b * a.k + r.n] : -1;
+  const int j0 = seg_at(0, a.V, piece, a.pieces), j1 = seg_at(0, a.V, piece + 1, a.pieces);
+  const double s = wave_range64<T>(row_ptr(a, b, r.n, T::kBytes), seg_at(j0, j1, wave, kRowWaves),
+                                   seg_at(j0, j1, wave + 1, kRowWaves),
+                                   weights64(table, r.m, temp, false), d, lane);
+  if (lane == 0) a.sums[((int64_t)b * a.pieces + piece) * kRowWaves + wave] = s;
+}
+
+// One workgroup per request: the tests in order (of a large call those of its last phase and any
+// too close for fp32), then the draw from the row they end at.  The row is summed in segments, the
+// segment that holds the draw in turn, until 1024 logits are left, which are taken one a thread.
+template <typename T, bool kSmall>
+__global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) {
+  __shared__ double seg[kRowWaves], table[kTable];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const float temp = temperature(a, b);
+  const bool greedy = !(temp > 0.f);
+  Drawn r;
+  if (!kSmall && a.pieces > 1) {
+    const VerifyPart p = a.outcome[b];
+    r = Drawn{p.pad, p.m, p.at};
+  } else {
+    fill_table(table);
+    __syncthreads();
+    r = accepted<T, kSmall>(a, b, temp, greedy, seg, table);
+  }
   int pick = -1;
   if (r.m > -__builtin_inff()) {
     pick = r.at;
     if (!greedy) {
       const int d = r.n < clamp_valid(a, b) ? a.draft[(int64_t)b * a.k + r.n] : -1;
       const char* row = row_ptr(a, b, r.n, T::kBytes);
-      const Weights64 w = weights64(table, r.m, temp, false);
-      const double inv = inv64(temp);
+      const double u = a.u_sample[b], inv = inv64(temp);
       int j0 = 0, j1 = a.V;
       double base = 0.0, t = 0.0;
-      bool none = false;
+      bool fresh = true, none = false;
+      if (!kSmall && a.pieces > 1) {
+        const int segs = a.pieces * kRowWaves;
+        const double x = tid < segs ? a.sums[(int64_t)b * segs + tid] : 0.0;
+        const Found f = find_in_block(x, kTiny, base, t, fresh, u, seg);
+        none = f.at < 0;
+        const int s = f.at < 0 ? 0 : f.at;
+        const int p0 = seg_at(0, a.V, s / kRowWaves, a.pieces);
+        const int p1 = seg_at(0, a.V, s / kRowWaves + 1, a.pieces);
+        j0 = seg_at(p0, p1, s % kRowWaves, kRowWaves);
+        j1 = seg_at(p0, p1, s % kRowWaves + 1, kRowWaves);
+        base = f.before;
+        t = f.t;
+        fresh = false;
+        if (j1 - j0 > kRowThreads) {
+          fill_table(table);
+          __syncthreads();
+        }
+      }
       while (j1 - j0 > kRowThreads) {
+        const Weights64 w = weights64(table, r.m, temp, false);
         const double s = wave_range64<T>(row, seg_at(j0, j1, wave, kRowWaves),
                                          seg_at(j0, j1, wave + 1, kRowWaves), w, d, lane);
         __syncthreads();
         if (lane == 0) seg[wave] = s;
         __syncthreads();
-        if (j0 == 0 && j1 == a.V) {
+        if (fresh) {
           double z = 0.0;
           for (int i = 0; i < kRowWaves; ++i) z += seg[i];
-          t = (double)a.u_sample[b] * z;
+          t = u * z;
           none = !(z > kTiny);
+          fresh = false;
         }
         // the segment whose sums pass t; the last that holds anything if rounding hides it
         int at = 0;
@@ -591,45 +730,16 @@ __global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) 
         j0 = s0;
         j1 = s1;
       }
-      const bool whole = j0 == 0 && j1 == a.V;
-      // one logit a thread: running sums of the wavefront, then of those before it
-      const int j = j0 + tid;
-      double x = 0.0;
-      if (j < j1 && j != d)
-        x = weight64_full(logit<T>(row, j), r.m, inv);
-      double inc = x;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double y = __shfl_up(inc, o);
-        if (lane >= o) inc += y;
-      }
-      __syncthreads();
-      if (lane == 63) seg[wave] = inc;
-      if (tid == 0) found = 0x7fffffff;
-      __syncthreads();
-      double before = base, z = 0.0;
-      for (int i = 0; i < kRowWaves; ++i) {
-        if (i < wave) before += seg[i];
-        z += seg[i];
-      }
-      if (whole) {
-        t = (double)a.u_sample[b] * z;
-        none = !(z > 0.0);
-      }
-      const unsigned long long hit = __ballot(x > 0.0 && before + inc > t);
-      if (hit && lane == 0) atomicMin(&found, j + __ffsll((long long)hit) - 1);
-      __syncthreads();
-      if (found == 0x7fffffff) {  // rounding hid it: the last that weighs anything
-        const unsigned long long some = __ballot(x > 0.0);
-        __syncthreads();
-        if (tid == 0) found = -1;
-        __syncthreads();
-        if (some && lane == 0) atomicMax(&found, j + 63 - __clzll(some));
-        __syncthreads();
-      }
-      if (!none) pick = found;
-      if (!whole && t < kTiny && !none) {
+      const bool tiny = !fresh && t < kTiny;
+      if (!none && !tiny) {
+        const int j = j0 + tid;
+        double x = 0.0;
+        if (j < j1 && j != d) x = weight64_full(logit<T>(row, j), r.m, inv);
+        const int at = find_in_block(x, 0.0, base, t, fresh, u, seg).at;
+        if (at >= 0) pick = j0 + at;
+      } else if (!none) {
         // A draw this close to 0 can land on weights that the fast ones leave out.
+        __shared__ int found;
         if (wave == 0) {
           double run = 0.0;
           int last = -1;
@@ -653,7 +763,7 @@ __global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) 
           if (lane == 0) found = last;
         }
         __syncthreads();
-        pick = found;
+        if (found >= 0) pick = found;
       }
     }
   }
@@ -666,8 +776,13 @@ __global__ __launch_bounds__(kRowThreads) void verify_draw_kernel(VerifyArgs a) 
 template <typename T>
 hipError_t launch_type(const VerifyArgs& a, hipStream_t st) {
   const int64_t rows = (int64_t)a.B * (a.k + 1);
+  const dim3 requests((unsigned)a.B), whole(kRowThreads);
+  if (a.small) {
+    hipLaunchKernelGGL((verify_draw_kernel<T, true>), requests, whole, 0, st, a);
+    return hipGetLastError();
+  }
   if (a.stop) {
-    hipLaunchKernelGGL(verify_first_kernel<T>, dim3((unsigned)a.B), dim3(kRowThreads), 0, st, a);
+    hipLaunchKernelGGL(verify_first_kernel<T>, requests, whole, 0, st, a);
     for (int phase = 1; phase <= last_phase(a.k); ++phase)
       hipLaunchKernelGGL(verify_phase_kernel<T>, dim3(kPhaseGroups), dim3(kPhaseThreads), 0, st, a,
                          phase);
@@ -677,7 +792,11 @@ hipError_t launch_type(const VerifyArgs& a, hipStream_t st) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(verify_draw_kernel<T>, dim3((unsigned)a.B), dim3(kRowThreads), 0, st, a);
+  if (a.pieces > 1) {
+    hipLaunchKernelGGL(verify_sums_kernel<T>, dim3((unsigned)(a.B * a.pieces)), whole, 0, st, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((verify_draw_kernel<T, false>), requests, whole, 0, st, a);
   return hipGetLastError();
 }
 
@@ -686,24 +805,51 @@ hipError_t launch_type(const VerifyArgs& a, hipStream_t st) {
 size_t verify_plan(VerifyArgs* a, KvType type) {
   const int bytes = type == kFp32 ? 4 : 2;
   const int64_t rows = (int64_t)a->B * (a->k + 1);
-  a->in_order = a->B <= kVerifyMaxOrdered && (double)rows * a->V * bytes >= 2e8;
-  // else parts of at least 16K logits, enough of them to fill 256 CUs four times over
-  int64_t parts = rows > 0 ? (1024 + rows - 1) / rows : 1;
-  const int64_t most = ((int64_t)a->V + 16383) / 16384;
-  parts = parts > most ? most : parts;
-  parts = parts < 1 ? 1 : parts;
-  const int64_t size = (a->V + parts - 1) / parts;
-  a->part_size = (int32_t)((size + 7) / 8 * 8);
-  a->parts = (int32_t)((a->V + a->part_size - 1) / a->part_size);
-  if (a->in_order) a->parts = kVerifyMaxParts;
-  return (size_t)rows * a->parts * sizeof(VerifyPart) +
-         (a->in_order ? (size_t)kPhases * (a->B + 1) * sizeof(int32_t) : 0);
+  a->in_order = false;
+  a->parts = a->pieces = 1;
+  a->part_size = a->V;
+  a->small = a->V <= kSmallV;
+  if (a->small) return 0;
+  // Phases pay from about 0.4 GB of logits: at B = 256, k = 32, V = 32000 (0.54 GB) 90 us against
+  // 145 when 64% of the drafted tokens are accepted, 220 against 143 when all are; at 1.3 GB 154
+  // against 298 and 367 against 297; at 0.28 GB 86 against 81 and 148 against 82.
+  a->in_order = a->B <= kVerifyMaxOrdered && (double)rows * a->V * bytes >= 4e8;
+  if (a->in_order) {
+    a->parts = kVerifyMaxParts;
+  } else {
+    // parts of at least 16K logits, enough of them to fill 256 CUs four times over
+    int64_t parts = rows > 0 ? (1024 + rows - 1) / rows : 1;
+    const int64_t most = ((int64_t)a->V + 16383) / 16384;
+    parts = parts > most ? most : parts;
+    parts = parts < 1 ? 1 : parts;
+    const int64_t size = (a->V + parts - 1) / parts;
+    a->part_size = (int32_t)((size + 7) / 8 * 8);
+    a->parts = (int32_t)((a->V + a->part_size - 1) / a->part_size);
+  }
+  // the drawn rows' fp64 sums: one workgroup per CU, of at least 4K logits, 1024 segments a row
+  int64_t pieces = a->B > 0 ? 256 / a->B : 1;
+  pieces = pieces > a->V / 4096 ? a->V / 4096 : pieces;
+  pieces = pieces > kRowThreads / kRowWaves ? kRowThreads / kRowWaves : pieces;
+  a->pieces = pieces < 1 ? 1 : (int32_t)pieces;
+  size_t size = (size_t)rows * a->parts * sizeof(VerifyPart);
+  if (a->pieces > 1)
+    size += (size_t)a->B * (sizeof(VerifyPart) + a->pieces * kRowWaves * sizeof(double));
+  if (a->in_order) size += (size_t)kPhases * (a->B + 1) * sizeof(int32_t);
+  return size;
 }
 
 void verify_place(VerifyArgs* a, void* workspace) {
   const size_t rows = (size_t)a->B * (a->k + 1);
   a->part = (VerifyPart*)workspace;
-  a->stop = a->in_order ? (int32_t*)(a->part + rows * a->parts) : nullptr;
+  VerifyPart* next = a->part + rows * a->parts;
+  a->outcome = nullptr;
+  a->sums = nullptr;
+  if (a->pieces > 1) {
+    a->outcome = next;
+    a->sums = (double*)(a->outcome + a->B);
+    next = (VerifyPart*)(a->sums + (size_t)a->B * a->pieces * kRowWaves);
+  }
+  a->stop = a->in_order ? (int32_t*)next : nullptr;
   a->phase_parts = a->in_order ? a->stop + (size_t)kPhases * a->B : nullptr;
 }
 

@@ -37,7 +37,7 @@ def attend(c, B=1, T=1, H=4, mp=2, table=P, lens=P, q=P, out=P, ty=0, scale=0.1,
                                        None)
 
 
-def verify(B=1, k=4, V=100, logits=P, ty=0, draft=P, ua=P, us=P, out=P, na=P, ws=P, nws=1 << 20):
+def verify(B=1, k=4, V=100000, logits=P, ty=0, draft=P, ua=P, us=P, out=P, na=P, ws=P, nws=1 << 20):
     return sfx.load().sfx_verify(B, k, V, logits, 0, 0, ty, None, draft, None, ua, us, out, na,
                                  ws, nws, None)
 
@@ -98,7 +98,7 @@ def test_bad_verify():
     assert L.sfx_verify_workspace_bytes(4, 8, 1000, 0, None) == sfx.EINVAL
     assert L.sfx_verify_workspace_bytes(4, 33, 1000, 0, ctypes.byref(n)) == sfx.EINVAL
     assert L.sfx_verify_workspace_bytes(4, 8, 1000, 3, ctypes.byref(n)) == sfx.EINVAL
-    assert L.sfx_verify_workspace_bytes(4, 8, 1000, 2, ctypes.byref(n)) == sfx.OK and n.value > 0
+    assert L.sfx_verify_workspace_bytes(4, 8, 100000, 2, ctypes.byref(n)) == sfx.OK and n.value > 0
 
 
 def test_python_refusals():

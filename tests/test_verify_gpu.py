@@ -283,3 +283,34 @@ def test_large_calls(S, dtype, B, k, V):
             assert na[b].item() == n and np.array_equal(out[b].cpu().numpy(), s), (b, n)
         us = rng.random(B).astype(np.float32)
         ua = rng.random((B, k)).astype(np.float32)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("B,V", [(1, 4097), (1, 8192), (2, 70001), (3, 262147), (20, 33000),
+                                 (100, 9001), (129, 9001), (2, 4096), (2, 1025), (2, 1024)])
+def test_draws(S, dtype, B, V):
+    """Draws alone, over every way of splitting a row: first and last tokens, u of 0, masked ends,
+    heavy tokens at the borders of segments."""
+    import torch
+
+    rng = np.random.default_rng(V)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    x = torch.randn((B, 1, V), generator=g, device="cuda").to(getattr(torch, dtype))
+    empty = np.zeros((B, 0), np.int32)
+    for step in range(6):
+        us = rng.random(B).astype(np.float32)
+        if step == 1:
+            us[:] = 0.0
+        if step == 2:
+            us[:] = np.nextafter(np.float32(1), np.float32(0))
+        if step == 3:
+            x[:, 0, :V // 3] = -float("inf")
+            us[0] = 0.0
+        if step == 4:
+            x[:, 0, V - V // 5:] = -float("inf")
+            us[:] = np.nextafter(np.float32(1), np.float32(0))
+        if step == 5:
+            for j in (V // 2, V // 2 + 1, V // 16 * 9, V // 16 * 9 - 1):
+                x[:, 0, j] = 11.0
+        check(S, x, empty, None, empty.astype(np.float32), us, None)
