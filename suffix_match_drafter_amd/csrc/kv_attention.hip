@@ -516,35 +516,73 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
   }
 }
 
-// Joins the splits of the rows that had more than one, D / 4 lanes a row; the loads of up to eight
-// splits are in flight together.
-template <typename T, int D>
+// Joins the splits of the rows that had more than one: D / 4 lanes hold a row, kGroups such groups
+// take every kGroups-th split and meet in LDS.  With many splits one group alone would wait for
+// its loads again and again (10 us for 64 splits of 65 rows, 4 with all of a workgroup on a row).
+template <typename T, int D, int kGroups>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chunk_rows) {
-  constexpr int kLanes = D / 4;
-  const int d = (threadIdx.x % kLanes) * 4;
-  const int64_t at = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+  constexpr int kLanes = D / 4, kRows = 256 / kLanes / kGroups;
+  __shared__ f32x4 xs[kRows][kGroups][kLanes];
+  __shared__ float ms[kRows][kGroups], ls[kRows][kGroups];
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes % kGroups;
+  const int mine = threadIdx.x / kLanes / kGroups, d = lane * 4;
+  const int64_t at = (int64_t)blockIdx.x * kRows + mine;
   const int all_rows = a.T * a.group;
   const int64_t rows = (int64_t)a.B * a.c.heads * all_rows;
-  if (at >= rows) return;
-  const int row = (int)(at % all_rows);
-  const int h = (int)(at / all_rows % a.c.heads);
-  const int b = (int)(at / all_rows / a.c.heads);
+  const bool live = at < rows;
+  const int row = live ? (int)(at % all_rows) : 0;
+  const int h = live ? (int)(at / all_rows % a.c.heads) : 0;
+  const int b = live ? (int)(at / all_rows / a.c.heads) : 0;
   const Span s = span_of(a, b, row / chunk_rows * chunk_rows, chunk_rows);
-  const int active = (s.tiles + a.tiles_per_split - 1) / a.tiles_per_split;
-  if (active <= 1) return;
-  float m = -__builtin_inff();
-#pragma unroll 8
-  for (int i = 0; i < active; ++i) m = fmaxf(m, a.part_lse[i * rows + at]);
+  const int active = live ? (s.tiles + a.tiles_per_split - 1) / a.tiles_per_split : 0;
+  float m = -__builtin_inff(), l = 0.f;
   f32x4 x{0, 0, 0, 0};
-  float l = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < active; ++i) {
-    const float e = a.part_lse[i * rows + at];
-    const f32x4 o = *(const f32x4*)(a.part_o + (i * rows + at) * D + d);
-    const float w = e == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(e - m);
-    l += w;
-    x += w * o;
+  for (int i = group; active > 1 && i < active; i += 8 * kGroups) {
+    float e[8];
+    f32x4 o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int j = i + k * kGroups < active ? i + k * kGroups : i;
+      e[k] = a.part_lse[j * rows + at];
+      o[k] = *(const f32x4*)(a.part_o + (j * rows + at) * D + d);
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, e[k]);
+    const float z = top == -__builtin_inff() ? 0.f : top;
+    const float f = __builtin_amdgcn_exp2f(m - z);
+    x *= f;
+    l *= f;
+    m = top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i + k * kGroups < active) {
+        const float w = __builtin_amdgcn_exp2f(e[k] - z);  // 0 for a split that saw nothing
+        l += w;
+        x += e[k] == -__builtin_inff() ? f32x4{0, 0, 0, 0} : w * o[k];
+      }
   }
+  if constexpr (kGroups > 1) {
+    xs[mine][group][lane] = x;
+    if (lane == 0) {
+      ms[mine][group] = m;
+      ls[mine][group] = l;
+    }
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) m = fmaxf(m, ms[mine][k]);
+    const float z = m == -__builtin_inff() ? 0.f : m;
+    x = f32x4{0, 0, 0, 0};
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const float w = __builtin_amdgcn_exp2f(ms[mine][k] - z);
+      l += w * ls[mine][k];
+      x += w * xs[mine][k][lane];
+    }
+  }
+  if (active <= 1) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t out =
       ((int64_t)b * a.T + row / a.group) * a.c.heads * a.group + h * a.group + row % a.group;
@@ -619,8 +657,14 @@ hipError_t launch_dim(const KvAttentionArgs& a, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t rows = (int64_t)a.B * a.c.heads * a.T * a.group;
-  hipLaunchKernelGGL((kv_join_kernel<T, D>), dim3((unsigned)((rows * (D / 4) + 255) / 256)),
-                     dim3(256), 0, st, a, rt * 16);
+  // all of a workgroup on a row where there are many splits (then there are few rows)
+  constexpr int kWide = 256 / (D / 4);
+  if (a.splits > 4)
+    hipLaunchKernelGGL((kv_join_kernel<T, D, kWide>), dim3((unsigned)rows), dim3(256), 0, st, a,
+                       rt * 16);
+  else
+    hipLaunchKernelGGL((kv_join_kernel<T, D, 1>), dim3((unsigned)((rows * (D / 4) + 255) / 256)),
+                       dim3(256), 0, st, a, rt * 16);
   return hipGetLastError();
 }
 
