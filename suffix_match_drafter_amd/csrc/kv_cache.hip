@@ -210,7 +210,8 @@ __device__ __forceinline__ void to_order(const unsigned (&raw)[kWords<T>],
 // registers between the maximum and the rounding, so the input is read once and the kernel is
 // bounded by that traffic (prompts: 1.5 vector instructions an element in 16 bits) or by one
 // dependent chain of loads (a few tokens: counts, page id, then inputs, old codes and scale
-// together).
+// together).  Measured: 8 prompts of 8192 tokens of 8 heads of 128 in bf16 78 us, 4.8 TB/s; 256
+// drafts of 17 tokens 16 us, a single token for 4 requests 4 us.
 template <typename T, int D, bool kVal>
 __device__ void write_block(const KvMoveArgs& a, int b, int h, int block, int start, int count,
                             int lane) {
@@ -413,7 +414,9 @@ struct ReadLds {
 };
 
 // The reverse: one wavefront per (request, 32-token block, tensor, head), zeros for rows past the
-// count or on an unmapped page.  Bounded by the traffic, which is mostly the result's.
+// count or on an unmapped page.  Bounded by the traffic, which is mostly the result's: 8 x 16384
+// tokens of 8 heads of 128 in bf16 150 to 167 us, 4.5 to 5.0 TB/s (stored straight from the
+// lanes that hold them, 4 bytes at a time, the values took it to 184 to 203).
 template <typename T, int D, bool kVal>
 __device__ void read_block(const KvMoveArgs& a, int b, int h, int64_t block, int start, int count,
                            int lane, u32x4* turn) {
