@@ -5,11 +5,11 @@
 //   out_t = sum_j softmax_j(scale q_t . k_j) v_j,    zero for a row that sees nothing.
 //
 // Decomposition.  The rows of one request and cached head (tokens x query heads of its group)
-// are cut into chunks of up to 64, the tokens into splits; a workgroup takes one (chunk, split)
-// and its four wavefronts take the 32-token tiles of it in turn, each on its own: a wavefront
-// holds its rows' queries and outputs in registers, streams keys and values from memory into
-// operand registers in the order in which the cache keeps them, and meets the other three only
-// at the end.  No LDS and no barrier lies on the way of a tile.
+// are cut into chunks of up to 64 (48 at 128 dims, 32 at 256), the tokens into splits; a workgroup
+// takes one (chunk, split) and its four wavefronts take the 32-token tiles of it in turn, each on
+// its own: a wavefront holds its rows' queries and outputs in registers, streams keys and values
+// from memory into operand registers in the order in which the cache keeps them, and meets the
+// other three only at the end.  No LDS and no barrier lies on the way of a tile.
 //
 // Per tile, with the 16x16x32 matrix instructions (lane = 16 g + n):
 //   S^T = K Q^T: rows are tokens, columns query rows, so lane (n, g) gets the scores of query
@@ -599,8 +599,15 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chu
       u32x2{T::pack(x[0] * inv, x[1] * inv), T::pack(x[2] * inv, x[3] * inv)};
 }
 
-int max_row_tiles(int dim) { return dim > 128 ? 2 : 4; }
+// Row tiles of a chunk at most.  At 128 dims a fourth would leave room for one wavefront a SIMD only:
+// 64 rows for 32 requests of 8192 tokens took 148 us so and take 124 in two chunks of two.  At 256
+// dims two tiles, with one wavefront, take 108 us for 20 rows and 151 for 36 where two chunks of
+// one and two wavefronts take 130 and 167.  At 64 dims four against three: 79 us and 91.
+int max_row_tiles(int dim) { return dim > 128 ? 2 : (dim > 64 ? 3 : 4); }
 
+// Chunks of equal size: 17 rows of a draft and 4 query heads are five tiles, cut 3 + 3.  Cut 3 + 2
+// the smaller chunk runs ahead of the other, the two no longer meet in L2, and the call takes 255 us
+// where it takes 237.
 int row_tiles(const KvAttentionArgs& a, int dim, int* chunks) {
   const int64_t tiles = ((int64_t)a.T * a.group + 15) / 16;
   const int most = max_row_tiles(dim);
@@ -654,14 +661,12 @@ hipError_t launch_dim(const KvAttentionArgs& a, hipStream_t st) {
   const dim3 block(64 * kWaves);
   if (rt == 1)
     hipLaunchKernelGGL((kv_attention_kernel<T, D, 1>), grid, block, 0, st, a);
-  else if (rt == 2)
+  if (rt == 2)
     hipLaunchKernelGGL((kv_attention_kernel<T, D, 2>), grid, block, 0, st, a);
-  if constexpr (D <= 128) {
-    if (rt == 3)
-      hipLaunchKernelGGL((kv_attention_kernel<T, D, 3>), grid, block, 0, st, a);
-    else if (rt == 4)
-      hipLaunchKernelGGL((kv_attention_kernel<T, D, 4>), grid, block, 0, st, a);
-  }
+  if constexpr (D <= 128)
+    if (rt == 3) hipLaunchKernelGGL((kv_attention_kernel<T, D, 3>), grid, block, 0, st, a);
+  if constexpr (D <= 64)
+    if (rt == 4) hipLaunchKernelGGL((kv_attention_kernel<T, D, 4>), grid, block, 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t rows = (int64_t)a.B * a.c.heads * a.T * a.group;

@@ -114,6 +114,25 @@ def test_against_model(S, case, dtype):
     compare(out, model, q, table, lens, qlens, dim ** -0.5, window, sinks)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [16, 17, 33, 49, 65, 68, 81, 97, 119, 136, 150])
+def test_row_chunks(S, dim, rows):
+    """Every way of cutting a head's rows into chunks, split and not, with fewer live rows than
+    there is room for."""
+    import torch
+
+    rng = np.random.default_rng(rows)
+    page, group = 64, next(g for g in (17, 7, 4, 3, 2, 1) if rows % g == 0)
+    T = rows // group
+    for lens, width in (([90, 3], 3), ([2500, 700], 40)):
+        cache, model = filled(S, rng, 2 * width, page, 1, dim)
+        table = rng.permutation(2 * width).reshape(2, width)
+        q = dev(rng.standard_normal((2, T, group, dim))).to(torch.bfloat16)
+        qlens = [T, max(0, T - 2)]
+        out = cache.attend(q, i32(table), i32(lens), i32(qlens))
+        compare(out, model, q, table, lens, qlens, dim ** -0.5, 0, 0)
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 def test_long_and_split(S, dtype):
     """Long requests beside short ones: several splits, some of them empty."""
