@@ -664,7 +664,8 @@ class KVCache:
         elif _heads(k, "k", self.kv_heads, self.head_dim, i) != shape or k.dtype is not dtype:
             raise ValueError(f"k must be {shape} of {dtype}")
         if v is None:
-            v = _empty(shape, dtype, self.device, stream)
+            v = torch.empty_like(k) if stream is None and k.is_contiguous() else \
+                _empty(shape, dtype, self.device, stream)
         elif _heads(v, "v", self.kv_heads, self.head_dim, i) != shape or v.dtype is not dtype:
             raise ValueError(f"v must be {shape} of {dtype}")
         _check(load().sfx_kv_read(self._p, B, shape[1], pages, tab, st, ct, k.data_ptr(),
@@ -688,7 +689,8 @@ class KVCache:
         sl = _array(seq_lens, "seq_lens", (B,), torch.int32, i)
         ql = None if q_lens is None else _array(q_lens, "q_lens", (B,), torch.int32, i)
         if out is None:
-            out = _empty(shape, q.dtype, self.device, stream)
+            out = torch.empty_like(q) if stream is None and q.is_contiguous() else \
+                _empty(shape, q.dtype, self.device, stream)
         to = _array(out, "out", shape, q.dtype, i)
         L = load()
         window, sinks = int(window), int(sinks)
@@ -733,9 +735,11 @@ def verify(logits, draft, num_valid, u_accept, u_sample, temperature=None, sampl
     tp = None if temperature is None else _array(temperature, "temperature", (B,),
                                                  torch.float32, i)
     if sampled is None:
-        sampled = _empty((B, k1), torch.int32, logits.device, stream)
+        sampled = draft.new_empty(B, k1) if stream is None else \
+            _empty((B, k1), torch.int32, logits.device, stream)
     if num_accepted is None:
-        num_accepted = _empty((B,), torch.int32, logits.device, stream)
+        num_accepted = draft.new_empty(B) if stream is None else \
+            _empty((B,), torch.int32, logits.device, stream)
     so = _array(sampled, "sampled", (B, k1), torch.int32, i)
     no = _array(num_accepted, "num_accepted", (B,), torch.int32, i)
     L = load()
