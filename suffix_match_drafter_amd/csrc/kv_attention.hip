@@ -26,7 +26,9 @@
 // follows a new maximum only once a score passes m + 7 (P would near fp16's largest value), so
 // most tiles touch neither the sums nor the other lanes.  Weights down to 2^-22 of the largest
 // keep fp16's full 11 bits; their rounding (2^-11 relative) is the only one between the
-// stored values and the fp32 sums.  The denominators add the unrounded weights in fp32.
+// stored values and the fp32 sums.  The denominators add the unrounded weights in fp32.  s is
+// (sum q k) c; s - m is one multiply-add of the unrounded product, unless m is so large that its
+// own rounding (16 at 2^28) would decide the weight: then the product is rounded as m was.
 //
 // Measured (8 cached heads of 128, bf16): one row and 4 query heads for 64 requests of up to 4096
 // tokens 68 us, 5.0 TB/s, bounded by memory; 17 rows for 32 requests of up to 16384 tokens 229 us,
@@ -51,7 +53,8 @@ namespace {
 constexpr int kWaves = 4;
 constexpr float kPShift = 8.f;   // P = 2^(s - m + kPShift)
 constexpr float kPLimit = 15.f;  // m moves when some s - m + kPShift passes this
-constexpr float kNoMax = -1e30f;
+constexpr float kNoMax = -3e38f;  // below every score, finite
+constexpr float kLarge = 65536.f;  // |m| from which s and m are rounded alike before the difference
 constexpr int kRefLo = -5, kRefHi = 7;  // block exponent minus reference: code * 2^that is normal
                                         // in fp16 (2^-9 * 2^-5 = 2^-14, 448 * 2^7 < 65504)
 
@@ -103,6 +106,14 @@ struct Fp16 {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
+// x y rounded by itself, never as part of a multiply-add.
+__device__ __forceinline__ float product(float x, float y) {
+#pragma clang fp contract(off)
+  float r = x * y;
+  asm("" : "+v"(r));
   return r;
 }
 
@@ -280,7 +291,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
   }
   int kref = 0, vref = 0;
   float cs = a.scale_log2;
-  bool first_tile = true;
+  bool first_tile = true, large = false;
 
   // A tile's codes stay in one set of registers: the next keys are loaded as soon as the scores
   // are made, the next values as soon as the outputs are, each behind the other's work.
@@ -398,12 +409,14 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
     for (int rt = 0; rt < RT; ++rt) {
       const f32x4 x = sc[rt][0], y = sc[rt][1];
       top[rt] = max3(max3(x[0], x[1], x[2]), max3(x[3], y[0], y[1]), max3(y[2], y[3], y[3]));
-      move |= fmaf(top[rt], cs, kPShift - mx[rt]) > kPLimit;
+      move |= product(top[rt], cs) - mx[rt] > kPLimit - kPShift;
     }
     if (__any(move)) {
+      bool wide = false;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const float m = fmaxf(mx[rt], group_max(top[rt]) * cs);
+        const float m = fmaxf(mx[rt], product(group_max(top[rt]), cs));
+        wide |= fabsf(m) > kLarge && m != kNoMax;
         const float f = __builtin_amdgcn_exp2f(mx[rt] - m);
         mx[rt] = m;
         l[rt] *= f;
@@ -413,14 +426,29 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
           o[rt][c][1] *= f;
         }
       }
+      large = __any(wide);
+    }
+    if (large) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          sc[rt][e >> 2][e & 3] = product(sc[rt][e >> 2][e & 3], cs) - mx[rt] + kPShift;
+    } else {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float bias = kPShift - mx[rt];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          sc[rt][e >> 2][e & 3] = fmaf(sc[rt][e >> 2][e & 3], cs, bias);
+      }
     }
     f16x8 p[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const float bias = kPShift - mx[rt];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float x = __builtin_amdgcn_exp2f(fmaf(sc[rt][e >> 2][e & 3], cs, bias));
+        const float x = __builtin_amdgcn_exp2f(sc[rt][e >> 2][e & 3]);
         l[rt] += x;
         p[rt][e] = (_Float16)x;
       }

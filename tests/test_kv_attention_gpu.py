@@ -373,3 +373,48 @@ def test_graph_stream_and_repeat(S):
         s.synchronize()
         assert torch.equal(mine, want)
     compare(want, model, q, table.cpu().numpy(), lens.cpu().tolist(), [4, 3], dim ** -0.5, 0, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("power", [16, 24, 27, 28, 30, 40, 60, 100])
+def test_very_large_scores(S, dtype, power):
+    """Scores of about +-2^power, where a step of fp32 passes the softmax's whole range: the token
+    that leads by more than the scores' error has all the weight (its own is rounded by 2^-11)."""
+    import torch
+
+    rng = np.random.default_rng(power)
+    heads, dim, page, T = 1, 64, 64, 3
+    dt = getattr(torch, dtype)
+    for L, width in ((70, 2), (2500, 40)):
+        model = M.Cache(width, page, heads, dim)
+        for n in "kv":
+            model.code[n] = M.encode(np.abs(rng.standard_normal(model.shape)) * 60)
+            model.exp[n][:] = -8
+        # one token far ahead, one far behind
+        model.code["k"][0, :, 5] = M.encode(np.full((heads, dim), 400.0))
+        model.code["k"][1, :, 3] = M.encode(np.full((heads, dim), 2.0 ** -5))
+        # the largest |sum q k| is about 2^15 times the units of q and of the keys
+        unit = max(-8, min(31, power - 20)) if dtype == "float16" else -8
+        model.exp["k"][:] = unit
+        big, scale = (5, 2.0 ** (power - 21 - unit)) if dtype == "float16" else \
+            (power - 16 - unit, 1.0)
+        cache = upload(S, model)
+        table = np.arange(width)[None]
+        x = np.abs(rng.standard_normal((1, T, 4, dim))) + 0.5
+        x[:, :, 1::2] *= -1
+        q = dev(x * 2.0 ** big).to(dt)
+        out = cache.attend(q, i32(table), i32([L]), scale=scale).double().cpu().numpy()
+        keys, values = (model.values(n, table[0], L)[0][:, 0] for n in "kv")
+        for t in range(T):
+            see = L - T + t + 1
+            for h in range(4):
+                row = q[0, t, h].double().cpu().numpy()
+                s = keys[:see] @ row * scale * np.log2(np.e)
+                err = 2 * (dim + 8) * 2.0 ** -24 * (np.abs(keys[:see]) @ np.abs(row)).max() * \
+                    scale * np.log2(np.e)
+                order = np.argsort(s)
+                assert s[order[-1]] - s[order[-2]] > 64 + err
+                assert 2.0 ** (power - 12) < np.abs(s).max() < 2.0 ** (power + 6)
+                want = values[order[-1]]
+                tol = (torch.finfo(dt).eps / 2 + 2.0 ** -11 + 2.0 ** -20) * np.abs(want)
+                assert (np.abs(out[0, t, h] - want) <= tol).all(), (L, t, h)
