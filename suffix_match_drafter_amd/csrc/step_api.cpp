@@ -3,8 +3,6 @@
 //
 // They need no context.  Host code checks the arguments it can see, derives the launch plan from
 // the shapes alone (never from device memory) and enqueues kernels.
-#include <cmath>
-
 #include "../../include/sfx.h"
 #include "errors.h"
 #include "kv_attention.h"
@@ -17,6 +15,8 @@ namespace {
 
 constexpr int64_t kMaxTokens = 0x7fffff00;  // positions and tile ends are int32
 constexpr int64_t kMaxGroups = 0x7fffffff;  // workgroups of one launch
+constexpr float kMaxScale = 0x1p64f;  // the softmax scale times a power of two in [2^-33, 2^30]
+                                      // has to stay a normal number
 
 bool dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
@@ -183,8 +183,8 @@ int sfx_kv_attention(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t q_
   int rc = attention_plan(cache, B, T, q_heads, max_pages, page_table, window, sinks, &a, &bytes);
   if (!rc) rc = check_type(type, false);
   if (rc) return rc;
-  if (!(scale > 0.f) || !std::isfinite(scale))
-    return fail(SFX_EINVAL, "scale=%g is not positive and finite", (double)scale);
+  if (!(scale >= 1.f / kMaxScale && scale <= kMaxScale))
+    return fail(SFX_EINVAL, "scale=%g outside [2^-64, 2^64]", (double)scale);
   if (B == 0 || T == 0) return SFX_OK;
   if (!seq_lens || !q || !out) return fail(SFX_EINVAL, "NULL array argument");
   if ((uintptr_t)out & 15) return fail(SFX_EINVAL, "out must be aligned to 16 bytes");

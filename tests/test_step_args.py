@@ -163,3 +163,11 @@ def test_model_verification_keeps_the_distribution():
                 got[s[0]] += 1
         # each border of the two grids can misplace one line of 1 / 200
         assert np.abs(got / got.sum() - p).max() <= 2 / 200
+
+
+def test_attention_scale_range():
+    """A scale whose product with a block's power of two would not be a normal number is refused."""
+    for scale in (2.0 ** 65, 2.0 ** -65, 1e-40, 3e38):
+        assert attend(cache(), scale=scale) == sfx.EINVAL, scale
+    for scale in (2.0 ** 64, 2.0 ** -64):
+        assert attend(cache(), B=0, scale=scale) == sfx.OK, scale
