@@ -694,6 +694,8 @@ class KVCache:
         to = _array(out, "out", shape, q.dtype, i)
         L = load()
         window, sinks = int(window), int(sinks)
+        if window >> 31 or sinks >> 31:
+            raise ValueError("window and sinks must be in [0, 2^31)")
         key = (B, T, H, pages, window, sinks)
         n = self._bytes.get(key)
         if n is None:

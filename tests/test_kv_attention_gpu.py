@@ -418,3 +418,13 @@ def test_very_large_scores(S, dtype, power):
                 want = values[order[-1]]
                 tol = (torch.finfo(dt).eps / 2 + 2.0 ** -11 + 2.0 ** -20) * np.abs(want)
                 assert (np.abs(out[0, t, h] - want) <= tol).all(), (L, t, h)
+
+
+def test_window_past_32_bits_is_refused(S):
+    import torch
+
+    cache = S.KVCache(1, 32, 1, 64)
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.float16, device="cuda")
+    for kw in (dict(window=2 ** 32 + 5), dict(window=2 ** 31), dict(sinks=2 ** 32), dict(sinks=-1)):
+        with pytest.raises(ValueError):
+            cache.attend(q, i32([[0]]), i32([0]), **kw)
