@@ -53,11 +53,12 @@ __device__ __forceinline__ float from_half(unsigned short b) {
   return (float)h;
 }
 
-// A logit as the sums take it: NaN is -inf (a maximum drops it); +inf becomes the largest float,
-// so that equal infinities differ by 0 and share the row.
-__device__ __forceinline__ float clean(float x) {
-  return fminf(fmaxf(x, -__builtin_inff()), 3.402823466e38f);
-}
+// A logit as the sums take it: NaN is -inf (a maximum drops it).
+__device__ __forceinline__ float clean(float x) { return fmaxf(x, -__builtin_inff()); }
+
+// x - m for x <= m.  Equal infinities differ by 0: logits of +inf share their row, and what is
+// finite beside them weighs nothing at any temperature.
+__device__ __forceinline__ float below(float x, float m) { return x == m ? 0.f : x - m; }
 
 // One logit, and eight as they lie in memory (any alignment of their type) and as floats.
 struct Bf16 {
@@ -183,9 +184,9 @@ __device__ __forceinline__ double inv64(float t) { return fmax(1.0 / (double)t, 
 
 // Two parts of a row as one; of equal largest logits the lowest index.
 __device__ __forceinline__ VerifyPart join(const VerifyPart& p, const VerifyPart& q, float c) {
-  const float m = fmaxf(p.m, q.m), z = m == -__builtin_inff() ? 0.f : m;
-  return VerifyPart{m, p.s * __builtin_amdgcn_exp2f((p.m - z) * c) +
-                           q.s * __builtin_amdgcn_exp2f((q.m - z) * c),
+  const float m = fmaxf(p.m, q.m);
+  return VerifyPart{m, p.s * __builtin_amdgcn_exp2f(below(p.m, m) * c) +
+                           q.s * __builtin_amdgcn_exp2f(below(q.m, m) * c),
                     q.m > p.m || (q.m == p.m && q.at < p.at) ? q.at : p.at, 0};
 }
 
@@ -213,7 +214,8 @@ __device__ __forceinline__ VerifyPart wave_stats(const char* row, int j, int j1,
     if (!greedy) {
       const float z = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f((x[e] - z) * c);
+      for (int e = 0; e < 8; ++e)
+        x[e] = __builtin_amdgcn_exp2f((kClean ? below(x[e], z) : x[e] - z) * c);
       s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
     }
   });
@@ -287,7 +289,7 @@ __device__ __forceinline__ Weights64 weights64(const double* table, float m, flo
 }
 
 // Sum of four weights, stage by stage: each weight is one chain of dependent instructions.  The
-// median takes a NaN and -inf to the lowest float and +inf to the largest.
+// median takes a NaN and -inf to the lowest float (+inf does not get here).
 __device__ __forceinline__ double weights4(const Weights64& w, const float* x) {
   double f[4], p[4], ts[4];
 #pragma unroll
@@ -312,7 +314,7 @@ __device__ __forceinline__ double weights4(const Weights64& w, const float* x) {
 
 // The same to the last weight above 0 that fp64 has: for draws at the very start of a row.
 __device__ __forceinline__ double weight64_full(float x, float m, double inv) {
-  return exp(((double)x - (double)m) * inv);
+  return x == m ? 1.0 : exp(((double)x - (double)m) * inv);
 }
 
 __device__ __forceinline__ double wave_sum64(double x) {
@@ -321,11 +323,17 @@ __device__ __forceinline__ double wave_sum64(double x) {
   return x;
 }
 
-// Sum of the weights of [j0, j1) (as of weights4; `skip` counts as masked), one wavefront.
+// Sum of the weights of [j0, j1) (as of weights4; `skip` counts as masked), one wavefront.  Where
+// the largest logit is +inf, its equals weigh 1 and are counted.
 template <typename T>
 __device__ __forceinline__ double wave_range64(const char* row, int j0, int j1, const Weights64& w, int skip,
                                int lane) {
   double s = 0.0;
+  if (w.m == (double)__builtin_inff()) {
+    for (int j = j0 + lane; j < j1; j += 64)
+      if (j != skip && T::get(row, j) == __builtin_inff()) s += 1.0;
+    return wave_sum64(s);
+  }
   each8<T, 4 / T::kBytes>(row, j0 + lane * 8, j1, 512, [&](float (&x)[8], int j) {
     if ((unsigned)(skip - j) < 8u)
 #pragma unroll
@@ -361,7 +369,7 @@ __device__ int test_slot(const VerifyArgs& a, int b, int slot, const VerifyPart&
   const int d = a.draft[(int64_t)b * a.k + slot];
   if (d < 0 || d >= a.V) return kReject;
   if (greedy) return p.at == d ? kAccept : kReject;
-  const float x = (logit<T>(row_ptr(a, b, slot, T::kBytes), d) - p.m) * c;
+  const float x = below(logit<T>(row_ptr(a, b, slot, T::kBytes), d), p.m) * c;
   const float w = __builtin_amdgcn_exp2f(x);
   const float uz = a.u_accept[(int64_t)b * a.k + slot] * p.s;
   const float off = uz * (3 * groups + 64) + w * (1.04f * fminf(-x, 200.f) + 4);

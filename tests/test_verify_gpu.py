@@ -314,3 +314,55 @@ def test_draws(S, dtype, B, V):
             for j in (V // 2, V // 2 + 1, V // 16 * 9, V // 16 * 9 - 1):
                 x[:, 0, j] = 11.0
         check(S, x, empty, None, empty.astype(np.float32), us, None)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("V", [300, 1024, 5000, 40001])
+@pytest.mark.parametrize("temp", [0.0, 1e-30, 1.0, 1e31, 1e38, np.inf])
+def test_infinite_logits_share_the_row(S, dtype, V, temp):
+    """Logits of +inf leave nothing to finite ones, the type's largest value among them, whatever
+    the temperature; greedy takes the first +inf.  A draft among n of them has weight 1 / n."""
+    import torch
+
+    rng = np.random.default_rng(V)
+    B, k, n = 16, 2, 4
+    x = rng.standard_normal((B, k + 1, V))
+    x = torch.from_numpy(x).to(getattr(torch, dtype)).cuda()
+    x[:, :, ::3] = torch.finfo(x.dtype).max
+    x[3, :, 1::3] = -float("inf")
+    x[5, :, 1::3] = float("nan")
+    draft = np.zeros((B, k), np.int32)
+    for b in range(B):
+        for i in range(k + 1):
+            at = rng.choice(np.arange(1, V), n, replace=False)
+            x[b, i, dev(at)] = float("inf")
+            if i < k:
+                draft[b, i] = np.sort(at)[0 if b % 4 == 0 else rng.integers(0, n)]
+    draft[15, 0] = 0  # finite
+    ua = np.full((B, k), 0.3, np.float32)
+    ua[:8] = np.nextafter(np.float32(0.25), np.float32(0))
+    ua[8:12, 1] = 0.25
+    us = rng.random(B).astype(np.float32)
+    us[0], us[1] = 0.0, np.nextafter(np.float32(1), np.float32(0))
+    check(S, x, draft, None, ua, us, np.full(B, temp, np.float32))
+
+
+@pytest.mark.parametrize("temp", [1.0, np.inf])
+def test_infinite_logits_in_phases(S, temp):
+    """The same in a call that goes through the slots in phases."""
+    import torch
+
+    rng = np.random.default_rng(9)
+    B, k, V = 26, 16, 120011
+    x = torch.zeros((B, k + 1, V), device="cuda")
+    x[:, :, ::7] = torch.finfo(x.dtype).max
+    draft = rng.integers(2000, V // 2, size=(B, k)).astype(np.int32)
+    for i in range(k + 1):
+        at = draft[:, i] if i < k else np.full(B, 77, np.int32)
+        for far in (0, -1500, 30011, 60000):
+            x[dev(np.arange(B)), i, dev(at + far).long() % V] = float("inf")
+    ua = np.full((B, k), np.nextafter(np.float32(0.25), np.float32(0)), np.float32)
+    for b in range(B):
+        ua[b, b:] = 0.25
+    us = rng.random(B).astype(np.float32)
+    check(S, x, draft, None, ua, us, np.full(B, temp, np.float32))
