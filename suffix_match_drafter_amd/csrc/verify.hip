@@ -289,13 +289,12 @@ __device__ __forceinline__ Weights64 weights64(const double* table, float m, flo
 }
 
 // Sum of four weights, stage by stage: each weight is one chain of dependent instructions.  The
-// median takes a NaN and -inf to the lowest float (+inf does not get here).
+// maximum takes -inf and NaN to the floor too, at any temperature (+inf does not get here).
 __device__ __forceinline__ double weights4(const Weights64& w, const float* x) {
   double f[4], p[4], ts[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const double d = fmax(
-        (double)__builtin_amdgcn_fmed3f(x[e], -3.402823466e38f, 3.402823466e38f) - w.m, w.lo);
+    const double d = fmax((double)x[e] - w.m, w.lo);
     const double t = fma(d, w.k, kMagic);
     const int n = (int)__double_as_longlong(t);  // low word: the integer
     f[e] = fma(d, w.k, -(t - kMagic));

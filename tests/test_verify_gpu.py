@@ -366,3 +366,79 @@ def test_infinite_logits_in_phases(S, temp):
         ua[b, b:] = 0.25
     us = rng.random(B).astype(np.float32)
     check(S, x, draft, None, ua, us, np.full(B, temp, np.float32))
+
+
+def masked_rows(rng, B, k, V, dtype):
+    """Rows with 512 tokens left: masks of -inf or NaN in one run (so that whole segments of a row
+    are masked) or scattered, and drafts among the tokens that are left."""
+    import torch
+
+    x = rng.standard_normal((B, k + 1, V))
+    draft = np.zeros((B, k), np.int32)
+    for b in range(B):
+        for i in range(k + 1):
+            first = rng.integers(0, V - 512)
+            left = np.arange(first, first + 512) if b % 2 else rng.choice(V, 512, replace=False)
+            out = np.ones(V, bool)
+            out[left] = False
+            x[b, i, out] = np.nan if b % 3 == 2 else -np.inf
+            if i < k:
+                draft[b, i] = left[rng.integers(0, 512)]
+    return torch.from_numpy(x).to(getattr(torch, dtype)).cuda(), draft
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("V", [1025, 4096, 4097, 40001])
+@pytest.mark.parametrize("temp", [1e31, 1e37, 1e38, np.inf])
+def test_masks_at_large_temperatures(S, dtype, V, temp):
+    """A masked token, and the draft that was rejected, weigh nothing at any temperature.  The 512
+    tokens that are left have a weight of 1 each, so a draft is accepted just below u = 1 / 512."""
+    rng = np.random.default_rng(V)
+    border = np.float32(1 / 512)
+    for k in (0, 3):
+        B = 24
+        x, draft = masked_rows(rng, B, k, V, dtype)
+        ua = np.full((B, k), 0.75, np.float32)
+        if k:
+            ua[:8] = np.nextafter(border, np.float32(0))
+            ua[8:12] = border
+            ua[12:16, 0] = np.nextafter(border, np.float32(0))
+        us = rng.random(B).astype(np.float32)
+        us[0], us[1] = 0.0, np.nextafter(np.float32(1), np.float32(0))
+        check(S, x, draft, None, ua, us, np.full(B, temp, np.float32))
+
+
+@pytest.mark.parametrize("temp", [1e31, np.inf])
+def test_masks_at_large_temperatures_in_phases(S, temp):
+    """The same in a call that goes through the slots in phases."""
+    import torch
+
+    rng = np.random.default_rng(7)
+    B, k, V = 26, 16, 120011
+    x = torch.full((B, k + 1, V), -float("inf"), device="cuda")
+    draft = rng.integers(512, V - 512, size=(B, k)).astype(np.int32)
+    at = dev(draft.astype(np.int64))[:, :, None] + torch.arange(-256, 256, device="cuda")
+    x[:, :k].scatter_(2, at, 0.5)
+    x[:, k, 1000:1512] = -0.25
+    border = np.float32(1 / 512)
+    ua = np.full((B, k), np.nextafter(border, np.float32(0)), np.float32)
+    for b in range(B):
+        ua[b, b:] = border if b % 2 else 0.75
+    us = rng.random(B).astype(np.float32)
+    check(S, x, draft, None, ua, us, np.full(B, temp, np.float32))
+
+
+@pytest.mark.parametrize("V", [1025, 5000, 40000])
+def test_infinities_beside_the_lowest_float(S, V):
+    """fp32 rows whose largest logit is the type's lowest value: -inf is masked all the same."""
+    import torch
+
+    rng = np.random.default_rng(V)
+    B = 8
+    x = torch.full((B, 1, V), -float("inf"), device="cuda")
+    for b in range(B):
+        x[b, 0, dev(rng.choice(V, 1 + 37 * b, replace=False))] = torch.finfo(torch.float32).min
+    empty = np.zeros((B, 0), np.int32)
+    us = rng.random(B).astype(np.float32)
+    for temp in (1e-3, 1.0, 1e31):
+        check(S, x, empty, None, empty.astype(np.float32), us, np.full(B, temp, np.float32))
