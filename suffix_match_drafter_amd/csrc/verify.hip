@@ -176,9 +176,11 @@ __device__ __forceinline__ float temperature(const VerifyArgs& a, int b) {
   return a.temperature ? a.temperature[b] : 1.f;
 }
 // log2(e) / T and 1 / T, finite and above 0 whatever T > 0 is, so that 0 and -inf times it stay
-// 0 and -inf.
+// 0 and -inf.  In fp32 the range is narrower than T's; beyond it the fp32 sums decide nothing
+// (test_slot).
+constexpr float kInvLo = 1e-30f, kInvHi = 1e30f;
 __device__ __forceinline__ float inv_log2(float t) {
-  return fminf(fmaxf(1.4426950408889634f / t, 1e-30f), 1e30f);
+  return fminf(fmaxf(1.4426950408889634f / t, kInvLo), kInvHi);
 }
 __device__ __forceinline__ double inv64(float t) { return fmax(1.0 / (double)t, 1e-300); }
 
@@ -368,6 +370,7 @@ __device__ int test_slot(const VerifyArgs& a, int b, int slot, const VerifyPart&
   const int d = a.draft[(int64_t)b * a.k + slot];
   if (d < 0 || d >= a.V) return kReject;
   if (greedy) return p.at == d ? kAccept : kReject;
+  if (c <= kInvLo || c >= kInvHi) return kClose;  // another temperature than the request's
   const float x = below(logit<T>(row_ptr(a, b, slot, T::kBytes), d), p.m) * c;
   const float w = __builtin_amdgcn_exp2f(x);
   const float uz = a.u_accept[(int64_t)b * a.k + slot] * p.s;

@@ -442,3 +442,65 @@ def test_infinities_beside_the_lowest_float(S, V):
     us = rng.random(B).astype(np.float32)
     for temp in (1e-3, 1.0, 1e31):
         check(S, x, empty, None, empty.astype(np.float32), us, np.full(B, temp, np.float32))
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("V", [300, 1025, 4097, 40001])
+@pytest.mark.parametrize("temp", [1e29, 2e30, 1e31, 1e37, 1e38, 3e38, np.inf])
+def test_finite_masks_at_large_temperatures(S, dtype, V, temp):
+    """The type's lowest value is a logit like another: at a temperature as large as itself it has
+    a weight, with which drafts are accepted and tokens drawn."""
+    import torch
+
+    rng = np.random.default_rng(V)
+    B, k = 24, 3
+    x, draft, nv, ua, us, _ = case(rng, B, k, V, dtype)
+    nv[:] = k
+    low = torch.finfo(x.dtype).min
+    left = V // 3
+    for b in range(B):
+        x[b, :, left:] = low
+        draft[b] = rng.integers(0, left if b % 3 else V, size=k)
+        if b % 4 == 0:
+            x[b, :, 2 * left:] = -float("inf")
+        if b % 4 == 1:
+            x[b, :, :left] = torch.finfo(x.dtype).max
+    # about the weight of a masked and of another draft
+    ua[:] = rng.choice([0.5, 0.9, 1.1, 2.0], (B, k)) / V
+    check(S, x, draft, nv, ua, us, np.full(B, temp, np.float32))
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("V", [300, 5000, 40001])
+@pytest.mark.parametrize("temp", [1e-29, 1e-30, 1e-31, 1e-35, 1e-38])
+def test_small_temperatures_of_small_logits(S, dtype, V, temp):
+    """Logits that differ by some temperatures, however small these are."""
+    import torch
+
+    rng = np.random.default_rng(V)
+    B, k = 16, 3
+    x = torch.from_numpy(rng.standard_normal((B, k + 1, V)) * 2 * max(temp, 1e-34))
+    draft = rng.integers(0, V, size=(B, k)).astype(np.int32)
+    at = torch.from_numpy(draft).long()[:, :, None]
+    x[:, :k].scatter_(2, at, (np.log(V) + rng.uniform(-3, 3)) * temp)
+    x = x.to(getattr(torch, dtype)).cuda()
+    ua, us = rng.random((B, k)).astype(np.float32), rng.random(B).astype(np.float32)
+    check(S, x, draft, None, ua, us, np.full(B, temp, np.float32))
+
+
+@pytest.mark.parametrize("temp", [3e38, 1e-31])
+def test_extreme_temperatures_in_phases(S, temp):
+    """The same in a call that goes through the slots in phases."""
+    import torch
+
+    rng = np.random.default_rng(10)
+    B, k, V = 26, 16, 120011
+    g = torch.Generator(device="cuda")
+    g.manual_seed(10)
+    unit = 0.5 * temp
+    x = torch.randn((B, k + 1, V), generator=g, device="cuda").clamp_(-1, 1) * unit
+    draft = rng.integers(0, V, size=(B, k)).astype(np.int32)
+    x[:, :k].scatter_(2, dev(draft).long()[:, :, None], unit * 1.5 if temp > 1 else unit * 24)
+    ua = rng.random((B, k)).astype(np.float32) * (3.0 / V if temp > 1 else 1.0)
+    us = rng.random(B).astype(np.float32)
+    check(S, x, draft, None, ua.astype(np.float32), us, np.full(B, temp, np.float32))
