@@ -501,7 +501,8 @@ int sfx_kv_attention(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t q_
  *   (NULL: k).  u_accept [B, k], u_sample [B]: uniform in [0, 1).
  *   sampled [B, k + 1] receives the accepted tokens, then the drawn one, then -1;
  *   num_accepted [B] the number accepted.  A row with no token above -inf draws -1.
- * Comparisons are decided as in exact arithmetic up to fp64 rounding.  k within [0, 32].
+ * Comparisons are made in fp64, of weights within 2^-42 of exp((logit - largest) / temperature),
+ * relatively; those below e^-700 count as e^-700 in a row's sum.  k within [0, 32].
  * workspace: sfx_verify_workspace_bytes, aligned to 16 bytes. */
 int sfx_verify_workspace_bytes(int32_t B, int32_t k, int32_t V, int32_t type, size_t* bytes);
 int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batch_stride,

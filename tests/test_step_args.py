@@ -171,3 +171,31 @@ def test_attention_scale_range():
         assert attend(cache(), scale=scale) == sfx.EINVAL, scale
     for scale in (2.0 ** 64, 2.0 ** -64):
         assert attend(cache(), B=0, scale=scale) == sfx.OK, scale
+
+
+def test_verification_weights_keep_their_bound():
+    """The bound that the header states for sfx_verify's fp64 weights, over the kernel's arithmetic
+    (a table of 2^(i / 256) and a cubic) with every operation rounded as there."""
+    import os
+
+    text = open(os.path.join(os.path.dirname(sfx.__file__), "..", "include", "sfx.h")).read()
+    assert "within 2^-42 of exp" in text and "up to fp64 rounding" not in text
+    z, magic = np.log(2.0) / 256, 1.5 * 2.0 ** 52
+    wide = np.longdouble
+
+    def fma(a, b, c):
+        return np.float64(wide(a) * wide(b) + wide(c))
+
+    rng = np.random.default_rng(0)
+    for temp in (0.3, 0.7, 1.0, 1.7, 30.0):
+        for reach in (1.0, 20.0, 700.0):
+            d = -rng.uniform(0, reach, 20000) * temp
+            k = np.float64(1.0 / temp) * (256 * np.float64(np.log2(np.e)))
+            n = fma(d, k, magic) - magic
+            f = fma(d, k, -n)
+            n = n.astype(np.int64)
+            t = np.ldexp(np.exp2((n & 255) / 256.0), (n >> 8).astype(np.int32))
+            p = fma(f, fma(f, z ** 3 / 6, z * z / 2), z)
+            got = fma(t, p * f, t)
+            want = np.exp(wide(d) / wide(temp))
+            assert np.abs(wide(got) / want - 1).max() <= 2.0 ** -42, (temp, reach)
