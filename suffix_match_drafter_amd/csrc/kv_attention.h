@@ -21,7 +21,7 @@ struct KvAttentionArgs {
   int32_t splits;           // workgroups over the tokens
   int32_t tiles_per_split;  // 32-token tiles of one split
   float* part_o;            // [splits][B * heads * T * group][dim]  (splits > 1)
-  float* part_lse;          // [splits][B * heads * T * group]
+  float2* part_ml;          // [splits][B * heads * T * group]: maximum, sum
 };
 
 // Fills the plan from the shapes; returns the workspace bytes it needs.

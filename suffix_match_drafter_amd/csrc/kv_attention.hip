@@ -536,8 +536,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
 #pragma unroll
           for (int e = 0; e < kPer; e += 4)
             *(f32x4*)(a.part_o + at * D + d + e) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
-          if (d == 0)
-            a.part_lse[at] = none ? -__builtin_inff() : mm + __builtin_amdgcn_logf(ll);
+          if (d == 0) a.part_ml[at] = none ? float2{-__builtin_inff(), 0.f} : float2{mm, ll};
         } else {
           const int64_t at =
               ((int64_t)b * a.T + row / a.group) * a.c.heads * a.group + h * a.group +
@@ -555,6 +554,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
 // Joins the splits of the rows that had more than one: D / 4 lanes hold a row, kGroups such groups
 // take every kGroups-th split and meet in LDS.  With many splits one group alone would wait for
 // its loads again and again (10 us for 64 splits of 65 rows, 4 with all of a workgroup on a row).
+// A split brings its maximum and its sum apart: as one logarithm the sum would be rounded to the
+// maximum's step, 4% of a split's weight at scores of 2^20 and all of it at 2^28.
 template <typename T, int D, int kGroups>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chunk_rows) {
   constexpr int kLanes = D / 4, kRows = 256 / kLanes / kGroups;
@@ -574,17 +575,17 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chu
   float m = -__builtin_inff(), l = 0.f;
   f32x4 x{0, 0, 0, 0};
   for (int i = group; active > 1 && i < active; i += 8 * kGroups) {
-    float e[8];
+    float2 ml[8];
     f32x4 o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int j = i + k * kGroups < active ? i + k * kGroups : i;
-      e[k] = a.part_lse[j * rows + at];
+      ml[k] = a.part_ml[j * rows + at];
       o[k] = *(const f32x4*)(a.part_o + (j * rows + at) * D + d);
     }
     float top = m;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, e[k]);
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
     const float z = top == -__builtin_inff() ? 0.f : top;
     const float f = __builtin_amdgcn_exp2f(m - z);
     x *= f;
@@ -593,9 +594,10 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chu
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (i + k * kGroups < active) {
-        const float w = __builtin_amdgcn_exp2f(e[k] - z);  // 0 for a split that saw nothing
+        // 0 for a split that saw nothing
+        const float w = __builtin_amdgcn_exp2f(ml[k].x - z) * ml[k].y;
         l += w;
-        x += e[k] == -__builtin_inff() ? f32x4{0, 0, 0, 0} : w * o[k];
+        x += w * o[k];
       }
   }
   if constexpr (kGroups > 1) {
@@ -669,13 +671,13 @@ size_t kv_attention_plan(KvAttentionArgs* a, int dim) {
   a->splits = (int)splits;
   if (splits == 1) return 0;
   const size_t rows = (size_t)a->B * a->c.heads * a->T * a->group;
-  return (size_t)splits * rows * (dim + 1) * sizeof(float);
+  return (size_t)splits * rows * (dim + 2) * sizeof(float);
 }
 
 void kv_attention_place(KvAttentionArgs* a, int dim, void* workspace) {
   const size_t rows = (size_t)a->B * a->c.heads * a->T * a->group;
   a->part_o = (float*)workspace;
-  a->part_lse = a->part_o + (size_t)a->splits * rows * dim;
+  a->part_ml = (float2*)(a->part_o + (size_t)a->splits * rows * dim);
 }
 
 namespace {

@@ -428,3 +428,43 @@ def test_window_past_32_bits_is_refused(S):
     for kw in (dict(window=2 ** 32 + 5), dict(window=2 ** 31), dict(sinks=2 ** 32), dict(sinks=-1)):
         with pytest.raises(ValueError):
             cache.attend(q, i32([[0]]), i32([0]), **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("power", [8, 16, 18, 20, 24, 28, 34])
+@pytest.mark.parametrize("counts", [(48, 16, 0, 5), (1, 300, 7, 0), (3, 1, 1, 1)], ids=str)
+def test_equal_large_scores(S, dtype, power, counts):
+    """Tokens of one key, whose scores of +-2^power are equal to the last bit, share the softmax
+    equally however they are spread over a long request's splits; all others are far behind.  So
+    the scores' error does not count: the result's own rounding, the weights' 2^-11 and the fp32
+    sums do."""
+    import torch
+
+    rng = np.random.default_rng(power)
+    heads, dim, page, width, run = 1, 64, 64, 40, 512
+    L = width * page
+    dt = getattr(torch, dtype)
+    lead = np.concatenate([512 * i + rng.choice(run, n, replace=False)
+                           for i, n in enumerate(counts)])
+    for sign in (1, -1):
+        # the other tokens' scores are -7 2^power
+        key = np.full((L, heads, dim), -448.0)
+        key[lead] = sign * 64.0
+        value = rng.standard_normal((L, heads, dim)) * 100
+        value[lead] = np.where(lead % 2 == 0, 64.0, -8.0)[:, None, None]
+        model = M.Cache(width, page, heads, dim)
+        for n, x in (("k", key), ("v", value)):
+            model.code[n] = M.encode(x).reshape(width, page, heads, dim).transpose(0, 2, 1, 3)
+        model.exp["k"][:], model.exp["v"][:] = -6, -3
+        cache = upload(S, model)
+        scale = 2.0 ** (power - 6)  # 64 dims of q = 1 and |k| = 1
+        values = model.values("v", np.arange(width), L)[0][:, 0]
+        want = values[lead].mean(0)
+        tol = torch.finfo(dt).eps / 2 * np.abs(want) + \
+            np.abs(values[lead]).mean(0) * (2.0 ** -11 + (L / 32 + 64) * 2.0 ** -23)
+        q = torch.ones((1, 1, 2, dim), dtype=dt, device="cuda")
+        for B in (1, 800):  # split; as many requests as the card takes without
+            table = i32(np.arange(width)[None].repeat(B, 0))
+            out = cache.attend(q.expand(B, 1, 2, dim), table, i32([L] * B), scale=scale)
+            got = out.double().cpu().numpy()
+            assert (np.abs(got - want) <= tol).all(), (sign, B, got[0, 0, 0, 0], want[0])
