@@ -102,11 +102,10 @@ struct Fp16 {
   }
 };
 
-// Three-way maximum of scores as they come from the matrix unit (fmaxf would first quiet each).
+// Three-way maximum of scores as they come from the matrix unit, one instruction (fmaxf would first
+// quiet each operand).  A NaN among them stays one: its row is NaN whatever its maximum is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // x y rounded by itself, never as part of a multiply-add.

@@ -468,3 +468,29 @@ def test_equal_large_scores(S, dtype, power, counts):
             out = cache.attend(q.expand(B, 1, 2, dim), table, i32([L] * B), scale=scale)
             got = out.double().cpu().numpy()
             assert (np.abs(got - want) <= tol).all(), (sign, B, got[0, 0, 0, 0], want[0])
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_nan_key_among_growing_scores(S, dtype):
+    """A NaN key in a tile that every row of its request sees, before and after tiles that move the
+    maximum: that request is NaN, the other is not."""
+    import torch
+
+    rng = np.random.default_rng(23)
+    heads, dim, page, width = 1, 128, 64, 6
+    L = 300
+    cache, model = filled(S, rng, 2 * width, page, heads, dim)
+    base = np.sign(rng.standard_normal(dim))
+    grow = np.linspace(0, 200, width * page)[:, None, None] * base
+    for b in range(2):
+        model.code["k"][b * width:(b + 1) * width] = M.encode(grow).reshape(
+            width, page, heads, dim).transpose(0, 2, 1, 3)
+    table = np.arange(2 * width).reshape(2, width)
+    q = dev(np.tile(base, (2, 3, 4, 1))).to(getattr(torch, dtype))
+    for tok in (0, 130, 250):
+        keep = model.code["k"].copy()
+        model.code["k"][table[0][tok // page], :, tok % page, 7] = 255
+        out = upload(S, model).attend(q, i32(table), i32([L, L]))
+        model.code["k"] = keep
+        assert torch.isnan(out[0]).all()
+        compare(out[1:], model, q[1:], table[1:], [L], None, dim ** -0.5, 0, 0)

@@ -199,3 +199,16 @@ def test_verification_weights_keep_their_bound():
             got = fma(t, p * f, t)
             want = np.exp(wide(d) / wide(temp))
             assert np.abs(wide(got) / want - 1).max() <= 2.0 ** -42, (temp, reach)
+
+
+def test_attention_leaves_matrix_results_to_the_compiler():
+    """The wait states between a matrix instruction and a read of its result are put in by the
+    compiler, which does not look into inline assembly: the attention has none with instructions."""
+    import os
+    import re
+
+    path = os.path.join(os.path.dirname(sfx.__file__), "csrc", "kv_attention.hip")
+    code = re.sub(r"//[^\n]*", "", open(path).read())
+    texts = re.findall(r"\basm\b\s*(?:volatile\s*)?\(\s*\"([^\"]*)\"", code)
+    assert len(texts) == len(re.findall(r"\b(?:__)?asm(?:__)?\b", code))
+    assert all(t == "" for t in texts), texts
