@@ -27,6 +27,9 @@ struct KvAttentionArgs {
 // Fills the plan from the shapes; returns the workspace bytes it needs.
 size_t kv_attention_plan(KvAttentionArgs* a, int dim);
 
+// Threads of the planned launch (the join has fewer: calls that split have few rows).
+int64_t kv_attention_threads(const KvAttentionArgs& a);
+
 // Places the plan's buffers in the workspace.
 void kv_attention_place(KvAttentionArgs* a, int dim, void* workspace);
 

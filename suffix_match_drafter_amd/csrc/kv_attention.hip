@@ -673,6 +673,19 @@ size_t kv_attention_plan(KvAttentionArgs* a, int dim) {
   return (size_t)splits * rows * (dim + 2) * sizeof(float);
 }
 
+namespace {
+
+// Groups of eight workgroups, one per XCD: see the kernel's decoding of its index.
+int64_t grid_of(const KvAttentionArgs& a) {
+  return ((int64_t)a.B * a.c.heads * a.splits + 7) / 8 * 8 * a.chunks;
+}
+
+}  // namespace
+
+int64_t kv_attention_threads(const KvAttentionArgs& a) {
+  return a.B > 0 && a.T > 0 ? grid_of(a) * 64 * kWaves : 0;
+}
+
 void kv_attention_place(KvAttentionArgs* a, int dim, void* workspace) {
   const size_t rows = (size_t)a->B * a->c.heads * a->T * a->group;
   a->part_o = (float*)workspace;
@@ -685,8 +698,7 @@ template <typename T, int D>
 hipError_t launch_dim(const KvAttentionArgs& a, hipStream_t st) {
   int chunks = 0;
   const int rt = row_tiles(a, D, &chunks);
-  const int64_t groups = (int64_t)a.B * a.c.heads * a.splits;
-  const dim3 grid((unsigned)((groups + 7) / 8 * 8 * a.chunks));
+  const dim3 grid((unsigned)grid_of(a));
   const dim3 block(64 * kWaves);
   if (rt == 1)
     hipLaunchKernelGGL((kv_attention_kernel<T, D, 1>), grid, block, 0, st, a);

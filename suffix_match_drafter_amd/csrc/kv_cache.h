@@ -49,6 +49,17 @@ struct KvMoveArgs {
   KvStrides ks, vs;
 };
 
+constexpr int kKvMoveWaves = 4;  // wavefronts of a workgroup of the write and the read
+
+// Blocks that T tokens can touch, whatever the start.
+inline int64_t kv_blocks_of(int T) { return ((int64_t)T + kKvBlock - 2) / kKvBlock + 1; }
+
+// Threads of a write's or read's launch: one wavefront per (request, block, tensor, head).
+inline __int128 kv_move_threads(int B, int T, int heads) {
+  const __int128 units = __int128(B) * kv_blocks_of(T) * 2 * heads;
+  return (units + kKvMoveWaves - 1) / kKvMoveWaves * (64 * kKvMoveWaves);
+}
+
 hipError_t launch_kv_write(const KvMoveArgs& a, int dim, KvType type, hipStream_t st);
 hipError_t launch_kv_read(const KvMoveArgs& a, int dim, KvType type, hipStream_t st);
 

@@ -21,8 +21,6 @@ namespace sfx {
 
 namespace {
 
-constexpr int kWavesPerGroup = 4;
-
 // 16-byte vectors that need only their elements' alignment (gfx950 loads and stores them at any
 // address): inputs may be slices of a fused projection with odd strides.
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
@@ -376,7 +374,7 @@ struct Unit {
 };
 __device__ __forceinline__ Unit unit_of(int heads, int nb) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // a scalar to the compiler
-  unsigned u = blockIdx.x * kWavesPerGroup + wave;  // below 2^31 + 4
+  unsigned u = blockIdx.x * kKvMoveWaves + wave;  // below 2^26 + 4
   Unit r;
   r.h = u % heads;
   u /= heads;
@@ -388,7 +386,7 @@ __device__ __forceinline__ Unit unit_of(int heads, int nb) {
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(64 * kWavesPerGroup) void kv_write_kernel(KvMoveArgs a, int nb) {
+__global__ __launch_bounds__(64 * kKvMoveWaves) void kv_write_kernel(KvMoveArgs a, int nb) {
   const int lane = threadIdx.x & 63;
   const Unit u = unit_of(a.c.heads, nb);
   if (u.b >= a.B) return;
@@ -533,9 +531,9 @@ __device__ void read_block(const KvMoveArgs& a, int b, int h, int64_t block, int
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(64 * kWavesPerGroup) void kv_read_kernel(KvMoveArgs a, int nb) {
+__global__ __launch_bounds__(64 * kKvMoveWaves) void kv_read_kernel(KvMoveArgs a, int nb) {
   const int lane = threadIdx.x & 63;
-  __shared__ u32x4 turn[kWavesPerGroup][ReadLds<T, D>::kVecs];
+  __shared__ u32x4 turn[kKvMoveWaves][ReadLds<T, D>::kVecs];
   const Unit u = unit_of(a.c.heads, nb);
   if (u.b >= a.B) return;
   u32x4* mine = turn[threadIdx.x >> 6];
@@ -551,19 +549,15 @@ __global__ __launch_bounds__(64 * kWavesPerGroup) void kv_read_kernel(KvMoveArgs
     read_block<T, D, false>(a, u.b, u.h, block, start, count, lane, mine);
 }
 
-// Blocks that T tokens can touch, whatever the start.
-int blocks_of(int T) { return (int)(((int64_t)T + kKvBlock - 2) / kKvBlock + 1); }
-
 template <template <typename, int> class K>
 hipError_t dispatch(const KvMoveArgs& a, int dim, KvType type, hipStream_t st) {
   if (a.B <= 0 || a.T <= 0) return hipSuccess;
-  const int nb = blocks_of(a.T);
-  const int64_t units = (int64_t)a.B * nb * 2 * a.c.heads;
-  const dim3 grid((unsigned)((units + kWavesPerGroup - 1) / kWavesPerGroup));
+  const int nb = (int)kv_blocks_of(a.T);
+  const dim3 grid((unsigned)(kv_move_threads(a.B, a.T, a.c.heads) / (64 * kKvMoveWaves)));
   auto pick = [&](auto t) {
     using T = decltype(t);
     auto f = dim == 64 ? K<T, 64>::get() : dim == 128 ? K<T, 128>::get() : K<T, 256>::get();
-    hipLaunchKernelGGL(f, grid, dim3(64 * kWavesPerGroup), 0, st, a, nb);
+    hipLaunchKernelGGL(f, grid, dim3(64 * kKvMoveWaves), 0, st, a, nb);
   };
   if (type == kBf16)
     pick(Bf16{});

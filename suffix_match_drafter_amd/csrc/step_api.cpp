@@ -14,9 +14,12 @@ using namespace sfx;
 namespace {
 
 constexpr int64_t kMaxTokens = 0x7fffff00;  // positions and tile ends are int32
-constexpr int64_t kMaxGroups = 0x7fffffff;  // workgroups of one launch
+constexpr int64_t kMaxRows = 0x7fffffff;    // query rows of one call
+constexpr int64_t kMaxThreads = 0xffffffff;  // of one launch: the runtime counts them in 32 bits
 constexpr float kMaxScale = 0x1p64f;  // the softmax scale times a power of two in [2^-33, 2^30]
                                       // has to stay a normal number
+
+using Wide = __int128;  // products of three 32-bit sizes
 
 bool dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
@@ -79,8 +82,8 @@ int move_args(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t max_pages
   if (rc) return rc;
   if (B == 0 || T == 0) return SFX_OK;
   if (!start || !k || !v) return fail(SFX_EINVAL, "NULL array argument");
-  const int64_t units = (int64_t)B * ((int64_t)T / kKvBlock + 2) * 2 * cache->kv_heads;
-  if (units > kMaxGroups) return fail(SFX_ECAPACITY, "B=%d T=%d is too large for one call", B, T);
+  if (kv_move_threads(B, T, cache->kv_heads) > kMaxThreads)
+    return fail(SFX_ECAPACITY, "B=%d T=%d is too large for one call", B, T);
   a->B = B;
   a->T = T;
   a->max_pages = max_pages;
@@ -111,10 +114,10 @@ int attention_plan(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t q_he
   a->page_table = page_table;
   a->window = window;
   a->sinks = sinks;
-  if ((int64_t)T * a->group > (1 << 30) || (int64_t)B * T * q_heads > kMaxGroups)
+  if ((int64_t)T * a->group > (1 << 30) || Wide(B) * T * q_heads > kMaxRows)
     return fail(SFX_ECAPACITY, "B=%d T=%d q_heads=%d is too large for one call", B, T, q_heads);
   *bytes = kv_attention_plan(a, cache->head_dim);
-  if (((int64_t)B * cache->kv_heads * a->splits + 8) * a->chunks > kMaxGroups)
+  if (kv_attention_threads(*a) > kMaxThreads)
     return fail(SFX_ECAPACITY, "B=%d T=%d q_heads=%d is too large for one call", B, T, q_heads);
   return SFX_OK;
 }
@@ -129,7 +132,7 @@ int verify_shape(int32_t B, int32_t k, int32_t V, int32_t type, VerifyArgs* a, s
   a->k = k;
   a->V = V;
   *bytes = verify_plan(a, kv_type(type));
-  if ((int64_t)B * (k + 1) * a->parts > kMaxGroups)
+  if (verify_threads(*a) > kMaxThreads)
     return fail(SFX_ECAPACITY, "B=%d k=%d V=%d is too large for one call", B, k, V);
   return SFX_OK;
 }

@@ -47,6 +47,9 @@ constexpr int kVerifyMaxOrdered = 2048;  // requests of an in_order call (a list
 // Fills the plan from the shapes; returns the workspace bytes it needs.
 size_t verify_plan(VerifyArgs* a, KvType type);
 
+// Threads of the largest of the planned launches.
+int64_t verify_threads(const VerifyArgs& a);
+
 // Places the plan's buffers in the workspace.
 void verify_place(VerifyArgs* a, void* workspace);
 

@@ -852,6 +852,13 @@ size_t verify_plan(VerifyArgs* a, KvType type) {
   return size;
 }
 
+int64_t verify_threads(const VerifyArgs& a) {
+  const int64_t draws = (int64_t)a.B * a.pieces * kRowThreads;
+  if (a.small || a.in_order) return draws;
+  const int64_t parts = (int64_t)a.B * (a.k + 1) * a.parts * kPartThreads;
+  return parts > draws ? parts : draws;
+}
+
 void verify_place(VerifyArgs* a, void* workspace) {
   const size_t rows = (size_t)a->B * (a->k + 1);
   a->part = (VerifyPart*)workspace;

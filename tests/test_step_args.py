@@ -212,3 +212,37 @@ def test_attention_leaves_matrix_results_to_the_compiler():
     texts = re.findall(r"\basm\b\s*(?:volatile\s*)?\(\s*\"([^\"]*)\"", code)
     assert len(texts) == len(re.findall(r"\b(?:__)?asm(?:__)?\b", code))
     assert all(t == "" for t in texts), texts
+
+
+def test_launches_that_the_runtime_would_refuse():
+    """A launch has at most 2^32 - 1 threads: larger calls are refused as too large, by the size
+    queries too, and the largest ones that fit are not."""
+    L = sfx.load()
+    n = ctypes.c_size_t()
+
+    def attention_bytes(B, T=1, heads=8, H=8, mp=2):
+        c = cache(kv_heads=heads)
+        return L.sfx_kv_attention_workspace_bytes(ctypes.byref(c), B, T, H, mp, 0, 0,
+                                                  ctypes.byref(n))
+
+    def verify_bytes(B, k, V):
+        return L.sfx_verify_workspace_bytes(B, k, V, 0, ctypes.byref(n))
+
+    # one workgroup of 256 threads per request and head
+    assert attention_bytes((1 << 21) - 1) == sfx.OK
+    assert attention_bytes(1 << 21) == sfx.ECAPACITY
+    assert attend(cache(kv_heads=8), B=1 << 21, H=8) == sfx.ECAPACITY
+    assert attention_bytes(1 << 21, T=0) == sfx.OK                     # no launch
+    # 1024 threads a request; at larger vocabularies 256 a row and more
+    assert verify_bytes((1 << 22) - 1, 0, 10) == verify_bytes((1 << 22) - 1, 3, 4096) == sfx.OK
+    assert verify_bytes(1 << 22, 0, 10) == sfx.ECAPACITY
+    assert verify(B=1 << 22, k=0, V=10) == sfx.ECAPACITY
+    assert verify_bytes(508400, 32, 5000) == sfx.OK
+    assert verify_bytes(508401, 32, 5000) == sfx.ECAPACITY
+    # one wavefront per request, block, tensor and head
+    for fn in ("sfx_kv_write", "sfx_kv_read"):
+        assert write(cache(), B=1 << 24, fn=fn) == sfx.ECAPACITY
+        assert write(cache(kv_heads=2 ** 31 - 1), B=2 ** 31 - 1, T=2 ** 31 - 1,
+                     fn=fn) == sfx.ECAPACITY
+    # products past 64 bits
+    assert attention_bytes(2 ** 31 - 1, T=1, heads=2 ** 31 - 1, H=2 ** 31 - 1) == sfx.ECAPACITY
