@@ -560,6 +560,11 @@ def _array(t, name, shape, dtype, index):
     return t.data_ptr()
 
 
+def _too_large(*sizes):
+    """Sizes go to the library as int32, where larger ones would arrive as others."""
+    raise ValueError(f"sizes {sizes}: each must be in [0, 2^31)")
+
+
 def _heads(t, name, heads, dim, index):
     """A [B, T, heads, dim] tensor of any batch, token and head strides."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES or t.get_device() != index:
@@ -592,6 +597,8 @@ class KVCache:
             raise ValueError("page_size must be a multiple of 32 in [32, 2048]")
         if num_pages < 0 or kv_heads < 1:
             raise ValueError("num_pages must not be negative, kv_heads at least 1")
+        if (num_pages | kv_heads) >> 31:
+            _too_large(num_pages, kv_heads)
         codes = self.shapes(num_pages, page_size, kv_heads, head_dim)
         if buffers is None:
             dev = torch.device(device)
@@ -638,11 +645,13 @@ class KVCache:
         shape = _heads(k, "k", self.kv_heads, self.head_dim, i)
         if _heads(v, "v", self.kv_heads, self.head_dim, i) != shape or v.dtype is not k.dtype:
             raise ValueError("k and v differ in shape or type")
-        B = shape[0]
+        B, T = shape[0], shape[1]
         tab, pages = self._table(page_table, B)
+        if (B | T | pages) >> 31:
+            _too_large(B, T, pages)
         st = _array(start, "start", (B,), torch.int32, i)
         ct = None if count is None else _array(count, "count", (B,), torch.int32, i)
-        _check(load().sfx_kv_write(self._p, B, shape[1], pages, tab, st, ct, k.data_ptr(),
+        _check(load().sfx_kv_write(self._p, B, T, pages, tab, st, ct, k.data_ptr(),
                                    _strides(k), v.data_ptr(), _strides(v), _TYPES[k.dtype],
                                    _raw_stream(stream, i)))
 
@@ -654,11 +663,13 @@ class KVCache:
         _on(i)
         if dtype not in _TYPES:
             raise TypeError("dtype must be bfloat16, float16 or float32")
-        B = page_table.shape[0]
+        B, T = page_table.shape[0], int(T)
         tab, pages = self._table(page_table, B)
+        if (B | T | pages) >> 31:
+            _too_large(B, T, pages)
         st = _array(start, "start", (B,), torch.int32, i)
         ct = None if count is None else _array(count, "count", (B,), torch.int32, i)
-        shape = (B, int(T), self.kv_heads, self.head_dim)
+        shape = (B, T, self.kv_heads, self.head_dim)
         if k is None:
             k = _empty(shape, dtype, self.device, stream)
         elif _heads(k, "k", self.kv_heads, self.head_dim, i) != shape or k.dtype is not dtype:
@@ -668,7 +679,7 @@ class KVCache:
                 _empty(shape, dtype, self.device, stream)
         elif _heads(v, "v", self.kv_heads, self.head_dim, i) != shape or v.dtype is not dtype:
             raise ValueError(f"v must be {shape} of {dtype}")
-        _check(load().sfx_kv_read(self._p, B, shape[1], pages, tab, st, ct, k.data_ptr(),
+        _check(load().sfx_kv_read(self._p, B, T, pages, tab, st, ct, k.data_ptr(),
                                   _strides(k), v.data_ptr(), _strides(v), _TYPES[dtype],
                                   _raw_stream(stream, i)))
         return k, v
@@ -688,10 +699,6 @@ class KVCache:
         tab, pages = self._table(page_table, B)
         sl = _array(seq_lens, "seq_lens", (B,), torch.int32, i)
         ql = None if q_lens is None else _array(q_lens, "q_lens", (B,), torch.int32, i)
-        if out is None:
-            out = torch.empty_like(q) if stream is None and q.is_contiguous() else \
-                _empty(shape, q.dtype, self.device, stream)
-        to = _array(out, "out", shape, q.dtype, i)
         L = load()
         window, sinks = int(window), int(sinks)
         if window >> 31 or sinks >> 31:
@@ -699,11 +706,17 @@ class KVCache:
         key = (B, T, H, pages, window, sinks)
         n = self._bytes.get(key)
         if n is None:
+            if (B | T | H | pages) >> 31:
+                _too_large(B, T, H, pages)
             size = ctypes.c_size_t(0)
             _check(L.sfx_kv_attention_workspace_bytes(self._p, *key, ctypes.byref(size)))
             if len(self._bytes) >= 1024:
                 self._bytes.clear()
             n = self._bytes[key] = size.value
+        if out is None:
+            out = torch.empty_like(q) if stream is None and q.is_contiguous() else \
+                _empty(shape, q.dtype, self.device, stream)
+        to = _array(out, "out", shape, q.dtype, i)
         ws = _empty((n,), torch.uint8, self.device, stream) if n else None
         _check(L.sfx_kv_attention(self._p, B, T, H, pages, tab, sl, ql, q.data_ptr(),
                                   _strides(q), to, _TYPES[q.dtype],
@@ -748,6 +761,8 @@ def verify(logits, draft, num_valid, u_accept, u_sample, temperature=None, sampl
     key = (B, k1 - 1, V, _TYPES[logits.dtype])
     n = _verify_bytes.get(key)
     if n is None:
+        if (B | k1 | V) >> 31:
+            _too_large(B, k1, V)
         size = ctypes.c_size_t(0)
         _check(L.sfx_verify_workspace_bytes(*key, ctypes.byref(size)))
         if len(_verify_bytes) >= 1024:

@@ -287,3 +287,18 @@ def test_graph_and_stream(S):
         model.write("k", k[1][b], table[b], a, T)
         model.write("v", v[1][b], table[b], a, T)
     check(cache, model)
+
+
+def test_sizes_past_32_bits_are_refused(S):
+    """2^32 + 1 tokens (of one token's memory) would reach the library as 1."""
+    import torch
+
+    cache = S.KVCache(1, 32, 1, 64)
+    table, start, far = i32([[0]]), i32([0]), 2 ** 32 + 1
+    x = torch.ones((1, 1, 1, 64), dtype=torch.bfloat16, device="cuda").expand(1, far, 1, 64)
+    for call in (lambda: cache.write(x, x, table, start, i32([5])),
+                 lambda: cache.read(table, start, None, far, k=x, v=x),
+                 lambda: cache.attend(x, table, start)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    assert not cache.k.any().item()

@@ -246,3 +246,10 @@ def test_launches_that_the_runtime_would_refuse():
                      fn=fn) == sfx.ECAPACITY
     # products past 64 bits
     assert attention_bytes(2 ** 31 - 1, T=1, heads=2 ** 31 - 1, H=2 ** 31 - 1) == sfx.ECAPACITY
+
+
+def test_sizes_past_32_bits_are_refused():
+    """They would reach the library modulo 2^32."""
+    for pages, heads in ((2 ** 32 + 1, 1), (0, 2 ** 32 + 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            sfx.KVCache(pages, 64, heads, 64, device="meta")

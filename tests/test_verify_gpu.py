@@ -504,3 +504,13 @@ def test_extreme_temperatures_in_phases(S, temp):
     ua = rng.random((B, k)).astype(np.float32) * (3.0 / V if temp > 1 else 1.0)
     us = rng.random(B).astype(np.float32)
     check(S, x, draft, None, ua.astype(np.float32), us, np.full(B, temp, np.float32))
+
+
+def test_vocabulary_past_32_bits_is_refused(S):
+    """2^32 + 5 logits a row would reach the library as 5."""
+    import torch
+
+    x = torch.empty((1, 1, 2 ** 32 + 5), dtype=torch.float16, device="cuda")
+    none = torch.empty((1, 0), device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        S.verify(x, none.int(), None, none, torch.zeros(1, device="cuda"))
