@@ -624,6 +624,13 @@ class KVCache:
         self._p = ctypes.addressof(self._c)
         self._bytes = {}  # workspace sizes of the attention's shapes
 
+    def __setattr__(self, name, value):
+        # the library has the buffers' addresses and the sizes from the constructor
+        if name in self.__dict__:
+            raise AttributeError(f"{name} stays as it was made; write into the tensor, or make "
+                                 "another KVCache")
+        super().__setattr__(name, value)
+
     @staticmethod
     def shapes(num_pages, page_size, kv_heads, head_dim):
         """Shapes of k, v, k_scale and v_scale."""

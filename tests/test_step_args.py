@@ -253,3 +253,20 @@ def test_sizes_past_32_bits_are_refused():
     for pages, heads in ((2 ** 32 + 1, 1), (0, 2 ** 32 + 1)):
         with pytest.raises(ValueError, match="2\\^31"):
             sfx.KVCache(pages, 64, heads, 64, device="meta")
+
+
+def test_cache_keeps_its_buffers():
+    """The library reads the memory that the cache was made with: another tensor in its place would
+    be ignored, so it is refused."""
+    import torch
+
+    c = sfx.KVCache(2, 64, 1, 64, device="cpu")
+    for name in ("k", "v", "k_scale", "v_scale", "num_pages", "page_size", "kv_heads", "head_dim",
+                 "device"):
+        was = getattr(c, name)
+        with pytest.raises(AttributeError, match=name):
+            setattr(c, name, was.clone() if isinstance(was, torch.Tensor) else was)
+        assert getattr(c, name) is was
+    c.k.fill_(7)
+    c.owner = "a request"  # a caller's own attribute
+    assert c._c.k == c.k.data_ptr() and int(c.k.sum()) == 7 * c.k.numel()
