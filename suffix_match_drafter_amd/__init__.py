@@ -574,6 +574,9 @@ def _heads(t, name, heads, dim, index):
         raise ValueError(f"{name} must be [B, T, {heads}, {dim}], got {tuple(shape)}")
     if t.stride(3) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError(f"{name} requires grad, which ends here: these calls have no backward "
+                           "(detach it, or call under torch.no_grad())")
     return shape
 
 

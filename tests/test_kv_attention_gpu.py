@@ -494,3 +494,26 @@ def test_nan_key_among_growing_scores(S, dtype):
         model.code["k"] = keep
         assert torch.isnan(out[0]).all()
         compare(out[1:], model, q[1:], table[1:], [L], None, dim ** -0.5, 0, 0)
+
+
+def test_gradients_are_refused(S):
+    """There is no backward: a tensor that asks for one is refused where it would be dropped
+    without a word, and taken where gradients are off."""
+    import torch
+
+    cache = S.KVCache(1, 32, 1, 64)
+    table, one = i32([[0]]), i32([1])
+    x = torch.ones((1, 1, 1, 64), dtype=torch.float16, device="cuda")
+    g = x.clone().requires_grad_()
+    y = g * 2  # not a leaf
+    for call in (lambda: cache.attend(g, table, one), lambda: cache.attend(y, table, one),
+                 lambda: cache.write(g, x, table, i32([0])),
+                 lambda: cache.write(x, y, table, i32([0])),
+                 lambda: cache.read(table, i32([0]), None, 1, torch.float16, k=g, v=x)):
+        with pytest.raises(RuntimeError, match="requires grad"):
+            call()
+    assert not cache.k.any().item() and not cache.v.any().item()
+    with torch.no_grad():
+        cache.write(g, y, table, i32([0]))
+        assert torch.equal(cache.attend(g, table, one), 2 * x)
+    assert torch.equal(cache.attend(g.detach(), table, one), 2 * x)

@@ -270,3 +270,14 @@ def test_cache_keeps_its_buffers():
     c.k.fill_(7)
     c.owner = "a request"  # a caller's own attribute
     assert c._c.k == c.k.data_ptr() and int(c.k.sum()) == 7 * c.k.numel()
+
+
+def test_gradients_are_refused():
+    import torch
+
+    x = torch.zeros(1, 1, 2, 64, requires_grad=True)
+    with pytest.raises(RuntimeError, match="q requires grad"):
+        sfx._heads(x, "q", 2, 64, -1)
+    with torch.no_grad():
+        assert sfx._heads(x, "q", 2, 64, -1) == x.shape
+    assert sfx._heads(x.detach(), "q", 2, 64, -1) == x.shape
