@@ -517,3 +517,35 @@ def test_gradients_are_refused(S):
         cache.write(g, y, table, i32([0]))
         assert torch.equal(cache.attend(g, table, one), 2 * x)
     assert torch.equal(cache.attend(g.detach(), table, one), 2 * x)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompts(S, dim):
+    """Prompts of a thousand tokens attend over themselves, from an empty cache and behind a
+    prefix, with and without a window."""
+    import torch
+
+    rng = np.random.default_rng(dim)
+    heads, group, page, width, T = 1, 2, 64, 20, 1030
+    cache, model = filled(S, rng, 2 * width, page, heads, dim)
+    table = rng.permutation(2 * width).reshape(2, width)
+    q = dev(rng.standard_normal((2, T, heads * group, dim))).to(torch.bfloat16)
+    for lens, qlens, window, sinks in (([1030, 1200], [1030, 1001], 0, 0),
+                                       ([1030, 1200], [1030, 1001], 200, 4)):
+        out = cache.attend(q, i32(table), i32(lens), i32(qlens), window=window, sinks=sinks)
+        compare(out, model, q, table, lens, qlens, dim ** -0.5, window, sinks)
+
+
+def test_short_requests_in_a_wide_table(S):
+    """A table sized for the longest allowed context, mostly unmapped, with short requests."""
+    import torch
+
+    rng = np.random.default_rng(24)
+    heads, group, dim, page, T = 2, 4, 128, 128, 5
+    cache, model = filled(S, rng, 16, page, heads, dim)
+    table = np.full((2, 1024), -1)
+    table[:, :8] = rng.permutation(16).reshape(2, 8)
+    q = dev(rng.standard_normal((2, T, heads * group, dim))).to(torch.float16)
+    for lens in ([1000, 37], [129, 1024]):
+        out = cache.attend(q, i32(table), i32(lens))
+        compare(out, model, q, table, lens, None, dim ** -0.5, 0, 0)
