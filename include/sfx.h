@@ -475,6 +475,7 @@ int sfx_kv_read(const sfx_kv_cache* cache, int32_t B, int32_t T, int32_t max_pag
  *   j > p - window or j < sinks.  Tokens of unmapped pages are not seen.
  *   out = softmax(scale * q k) v in fp32 sums; zero for rows that see nothing or t >= q_len.
  * T = 1 is plain decoding, T = k + 1 the verification of a draft, larger T a prompt.
+ * Long requests are cut into parts by max_pages, so a table much wider than they are costs time.
  * workspace: sfx_kv_attention_workspace_bytes (may be 0), aligned to 16 bytes; its contents
  * mean nothing before or after.  scale: in [2^-64, 2^64]. */
 int sfx_kv_attention_workspace_bytes(const sfx_kv_cache* cache, int32_t B, int32_t T,

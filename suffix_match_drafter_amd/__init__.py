@@ -589,9 +589,9 @@ class KVCache:
     and head, in the layout that the attention reads (sfx_kv_cache in include/sfx.h).
 
     The buffers are allocated here, or given as ``buffers = (k, v, k_scale, v_scale)``: uint8 (or
-    float8_e4m3fn) codes and float32 scales of the shapes of :meth:`shapes`.  Page tables, starts
-    and lengths are int32 tensors in device memory; which pages a request owns is the caller's
-    business."""
+    float8_e4m3fn) codes and float32 scales of the shapes of :meth:`shapes`; they stay the
+    cache's.  Page tables, starts and lengths are contiguous int32 tensors in device memory; which
+    pages a request owns is the caller's business.  There is no backward."""
 
     def __init__(self, num_pages, page_size, kv_heads, head_dim, device="cuda", buffers=None):
         if head_dim not in (64, 128, 256):

@@ -64,8 +64,9 @@ hipError_t launch_kv_write(const KvMoveArgs& a, int dim, KvType type, hipStream_
 hipError_t launch_kv_read(const KvMoveArgs& a, int dim, KvType type, hipStream_t st);
 
 // ---------------------------------------------------------------- device helpers
-// Page of a 32-token block within its request: block / (page_size / 32) for blocks below 2^26
-// and at most 64 blocks a page (the magic's error stays below 2^-32 of a page).
+// Page of a 32-token block within its request: block / (page_size / 32).  With n <= 64 blocks a page
+// the magic is too large by less than n / 2^32 of itself, which over blocks below 2^26 adds less
+// than (n - 1) / n 2^-6 to the quotient: not enough to pass the next page, 1 / n >= 2^-6 away.
 __device__ __forceinline__ int kv_page_of(const KvCache& c, int block) {
   return c.page_magic ? (int)__umulhi((unsigned)block, c.page_magic) : block;
 }

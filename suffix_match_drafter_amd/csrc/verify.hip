@@ -20,7 +20,7 @@
 // read in vain and each launch fills the card.  Small calls, where four launches would cost more
 // than the rows they save, read all rows in parts at once.
 //
-// Measured, k = 8 and V = 151936 in bf16: B = 1 21 us, B = 16 33, B = 64 60; B = 256, k = 16 154 us
+// Measured, k = 8 and V = 151936 in bf16: B = 1 20 us, B = 16 33, B = 64 63; B = 256, k = 16 153 us
 // when 64% of the drafted tokens are accepted, of which 110 read 965 rows of 4352 (2.7 TB/s; 720
 // rows would do) and 40 sum and search the drawn ones.
 #include "verify.h"
@@ -264,8 +264,8 @@ __device__ __forceinline__ const char* row_ptr(const VerifyArgs& a, int b, int s
 // exp by a table of 2^(i/256) and a polynomial over 1/256 of an octave, |z| <= ln 2 / 512:
 //   2^(n/256 + f/256) = 2^(n div 256) T[n mod 256] (1 + z + z^2/2 + z^3/6),  z = f ln 2 / 256,
 // within 2^-42 of the function.  The search for the drawn token is bounded by these instructions
-// (20 a logit, 38 us for 256 rows of 151936; 27 a logit, with 32 entries, two more terms and a
-// select, took 49).  Logits more than 700 T below the largest weigh e^-700 here, whatever they
+// (19 a logit, 40 us for 256 rows of 151936 with the launch; 27 a logit, with 32 entries, two more
+// terms and a select, took 11 us more).  Logits more than 700 T below the largest weigh e^-700 here, whatever they
 // are: what they add is far below a draw's resolution unless the draw is below kTiny, which is
 // done again with the exact function.
 constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer
