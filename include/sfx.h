@@ -414,7 +414,8 @@ int sfx_build_suffix_array_noalloc(const int32_t* text, int64_t n, int32_t* sa, 
  * `num_accepted` are the next inputs of sfx_propose / sfx_update_state and of
  * sfx_accept_feedback.  These calls need no context; they neither allocate nor synchronise, use
  * no memory clears, and can be captured in a HIP graph.  Workspaces are the caller's; calls that
- * may overlap need one each. */
+ * may overlap need one each.  A call that would need a launch of more than 2^32 - 1 threads, or a
+ * table of more tokens than stated below, returns SFX_ECAPACITY. */
 
 /* Element types of the arrays marked `type`. */
 enum { SFX_TYPE_BF16 = 0, SFX_TYPE_FP16 = 1, SFX_TYPE_FP32 = 2 };

@@ -32,12 +32,12 @@
 //
 // Measured (8 cached heads of 128, bf16): one row and 4 query heads for 64 requests of up to 4096
 // tokens 68 us, 5.0 TB/s, bounded by memory; 17 rows for 32 requests of up to 16384 tokens 230 us
-// (220 to 237 by the lengths), 480 TFLOP/s, bounded by vector instructions (40% of the time) and the matrix unit (27%), which a
-// wavefront uses in turn, and by the longest request; the same of one request of 32768 tokens and 8
-// query heads 39 us.  Chunks of at most 48 rows at 128 dims leave room for two wavefronts a SIMD,
-// one of which computes weights while the other multiplies: with one wavefront and the compiler's
-// copies of a second set of codes the 17-row call took 540 us.  Three row tiles at 128 dims fill the
-// 256 registers of two wavefronts a SIMD and spill three.
+// (220 to 237 by the lengths), 480 TFLOP/s, bounded by vector instructions (40% of the time) and the
+// matrix unit (27%), which a wavefront uses in turn, and by the longest request; the same of one
+// request of 32768 tokens and 8 query heads 39 us.  Chunks of at most 48 rows at 128 dims leave room
+// for two wavefronts a SIMD, one of which computes weights while the other multiplies: with one
+// wavefront and the compiler's copies of a second set of codes the 17-row call took 540 us.  Three
+// row tiles at 128 dims fill the 256 registers of two wavefronts a SIMD and spill three.
 //
 // A NaN among the values reaches only the rows that see its token: a tile that some row does not
 // see in full is searched for NaN codes, and where there are any they are taken out of the

@@ -265,9 +265,9 @@ __device__ __forceinline__ const char* row_ptr(const VerifyArgs& a, int b, int s
 //   2^(n/256 + f/256) = 2^(n div 256) T[n mod 256] (1 + z + z^2/2 + z^3/6),  z = f ln 2 / 256,
 // within 2^-42 of the function.  The search for the drawn token is bounded by these instructions
 // (19 a logit, 40 us for 256 rows of 151936 with the launch; 27 a logit, with 32 entries, two more
-// terms and a select, took 11 us more).  Logits more than 700 T below the largest weigh e^-700 here, whatever they
-// are: what they add is far below a draw's resolution unless the draw is below kTiny, which is
-// done again with the exact function.
+// terms and a select, took 11 us more).  Logits more than 700 T below the largest weigh e^-700
+// here, whatever they are: what they add is far below a draw's resolution unless the draw is below
+// kTiny, which is done again with the exact function.
 constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to an integer
 constexpr double kZ = 0.69314718055994530942 / 256;
 constexpr int kTable = 256;
