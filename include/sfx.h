@@ -513,6 +513,90 @@ int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batc
                int32_t* sampled, int32_t* num_accepted, void* workspace, size_t workspace_bytes,
                void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Packed batches.  A batch of requests of different lengths without padding: the rows of request b
+ * (prompt chunks of any size, drafts, single tokens) are rows offsets[b] .. offsets[b + 1] - 1 of
+ * [N, ...] arrays.  offsets [B + 1] does not decrease and is clamped to [0, N]; rows before
+ * offsets[0] and from offsets[B] on belong to no request.  sfx_pages_reserve gives every request the
+ * pages that it needs, sfx_step_layout says where its rows and their slots are, sfx_kv_write_slots
+ * writes their keys and values, sfx_kv_attention_packed attends over the cache and
+ * sfx_prompt_attention, which needs no cache, over a whole prompt's own keys and values.  As the calls
+ * above, these need no context, neither allocate nor synchronise, and can be captured. */
+
+/* Pages for requests of given lengths, on the device.  Request b holds the first held[b] entries of
+ * page_table [B, max_pages] and needs ceil(tokens[b] / page_size) of them (tokens below 0 count
+ * as 0, held is clamped to [0, max_pages]).
+ *   Pages past that are released, in order of (request, entry); their entries become -1.
+ *   Requests that need more get all of it or nothing, in order of b: the first whose pages are not
+ *   there, and every later one that needs some, gets none, and missing[b] (may be NULL; 0 elsewhere) is
+ *   how many it lacks.  A request that needs more than max_pages gets none and keeps nobody waiting.
+ *   Released pages are handed on first, in their order, then free_pages [num_pages] from its end,
+ *   free_pages[*num_free - 1] and down; released pages left over are appended to it in order.
+ * held, num_free ([1], clamped to [0, num_pages]) and page_table are updated; entries of free_pages from
+ * num_free on mean nothing.  Ids are moved as they are.  A new pool has free_pages = 0, 1, ... and
+ * num_free = num_pages; a finished request has tokens 0.
+ * workspace: sfx_pages_reserve_workspace_bytes (may be 0), aligned to 16 bytes. */
+int sfx_pages_reserve_workspace_bytes(int32_t B, int32_t max_pages, size_t* bytes);
+int sfx_pages_reserve(int32_t B, int32_t max_pages, int32_t page_size, int32_t num_pages,
+                      const int32_t* tokens, int32_t* page_table, int32_t* held,
+                      int32_t* free_pages, int32_t* num_free, int32_t* missing, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* The layout of a packed batch of count[b] new tokens from position start[b] on (start below 0
+ * counts as 0; count below 0 as 0, and no position passes 2^31 - 2).
+ *   offsets [B + 1]: running sum of the counts from 0, cut at N.
+ *   seq_lens [B]: start plus the request's rows, tokens in the cache once they are written.
+ *   request, position [N], slots [N]: of each row, page_table[b, position / page_size] * page_size
+ *   + position % page_size; -1 for rows of no request, slots also where the page is outside
+ *   [0, num_pages) or past max_pages.
+ * The last four may be NULL; page_table is read for slots only. */
+int sfx_step_layout(int32_t B, int32_t N, int32_t max_pages, int32_t page_size, int32_t num_pages,
+                    const int32_t* page_table, const int32_t* start, const int32_t* count,
+                    int32_t* offsets, int32_t* seq_lens, int32_t* request, int32_t* position,
+                    int64_t* slots, void* stream);
+
+/* sfx_kv_write for a packed batch: token i of k, v [N, kv_heads, head_dim] goes to slots[i] = page *
+ * page_size + place; slots outside the cache write nothing.  strides: of {token, head}.
+ * New tokens of one block of 32 stand next to each other in slot order; the block is new when the
+ * first of them is its first place, and otherwise keeps the tokens before it, as sfx_kv_write does.
+ * A block must not be written by two separate stretches of one call. */
+int sfx_kv_write_slots(const sfx_kv_cache* cache, int32_t N, const int64_t* slots, const void* k,
+                       const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                       int32_t type, void* stream);
+
+/* sfx_kv_attention for a packed batch: q [N, q_heads, head_dim], strides of {token, head}; row t of
+ * the n of request b stands at position seq_lens[b] - n + t.  Rows t >= max_q of a request and rows
+ * of no request are zero: max_q is the most rows of a request that the call is planned for (at most
+ * N; a call with few takes another path, so a tight one saves time).
+ * out [N, q_heads, head_dim], dense.  Everything else is as for sfx_kv_attention. */
+int sfx_kv_attention_packed_workspace_bytes(const sfx_kv_cache* cache, int32_t B, int32_t N,
+                                            int32_t max_q, int32_t q_heads, int32_t max_pages,
+                                            int32_t window, int32_t sinks, size_t* bytes);
+int sfx_kv_attention_packed(const sfx_kv_cache* cache, int32_t B, int32_t N, int32_t max_q,
+                            int32_t q_heads, int32_t max_pages, const int32_t* page_table,
+                            const int32_t* seq_lens, const int32_t* offsets, const void* q,
+                            const int64_t* q_strides, void* out, int32_t type, float scale,
+                            int32_t window, int32_t sinks, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Causal attention of whole prompts over their own keys and values, packed: q [N, q_heads,
+ * head_dim], k, v [N, kv_heads, head_dim] of `type` (bf16 or fp16), strides of {token, head} (host
+ * arrays; NULL: dense), the dims of a head contiguous.  Row i of a request sees its rows j <= i; with
+ * window > 0 those with j > i - window or, counted from the request's first row, j < sinks.
+ *   out [N, q_heads, head_dim], dense, aligned to 16 bytes: softmax(scale * q k) v in fp32 sums;
+ *   zero for rows of no request.  head_dim: 64, 128 or 256; scale in [2^-64, 2^64].
+ * Weights are rounded to `type` before they meet the values.
+ * workspace: sfx_prompt_attention_workspace_bytes (may be 0), aligned to 16 bytes. */
+int sfx_prompt_attention_workspace_bytes(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads,
+                                         int32_t head_dim, int32_t window, int32_t sinks,
+                                         size_t* bytes);
+int sfx_prompt_attention(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                         const int32_t* offsets, const void* q, const int64_t* q_strides,
+                         const void* k, const int64_t* k_strides, const void* v,
+                         const int64_t* v_strides, void* out, int32_t type, float scale,
+                         int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import typing
 
 import torch
 
@@ -35,7 +36,10 @@ EXPORTS = ("sfx_create", "sfx_destroy", "sfx_last_error", "sfx_propose", "sfx_pr
            "sfx_build_suffix_array_noalloc", "sfx_graphs_create", "sfx_graphs_propose",
            "sfx_graphs_stats", "sfx_graphs_destroy", "sfx_kv_write", "sfx_kv_read",
            "sfx_kv_attention_workspace_bytes", "sfx_kv_attention",
-           "sfx_verify_workspace_bytes", "sfx_verify")
+           "sfx_verify_workspace_bytes", "sfx_verify", "sfx_pages_reserve_workspace_bytes",
+           "sfx_pages_reserve", "sfx_step_layout", "sfx_kv_write_slots",
+           "sfx_kv_attention_packed_workspace_bytes", "sfx_kv_attention_packed",
+           "sfx_prompt_attention_workspace_bytes", "sfx_prompt_attention")
 
 
 FLAG_STREAM_CONTEXT = 1  # read contexts from device memory instead of staging them in LDS
@@ -185,6 +189,22 @@ def load(path: str = LIB_PATH):
         "sfx_verify_workspace_bytes": (ctypes.c_int, [_I32, _I32, _I32, _I32, _SIZE_P]),
         "sfx_verify": (ctypes.c_int, [_I32, _I32, _I32, _V, _I64, _I64, _I32, _V, _V, _V, _V,
                                       _V, _V, _V, _V, ctypes.c_size_t, _V]),
+        "sfx_pages_reserve_workspace_bytes": (ctypes.c_int, [_I32, _I32, _SIZE_P]),
+        "sfx_pages_reserve": (ctypes.c_int, [_I32, _I32, _I32, _I32, _V, _V, _V, _V, _V, _V, _V,
+                                             ctypes.c_size_t, _V]),
+        "sfx_step_layout": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _V, _V, _V, _V, _V, _V,
+                                           _V, _V, _V]),
+        "sfx_kv_write_slots": (ctypes.c_int, [_V, _I32, _V, _V, _V, _V, _V, _I32, _V]),
+        "sfx_kv_attention_packed_workspace_bytes": (ctypes.c_int, [_V, _I32, _I32, _I32, _I32,
+                                                                   _I32, _I32, _I32, _SIZE_P]),
+        "sfx_kv_attention_packed": (ctypes.c_int, [_V, _I32, _I32, _I32, _I32, _I32, _V, _V, _V,
+                                                   _V, _V, _V, _I32, ctypes.c_float, _I32, _I32,
+                                                   _V, ctypes.c_size_t, _V]),
+        "sfx_prompt_attention_workspace_bytes": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32,
+                                                                _I32, _I32, _SIZE_P]),
+        "sfx_prompt_attention": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _V, _V, _V, _V, _V,
+                                                _V, _V, _V, _I32, ctypes.c_float, _I32, _I32, _V,
+                                                ctypes.c_size_t, _V]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -584,6 +604,47 @@ def _strides(t):
     return None if t.is_contiguous() else (_I64 * 3)(t.stride(0), t.stride(1), t.stride(2))
 
 
+def _rows(t, name, heads, dim, index):
+    """A packed [N, heads, dim] tensor of any row and head strides."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES or t.get_device() != index:
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor on cuda:{index}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [N, {heads}, {dim}], got {tuple(shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError(f"{name} requires grad, which ends here: these calls have no backward "
+                           "(detach it, or call under torch.no_grad())")
+    return shape
+
+
+def _row_strides(t):
+    return None if t.is_contiguous() else (_I64 * 2)(t.stride(0), t.stride(1))
+
+
+def _span(window, sinks):
+    window, sinks = int(window), int(sinks)
+    if window >> 31 or sinks >> 31:
+        raise ValueError("window and sinks must be in [0, 2^31)")
+    return window, sinks
+
+
+def _workspace(sizes, key, size_of, device, stream):
+    """Workspace of a call of these sizes, and its bytes; sizes remembers them per shape."""
+    n = sizes.get(key)
+    if n is None:
+        for x in key:
+            if x >> 31:
+                _too_large(*key)
+        size = ctypes.c_size_t(0)
+        _check(size_of(*key, ctypes.byref(size)))
+        if len(sizes) >= 1024:
+            sizes.clear()
+        n = sizes[key] = size.value
+    return (_empty((n,), torch.uint8, device, stream) if n else None), n
+
+
 class KVCache:
     """A paged 8-bit KV cache: e4m3 codes with a power-of-two scale for each block of 32 tokens
     and head, in the layout that the attention reads (sfx_kv_cache in include/sfx.h).
@@ -626,6 +687,7 @@ class KVCache:
                            self.v_scale.data_ptr())
         self._p = ctypes.addressof(self._c)
         self._bytes = {}  # workspace sizes of the attention's shapes
+        self._packed_bytes = {}
 
     def __setattr__(self, name, value):
         # the library has the buffers' addresses and the sizes from the constructor
@@ -733,6 +795,190 @@ class KVCache:
                                   self.head_dim ** -0.5 if scale is None else float(scale),
                                   window, sinks, ws.data_ptr() if n else None, n,
                                   _raw_stream(stream, i)))
+        return out
+
+
+    def write_slots(self, k, v, slots, stream=None):
+        """sfx_kv_write_slots: quantise token i of the packed k, v [N, kv_heads, head_dim] into
+        place slots[i] (int64; page * page_size + place, anything outside the cache: not written)."""
+        i = self._index
+        _on(i)
+        shape = _rows(k, "k", self.kv_heads, self.head_dim, i)
+        if _rows(v, "v", self.kv_heads, self.head_dim, i) != shape or v.dtype is not k.dtype:
+            raise ValueError("k and v differ in shape or type")
+        N = shape[0]
+        if N >> 31:
+            _too_large(N)
+        at = _array(slots, "slots", (N,), torch.int64, i)
+        _check(load().sfx_kv_write_slots(self._p, N, at, k.data_ptr(), _row_strides(k),
+                                         v.data_ptr(), _row_strides(v), _TYPES[k.dtype],
+                                         _raw_stream(stream, i)))
+
+    def attend_packed(self, q, page_table, seq_lens, offsets, max_q=None, scale=None, window=0,
+                      sinks=0, out=None, stream=None):
+        """sfx_kv_attention_packed: :meth:`attend` for rows offsets[b] .. offsets[b + 1] - 1 of the
+        packed q [N, heads, head_dim], the newest tokens of seq_lens[b] cached ones.  max_q: the
+        most rows of one request, if known (default N); rows past it are zero."""
+        i = self._index
+        _on(i)
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [N, heads, head_dim]")
+        N, H, _ = shape = _rows(q, "q", q.shape[1], self.head_dim, i)
+        if q.dtype is torch.float32:
+            raise TypeError("q must be bfloat16 or float16")
+        B = page_table.shape[0] if isinstance(page_table, torch.Tensor) else 0
+        tab, pages = self._table(page_table, B)
+        sl = _array(seq_lens, "seq_lens", (B,), torch.int32, i)
+        off = _array(offsets, "offsets", (B + 1,), torch.int32, i)
+        window, sinks = _span(window, sinks)
+        L = load()
+        key = (B, N, N if max_q is None else int(max_q), H, pages, window, sinks)
+        if stream is None and q.is_contiguous():
+            new = torch.empty_like(q) if out is None else out
+        else:
+            new = _empty(shape, q.dtype, self.device, stream) if out is None else out
+        to = _array(new, "out", shape, q.dtype, i)
+        ws, n = _workspace(self._packed_bytes, key, lambda *a: (
+            L.sfx_kv_attention_packed_workspace_bytes(self._p, *a)), self.device, stream)
+        _check(L.sfx_kv_attention_packed(
+            self._p, *key[:5], tab, sl, off, q.data_ptr(), _row_strides(q), to, _TYPES[q.dtype],
+            self.head_dim ** -0.5 if scale is None else float(scale), window, sinks,
+            ws.data_ptr() if n else None, n, _raw_stream(stream, i)))
+        return new
+
+
+_prompt_bytes = {}  # workspace sizes of attend_prompt's shapes
+
+
+def attend_prompt(q, k, v, offsets, scale=None, window=0, sinks=0, out=None, stream=None):
+    """sfx_prompt_attention: causal attention of packed whole prompts over their own keys and
+    values.  q [N, heads, head_dim], k, v [N, kv_heads, head_dim] (bf16 or fp16, any row and head
+    strides); request b is rows offsets[b] .. offsets[b + 1] - 1; window and sinks (counted from a
+    request's first row) restrict what they see (0: everything before).  Rows of no request are
+    zero.  scale defaults to head_dim ** -0.5.  There is no backward."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not q.is_cuda:
+        raise TypeError("q must be a [N, heads, head_dim] CUDA/HIP tensor")
+    i = q.get_device()
+    _on(i)
+    N, H, D = shape = _rows(q, "q", q.shape[1], q.shape[2], i)
+    if q.dtype is torch.float32:
+        raise TypeError("q must be bfloat16 or float16")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [N, kv_heads, head_dim]")
+    Hk = k.shape[1]
+    for t, name in ((k, "k"), (v, "v")):
+        if _rows(t, name, Hk, D, i)[0] != N or t.dtype is not q.dtype:
+            raise ValueError(f"{name} must have q's rows and type")
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be [B + 1]")
+    B = offsets.shape[0] - 1
+    off = _array(offsets, "offsets", (B + 1,), torch.int32, i)
+    window, sinks = _span(window, sinks)
+    L = load()
+    if out is None:
+        out = torch.empty_like(q) if stream is None and q.is_contiguous() else \
+            _empty(shape, q.dtype, q.device, stream)
+    to = _array(out, "out", shape, q.dtype, i)
+    key = (B, N, H, Hk, D, window, sinks)
+    ws, n = _workspace(_prompt_bytes, key, L.sfx_prompt_attention_workspace_bytes, q.device, stream)
+    _check(L.sfx_prompt_attention(
+        *key[:5], off, q.data_ptr(), _row_strides(q), k.data_ptr(), _row_strides(k), v.data_ptr(),
+        _row_strides(v), to, _TYPES[q.dtype], D ** -0.5 if scale is None else float(scale), window,
+        sinks, ws.data_ptr() if n else None, n, _raw_stream(stream, i)))
+    return out
+
+
+class StepLayout(typing.NamedTuple):
+    """Where the rows of a packed batch are (:meth:`PagePool.layout`)."""
+
+    offsets: torch.Tensor   # [B + 1] int32: the rows of request b are offsets[b] .. offsets[b + 1] - 1
+    seq_lens: torch.Tensor  # [B] int32: tokens in the cache once the rows are written
+    request: torch.Tensor   # [N] int32: a row's request, -1 for rows of none
+    position: torch.Tensor  # [N] int32: its position in the request
+    slots: torch.Tensor     # [N] int64: its place in the cache, for KVCache.write_slots
+
+
+class PagePool:
+    """The pages of one or more caches (of the same number and size of pages), handed out on the
+    device: a list of free page ids and their number, allocated here with every page free, or given
+    as ``buffers = (free, num_free)`` (int32 [num_pages] and [1]; they stay the pool's).
+
+    A request's row of page_table [B, pages] holds the pages that it has, held [B] how many; both
+    are int32 tensors of the caller's, -1 and 0 at first."""
+
+    def __init__(self, num_pages, page_size, device="cuda", buffers=None):
+        if num_pages < 0 or page_size < 1:
+            raise ValueError("num_pages must not be negative, page_size at least 1")
+        if (num_pages | page_size) >> 31:
+            _too_large(num_pages, page_size)
+        if buffers is None:
+            dev = torch.device(device)
+            self.free = torch.arange(num_pages, dtype=torch.int32, device=dev)
+            self.num_free = torch.full((1,), num_pages, dtype=torch.int32, device=dev)
+        else:
+            for t, n, name in zip(buffers, (num_pages, 1), ("free", "num_free")):
+                if t.dtype is not torch.int32 or not t.is_cuda or t.device != buffers[0].device:
+                    raise TypeError(f"{name} must be an int32 CUDA/HIP tensor")
+                if t.shape != (n,) or not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous of shape ({n},)")
+            self.free, self.num_free = buffers
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.device = self.free.device
+        self._index = self.free.get_device()
+        self._bytes = {}  # workspace sizes of reserve's shapes
+
+    def _table(self, page_table):
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table must be [B, pages]")
+        B, pages = page_table.shape
+        if (B | pages) >> 31:
+            _too_large(B, pages)
+        return _array(page_table, "page_table", (B, pages), torch.int32, self._index), B, pages
+
+    def reserve(self, page_table, held, tokens, missing=None, stream=None):
+        """sfx_pages_reserve: give every request pages for tokens[b] tokens and take back those past
+        them; page_table and held are updated.  Returns missing [B]: the pages that a request lacks,
+        which then got none (0: it has what it needs)."""
+        i = self._index
+        _on(i)
+        tab, B, pages = self._table(page_table)
+        h = _array(held, "held", (B,), torch.int32, i)
+        tk = _array(tokens, "tokens", (B,), torch.int32, i)
+        if missing is None:
+            missing = torch.empty_like(held) if stream is None else \
+                _empty((B,), torch.int32, self.device, stream)
+        to = _array(missing, "missing", (B,), torch.int32, i)
+        L = load()
+        ws, n = _workspace(self._bytes, (B, pages), L.sfx_pages_reserve_workspace_bytes,
+                           self.device, stream)
+        _check(L.sfx_pages_reserve(B, pages, self.page_size, self.num_pages, tk, tab, h,
+                                   self.free.data_ptr(), self.num_free.data_ptr(), to,
+                                   ws.data_ptr() if n else None, n, _raw_stream(stream, i)))
+        return missing
+
+    def layout(self, page_table, start, count, rows, out=None, stream=None):
+        """sfx_step_layout: the layout of a packed batch of `rows` rows (those past the counts' sum
+        belong to no request) with count[b] new tokens from position start[b] on."""
+        i = self._index
+        _on(i)
+        tab, B, pages = self._table(page_table)
+        st = _array(start, "start", (B,), torch.int32, i)
+        ct = _array(count, "count", (B,), torch.int32, i)
+        N = int(rows)
+        if N >> 31:
+            _too_large(N)
+        shapes = ((B + 1,), (B,), (N,), (N,), (N,))
+        if out is None:
+            if stream is None:
+                out = StepLayout(*[start.new_empty(s) for s in shapes[:4]],
+                                 start.new_empty(N, dtype=torch.int64))
+            else:
+                out = StepLayout(*[_empty(s, torch.int64 if k == 4 else torch.int32, self.device,
+                                          stream) for k, s in enumerate(shapes)])
+        to = [_array(t, name, s, torch.int64 if name == "slots" else torch.int32, i)
+              for t, name, s in zip(out, StepLayout._fields, shapes)]
+        _check(load().sfx_step_layout(B, N, pages, self.page_size, self.num_pages, tab, st, ct,
+                                      *to, _raw_stream(stream, i)))
         return out
 
 

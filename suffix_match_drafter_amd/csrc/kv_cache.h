@@ -60,6 +60,25 @@ inline __int128 kv_move_threads(int B, int T, int heads) {
   return (units + kKvMoveWaves - 1) / kKvMoveWaves * (64 * kKvMoveWaves);
 }
 
+// The write of a packed batch by slots; strides[batch] is not used.
+struct KvSlotArgs {
+  KvCache c;
+  int32_t N, window;  // tokens, and how many of them one wavefront looks at (1..32)
+  const int64_t* slots;
+  const void* k;
+  const void* v;
+  KvStrides ks, vs;
+};
+
+inline int32_t kv_slot_window(int32_t N) { return N > 4096 ? 8 : 1; }
+
+inline __int128 kv_slot_threads(int64_t N, int64_t window, int64_t heads) {
+  const __int128 units = __int128((N + window - 1) / window) * 2 * heads;
+  return (units + kKvMoveWaves - 1) / kKvMoveWaves * (64 * kKvMoveWaves);
+}
+
+hipError_t launch_kv_write_slots(const KvSlotArgs& a, int dim, KvType type, hipStream_t st);
+
 hipError_t launch_kv_write(const KvMoveArgs& a, int dim, KvType type, hipStream_t st);
 hipError_t launch_kv_read(const KvMoveArgs& a, int dim, KvType type, hipStream_t st);
 

@@ -210,29 +210,23 @@ __device__ __forceinline__ void to_order(const unsigned (&raw)[kWords<T>],
 // dependent chain of loads (a few tokens: counts, page id, then inputs, old codes and scale
 // together).  Measured: 8 prompts of 8192 tokens of 8 heads of 128 in bf16 78 us, 4.8 TB/s; 256
 // drafts of 17 tokens 16 us, a single token for 4 requests 4 us.
+//
+// `in`: the head's row of new token 0, further ones `stride` elements apart; the block `sub` of `page`
+// starts `rel` tokens behind new token 0 and takes those of the `count` that fall into it.
 template <typename T, int D, bool kVal>
-__device__ void write_block(const KvMoveArgs& a, int b, int h, int block, int start, int count,
-                            int lane) {
+__device__ void write_block(const KvCache& kc, const char* in, int64_t stride, int page, int sub,
+                            int h, int rel, int count, int lane) {
   constexpr int kChunks = Map<D, kVal>::kChunks, kB = T::kBytes, kW = kWords<T>;
-  const KvCache& kc = a.c;
-  const int per_page = kc.page_size / kKvBlock;
-  const int pi = kv_page_of(kc, block);
-  if (pi >= a.max_pages) return;
-  const int page = a.page_table[(int64_t)b * a.max_pages + pi];
-  if (page < 0 || page >= kc.num_pages) return;
-  const int sub = block - pi * per_page, tok0 = sub * kKvBlock;
+  const int per_page = kc.page_size / kKvBlock, tok0 = sub * kKvBlock;
   const int64_t ph = (int64_t)page * kc.heads + h;
   uint8_t* codes = (kVal ? kc.v : kc.k) + ph * kc.page_size * D;
   float* scale = (kVal ? kc.v_scale : kc.k_scale) + ph * per_page + sub;
-  const KvStrides& s = kVal ? a.vs : a.ks;
-  const char* in = (const char*)(kVal ? a.v : a.k) + (b * s.batch + h * s.head) * kB;
   const int r = lane >> 2, g = lane & 3;
-  const int rel = block * kKvBlock - start;  // input index of the block's first token
   const bool full = rel >= 0 && rel + kKvBlock <= count, live_before = rel < 0;
   auto is_new = [&](int tok) { return rel + tok >= 0 && rel + tok < count; };
   auto source = [&](int tok) {  // a row that can be read: one that is not new is cleared below
     const int j = rel + tok;
-    return in + (int64_t)(j < 0 ? 0 : (j < count ? j : count - 1)) * s.token * kB;
+    return in + (int64_t)(j < 0 ? 0 : (j < count ? j : count - 1)) * stride * kB;
   };
 
   // Old bytes: a 16-byte chunk of values mixes eight tokens and is read before it is written; one of
@@ -396,10 +390,64 @@ __global__ __launch_bounds__(64 * kKvMoveWaves) void kv_write_kernel(KvMoveArgs 
   if (start < 0 || count <= 0) return;
   const int64_t blk = (int64_t)start / kKvBlock + u.block;
   if (blk * kKvBlock >= (int64_t)start + count || blk >= (1 << 26)) return;
+  const KvCache& kc = a.c;
+  const int pi = kv_page_of(kc, (int)blk);
+  if (pi >= a.max_pages) return;
+  const int page = a.page_table[(int64_t)u.b * a.max_pages + pi];
+  if (page < 0 || page >= kc.num_pages) return;
+  const int sub = (int)blk - pi * (kc.page_size / kKvBlock);
+  const int rel = (int)blk * kKvBlock - start;  // input index of the block's first token
+  const KvStrides& s = u.val ? a.vs : a.ks;
+  const char* in = (const char*)(u.val ? a.v : a.k) + (u.b * s.batch + u.h * s.head) * T::kBytes;
   if (u.val)
-    write_block<T, D, true>(a, u.b, u.h, (int)blk, start, count, lane);
+    write_block<T, D, true>(kc, in, s.token, page, sub, u.h, rel, count, lane);
   else
-    write_block<T, D, false>(a, u.b, u.h, (int)blk, start, count, lane);
+    write_block<T, D, false>(kc, in, s.token, page, sub, u.h, rel, count, lane);
+}
+
+// The same for a packed batch by slots.  A run is a block's new tokens: neighbours whose slots follow
+// each other within one block.  A wavefront takes the runs that start among its `window` tokens: it
+// reads their slots and 32 more, one a lane, and finds starts and lengths by votes.
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kKvMoveWaves) void kv_write_slots_kernel(KvSlotArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  unsigned u = blockIdx.x * kKvMoveWaves + wave;  // below 2^26 + 4
+  const KvCache& kc = a.c;
+  const int h = u % kc.heads;
+  u /= kc.heads;
+  const bool val = u & 1;
+  const int64_t first = (int64_t)(u >> 1) * a.window;
+  if (first >= a.N) return;
+  const int per_page = kc.page_size / kKvBlock;
+  const int64_t slots = (int64_t)kc.num_pages * kc.page_size;
+  // lane 0 holds the token before the window
+  const int64_t i = first - 1 + lane;
+  int64_t slot = i >= 0 && i < a.N ? a.slots[i] : -1;
+  if (slot < 0 || slot >= slots) slot = -1;
+  const int64_t prev = __shfl_up(slot, 1);
+  const bool joins = slot >= 0 && slot % kKvBlock != 0 && prev == slot - 1;
+  const uint64_t join = __ballot(joins);
+  const uint64_t window = ((uint64_t(1) << a.window) - 1) << 1;
+  uint64_t starts = __ballot(slot >= 0 && !joins) & window;
+  const KvStrides& s = val ? a.vs : a.ks;
+  const char* in = (const char*)(val ? a.v : a.k) + h * s.head * T::kBytes;
+  while (starts) {
+    const int at = __builtin_ctzll(starts);
+    starts &= starts - 1;
+    const int count = __builtin_ctzll(~(join >> (at + 1))) + 1;  // at most 32: within a block
+    const int64_t first_slot = (int64_t)((uint64_t)(unsigned)__builtin_amdgcn_readlane(
+                                             (int)(slot >> 32), at) << 32 |
+                                         (unsigned)__builtin_amdgcn_readlane((int)slot, at));
+    const int64_t block = first_slot / kKvBlock;
+    const int page = (int)(block / per_page), sub = (int)(block - (int64_t)page * per_page);
+    const int rel = -(int)(first_slot % kKvBlock);
+    const char* row = in + (first - 1 + at) * s.token * T::kBytes;
+    if (val)
+      write_block<T, D, true>(kc, row, s.token, page, sub, h, rel, count, lane);
+    else
+      write_block<T, D, false>(kc, row, s.token, page, sub, h, rel, count, lane);
+  }
 }
 
 // LDS of one wavefront of the read: 32 rows of up to 256 bytes, 16 apart so that the lanes' words of
@@ -568,6 +616,17 @@ hipError_t dispatch(const KvMoveArgs& a, int dim, KvType type, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <typename T, int D>
+void launch_slots(const KvSlotArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(kv_slot_threads(a.N, a.window, a.c.heads) / (64 * kKvMoveWaves)));
+  hipLaunchKernelGGL((kv_write_slots_kernel<T, D>), grid, dim3(64 * kKvMoveWaves), 0, st, a);
+}
+template <typename T>
+void launch_slots_dim(const KvSlotArgs& a, int dim, hipStream_t st) {
+  dim == 64 ? launch_slots<T, 64>(a, st)
+            : dim == 128 ? launch_slots<T, 128>(a, st) : launch_slots<T, 256>(a, st);
+}
+
 template <typename T, int D> struct Write {
   static auto get() { return kv_write_kernel<T, D>; }
 };
@@ -583,6 +642,16 @@ hipError_t launch_kv_write(const KvMoveArgs& a, int dim, KvType type, hipStream_
 
 hipError_t launch_kv_read(const KvMoveArgs& a, int dim, KvType type, hipStream_t st) {
   return dispatch<Read>(a, dim, type, st);
+}
+
+hipError_t launch_kv_write_slots(const KvSlotArgs& a, int dim, KvType type, hipStream_t st) {
+  if (type == kBf16)
+    launch_slots_dim<Bf16>(a, dim, st);
+  else if (type == kFp16)
+    launch_slots_dim<Fp16>(a, dim, st);
+  else
+    launch_slots_dim<Fp32>(a, dim, st);
+  return hipGetLastError();
 }
 
 }  // namespace sfx

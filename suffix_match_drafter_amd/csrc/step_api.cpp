@@ -1,5 +1,6 @@
 // step_api.cpp -- host side of the verification step's operators declared in include/sfx.h: the
-// 8-bit KV cache's write and read, the attention over it, and the verification of a draft.
+// 8-bit KV cache's writes and read, the attention over it, the verification of a draft, and what a
+// packed batch needs besides: pages, the batch's layout and the attention of prompts.
 //
 // They need no context.  Host code checks the arguments it can see, derives the launch plan from
 // the shapes alone (never from device memory) and enqueues kernels.
@@ -7,6 +8,8 @@
 #include "errors.h"
 #include "kv_attention.h"
 #include "kv_cache.h"
+#include "pages.h"
+#include "tile_attention.h"
 #include "verify.h"
 
 using namespace sfx;
@@ -137,6 +140,89 @@ int verify_shape(int32_t B, int32_t k, int32_t V, int32_t type, VerifyArgs* a, s
   return SFX_OK;
 }
 
+KvStrides packed_strides(const int64_t* s, int64_t heads, int64_t dim) {
+  if (s) return KvStrides{0, s[0], s[1]};
+  return KvStrides{0, heads * dim, dim};
+}
+
+int check_heads(int32_t q_heads, int32_t kv_heads, int32_t window, int32_t sinks) {
+  if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads)
+    return fail(SFX_EINVAL, "q_heads=%d is not a multiple of kv_heads=%d", q_heads, kv_heads);
+  if (window < 0 || sinks < 0)
+    return fail(SFX_EINVAL, "negative window=%d or sinks=%d", window, sinks);
+  return SFX_OK;
+}
+
+// The plan of an attention of packed rows; a->c is filled for one over the cache.
+int tile_plan(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+              int32_t window, int32_t sinks, bool paged, TileAttentionArgs* a, size_t* bytes) {
+  a->B = B;
+  a->N = N;
+  a->heads = kv_heads;
+  a->group = q_heads / kv_heads;
+  a->window = window;
+  a->sinks = sinks;
+  if (Wide(N) * q_heads > kMaxRows || B > (1 << 24))
+    return fail(SFX_ECAPACITY, "B=%d N=%d q_heads=%d is too large for one call", B, N, q_heads);
+  *bytes = tile_attention_plan(a, head_dim, paged);
+  if (tile_attention_threads(*a, head_dim) > kMaxThreads)
+    return fail(SFX_ECAPACITY, "B=%d N=%d q_heads=%d is too large for one call", B, N, q_heads);
+  return SFX_OK;
+}
+
+int packed_plan(const sfx_kv_cache* cache, int32_t B, int32_t N, int32_t max_q, int32_t q_heads,
+                int32_t max_pages, const int32_t* page_table, int32_t window, int32_t sinks,
+                TileAttentionArgs* a, size_t* bytes) {
+  int rc = check_cache(cache, B, N, max_pages, page_table, &a->c);
+  if (!rc) rc = check_heads(q_heads, cache->kv_heads, window, sinks);
+  if (rc) return rc;
+  if (max_q < 0) return fail(SFX_EINVAL, "negative max_q=%d", max_q);
+  a->max_pages = max_pages;
+  a->max_q = max_q < N ? max_q : N;
+  a->page_table = page_table;
+  return tile_plan(B, N, q_heads, cache->kv_heads, cache->head_dim, window, sinks, true, a, bytes);
+}
+
+int prompt_plan(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                int32_t window, int32_t sinks, TileAttentionArgs* a, size_t* bytes) {
+  if (B < 0 || N < 0) return fail(SFX_EINVAL, "negative shape B=%d N=%d", B, N);
+  if (!dim_ok(head_dim)) return fail(SFX_EINVAL, "head_dim=%d is not 64, 128 or 256", head_dim);
+  int rc = check_heads(q_heads, kv_heads, window, sinks);
+  if (rc) return rc;
+  return tile_plan(B, N, q_heads, kv_heads, head_dim, window, sinks, false, a, bytes);
+}
+
+// What both attentions of packed rows check beyond the plan, and their common fields.
+int tile_args(const int32_t* offsets, const void* q, const int64_t* q_strides, void* out,
+              int32_t type, float scale, int32_t dim, size_t bytes, void* workspace,
+              size_t workspace_bytes, TileAttentionArgs* a) {
+  int rc = check_type(type, false);
+  if (rc) return rc;
+  if (!(scale >= 1.f / kMaxScale && scale <= kMaxScale))
+    return fail(SFX_EINVAL, "scale=%g outside [2^-64, 2^64]", (double)scale);
+  if (a->N == 0) return SFX_OK;
+  if (!offsets || !q || !out) return fail(SFX_EINVAL, "NULL array argument");
+  if ((uintptr_t)out & 15) return fail(SFX_EINVAL, "out must be aligned to 16 bytes");
+  if (bytes > 0 && (!workspace || workspace_bytes < bytes || ((uintptr_t)workspace & 15)))
+    return fail(SFX_EINVAL, "workspace of %zu bytes (16-byte aligned) needed, %zu given", bytes,
+                workspace ? workspace_bytes : (size_t)0);
+  a->offsets = offsets;
+  a->q = q;
+  a->qs = packed_strides(q_strides, (int64_t)a->heads * a->group, dim);
+  a->out = out;
+  a->scale_log2 = scale * 1.4426950408889634f;
+  if (bytes > 0) tile_attention_place(a, dim, workspace);
+  return SFX_OK;
+}
+
+int check_pages(int32_t B, int32_t max_pages, int32_t page_size, int32_t num_pages) {
+  if (B < 0 || max_pages < 0 || num_pages < 0)
+    return fail(SFX_EINVAL, "negative shape B=%d max_pages=%d num_pages=%d", B, max_pages,
+                num_pages);
+  if (page_size < 1) return fail(SFX_EINVAL, "page_size=%d is not positive", page_size);
+  return SFX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -238,6 +324,137 @@ int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batc
   a.num_accepted = num_accepted;
   verify_place(&a, workspace);
   HIP_OR_RETURN(launch_verify(a, kv_type(type), (hipStream_t)stream), "verify launch");
+  return SFX_OK;
+}
+
+int sfx_pages_reserve_workspace_bytes(int32_t B, int32_t max_pages, size_t* bytes) {
+  if (!bytes) return fail(SFX_EINVAL, "bytes is NULL");
+  int rc = check_pages(B, max_pages, 1, 0);
+  if (rc) return rc;
+  if ((int64_t)B * max_pages > kMaxRows)
+    return fail(SFX_ECAPACITY, "B=%d max_pages=%d is too large for one call", B, max_pages);
+  *bytes = reserve_plan_words(B, max_pages) * sizeof(int32_t);
+  return SFX_OK;
+}
+
+int sfx_pages_reserve(int32_t B, int32_t max_pages, int32_t page_size, int32_t num_pages,
+                      const int32_t* tokens, int32_t* page_table, int32_t* held,
+                      int32_t* free_pages, int32_t* num_free, int32_t* missing, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  size_t bytes = 0;
+  int rc = check_pages(B, max_pages, page_size, num_pages);
+  if (!rc) rc = sfx_pages_reserve_workspace_bytes(B, max_pages, &bytes);
+  if (rc || B == 0) return rc;
+  if (!tokens || !held || !num_free || (max_pages > 0 && !page_table) ||
+      (num_pages > 0 && !free_pages))
+    return fail(SFX_EINVAL, "NULL array argument");
+  if (bytes > 0 && (!workspace || workspace_bytes < bytes || ((uintptr_t)workspace & 15)))
+    return fail(SFX_EINVAL, "workspace of %zu bytes (16-byte aligned) needed, %zu given", bytes,
+                workspace ? workspace_bytes : (size_t)0);
+  const ReserveArgs a{B,    max_pages,  page_size, num_pages, tokens, page_table,
+                      held, free_pages, num_free,  missing,   (int32_t*)workspace};
+  HIP_OR_RETURN(launch_reserve(a, (hipStream_t)stream), "pages reserve launch");
+  return SFX_OK;
+}
+
+int sfx_step_layout(int32_t B, int32_t N, int32_t max_pages, int32_t page_size, int32_t num_pages,
+                    const int32_t* page_table, const int32_t* start, const int32_t* count,
+                    int32_t* offsets, int32_t* seq_lens, int32_t* request, int32_t* position,
+                    int64_t* slots, void* stream) {
+  int rc = check_pages(B, max_pages, page_size, num_pages);
+  if (rc) return rc;
+  if (N < 0) return fail(SFX_EINVAL, "negative N=%d", N);
+  if (!offsets || (B > 0 && (!start || !count || (slots && max_pages > 0 && !page_table))))
+    return fail(SFX_EINVAL, "NULL array argument");
+  if (layout_threads(N) > kMaxThreads)
+    return fail(SFX_ECAPACITY, "N=%d is too large for one call", N);
+  const LayoutArgs a{B,     N,       max_pages, page_size, num_pages, page_table, start,
+                     count, offsets, seq_lens,  request,   position,  slots};
+  HIP_OR_RETURN(launch_layout(a, (hipStream_t)stream), "step layout launch");
+  return SFX_OK;
+}
+
+int sfx_kv_write_slots(const sfx_kv_cache* cache, int32_t N, const int64_t* slots, const void* k,
+                       const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                       int32_t type, void* stream) {
+  KvSlotArgs a{};
+  int rc = check_cache(cache, 0, N, 0, nullptr, &a.c);
+  if (!rc) rc = check_type(type, true);
+  if (rc || N == 0) return rc;
+  if (!slots || !k || !v) return fail(SFX_EINVAL, "NULL array argument");
+  a.N = N;
+  a.window = kv_slot_window(N);
+  if (kv_slot_threads(N, a.window, cache->kv_heads) > kMaxThreads)
+    return fail(SFX_ECAPACITY, "N=%d is too large for one call", N);
+  a.slots = slots;
+  a.k = k;
+  a.v = v;
+  a.ks = packed_strides(k_strides, cache->kv_heads, cache->head_dim);
+  a.vs = packed_strides(v_strides, cache->kv_heads, cache->head_dim);
+  if (cache->num_pages == 0) return SFX_OK;
+  HIP_OR_RETURN(launch_kv_write_slots(a, cache->head_dim, kv_type(type), (hipStream_t)stream),
+                "kv write launch");
+  return SFX_OK;
+}
+
+int sfx_kv_attention_packed_workspace_bytes(const sfx_kv_cache* cache, int32_t B, int32_t N,
+                                            int32_t max_q, int32_t q_heads, int32_t max_pages,
+                                            int32_t window, int32_t sinks, size_t* bytes) {
+  if (!bytes) return fail(SFX_EINVAL, "bytes is NULL");
+  TileAttentionArgs a{};
+  static const int32_t none = 0;  // the plan does not look at the table
+  return packed_plan(cache, B, N, max_q, q_heads, max_pages, &none, window, sinks, &a, bytes);
+}
+
+int sfx_kv_attention_packed(const sfx_kv_cache* cache, int32_t B, int32_t N, int32_t max_q,
+                            int32_t q_heads, int32_t max_pages, const int32_t* page_table,
+                            const int32_t* seq_lens, const int32_t* offsets, const void* q,
+                            const int64_t* q_strides, void* out, int32_t type, float scale,
+                            int32_t window, int32_t sinks, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  TileAttentionArgs a{};
+  size_t bytes = 0;
+  int rc = packed_plan(cache, B, N, max_q, q_heads, max_pages, page_table, window, sinks, &a,
+                       &bytes);
+  if (!rc)
+    rc = tile_args(offsets, q, q_strides, out, type, scale, cache->head_dim, bytes, workspace,
+                   workspace_bytes, &a);
+  if (rc || N == 0) return rc;
+  if (B > 0 && !seq_lens) return fail(SFX_EINVAL, "NULL array argument");
+  a.seq_lens = seq_lens;
+  HIP_OR_RETURN(launch_chunk_attention(a, cache->head_dim, kv_type(type), (hipStream_t)stream),
+                "packed attention launch");
+  return SFX_OK;
+}
+
+int sfx_prompt_attention_workspace_bytes(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads,
+                                         int32_t head_dim, int32_t window, int32_t sinks,
+                                         size_t* bytes) {
+  if (!bytes) return fail(SFX_EINVAL, "bytes is NULL");
+  TileAttentionArgs a{};
+  return prompt_plan(B, N, q_heads, kv_heads, head_dim, window, sinks, &a, bytes);
+}
+
+int sfx_prompt_attention(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                         const int32_t* offsets, const void* q, const int64_t* q_strides,
+                         const void* k, const int64_t* k_strides, const void* v,
+                         const int64_t* v_strides, void* out, int32_t type, float scale,
+                         int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  TileAttentionArgs a{};
+  size_t bytes = 0;
+  int rc = prompt_plan(B, N, q_heads, kv_heads, head_dim, window, sinks, &a, &bytes);
+  if (!rc)
+    rc = tile_args(offsets, q, q_strides, out, type, scale, head_dim, bytes, workspace,
+                   workspace_bytes, &a);
+  if (rc || N == 0) return rc;
+  if (!k || !v) return fail(SFX_EINVAL, "NULL array argument");
+  a.k = k;
+  a.v = v;
+  a.ks = packed_strides(k_strides, kv_heads, head_dim);
+  a.vs = packed_strides(v_strides, kv_heads, head_dim);
+  HIP_OR_RETURN(launch_prompt_attention(a, head_dim, kv_type(type), (hipStream_t)stream),
+                "prompt attention launch");
   return SFX_OK;
 }
 

@@ -1,0 +1,780 @@
+// tile_attention.hip -- attention of many rows: whole prompts over their own keys and values, and
+// packed chunks over the 8-bit cache.
+//
+// A request's row t stands at position p (t in a prompt; seq_len - rows + t over the cache) and sees
+// the tokens j <= p of its request with, under a window, p - window < j or j < sinks:
+//   out_t = sum_j softmax_j(scale q_t . k_j) v_j,    zero for a row that sees nothing.
+//
+// Decomposition.  The rows of a request and head of keys and values (tokens x query heads of its
+// group, the heads of a token next to each other) are cut into tiles of 32 rows a wavefront; a
+// workgroup takes one tile by all tokens that its rows see, or by one of `splits` equal parts of them
+// where there are few tiles.  Tokens come in tiles of 64 (32 at 256 dims), brought from memory through
+// registers into one of two LDS buffers while the other is worked on: one barrier a tile.  Codes of
+// the cache become 16-bit operands on that way, once for the whole workgroup.
+//
+// Per 32 tokens, with the 32x32x16 matrix instructions (lane = 32 h + n):
+//   S^T = K Q^T: rows are tokens, columns query rows, so lane (n, h) gets the scores of query
+//         row n for the tokens 8 q + 4 h + i, q < 4, i < 4;
+//   O^T = V^T P^T: contraction slots may be taken in any order as long as both sides agree, so the
+//         lane supplies the probabilities that it has, and V is read in the matching order: rows of
+//         four tokens turned by the LDS transposed read (prompts), or eight tokens of a dim in
+//         one piece, as the cache has them (chunks, whose keys' rows are permuted to match).
+//
+// Softmax.  As in kv_attention.hip: one pass, running maximum m per row in base 2, P = 2^(s - m + 8),
+// m moves only once a score passes m + 7, scores past 2^16 rounded as m is.  P is rounded to the
+// values' type (the matrix unit takes operands of one type): fp16 over the cache and for fp16 prompts,
+// where weights down to 2^-22 of the largest keep 11 bits; bf16, 8 bits, for bf16 prompts, whose
+// values' range fp16 does not hold.  Each weight's rounding is its own, so their error in a sum of
+// many tokens is below the result's own rounding.  Denominators add the unrounded weights in fp32.
+//
+// Infinities and NaN among the values reach only the rows that see their token: a tile that some row
+// does not see in full is searched for them, and where there are any they are taken out of the
+// product and added to the rows that see them.
+#include "tile_attention.h"
+
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+
+#include <type_traits>
+
+namespace sfx {
+
+namespace {
+
+constexpr float kPShift = 8.f;   // P = 2^(s - m + kPShift)
+constexpr float kPLimit = 15.f;  // m moves when some s - m + kPShift passes this
+constexpr float kNoMax = -3e38f;  // below every score, finite
+constexpr float kLarge = 65536.f;  // |m| from which s and m are rounded alike before the difference
+constexpr int kRefLo = -5, kRefHi = 7;  // block exponent minus reference: code * 2^that is normal
+                                        // in fp16 (2^-9 * 2^-5 = 2^-14, 448 * 2^7 < 65504)
+
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+struct Bf16 {
+  static constexpr unsigned kExp = 0x7f80;  // the exponent's bits
+  static __device__ float value(unsigned bits) { return __uint_as_float(bits << 16); }
+  static __device__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ unsigned pack(float a, float b) {
+    const bf16x2 v{(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(unsigned, v);
+  }
+  template <bool kHi> static __device__ unsigned widen(unsigned codes, float scale) {
+    return __builtin_bit_cast(unsigned,
+                              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, kHi));
+  }
+};
+
+struct Fp16 {
+  static constexpr unsigned kExp = 0x7c00;
+  static __device__ float value(unsigned bits) {
+    return (float)__builtin_bit_cast(_Float16, (unsigned short)bits);
+  }
+  static __device__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ unsigned pack(float a, float b) {
+    const f16x2 v{(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(unsigned, v);
+  }
+  template <bool kHi> static __device__ unsigned widen(unsigned codes, float scale) {
+    return __builtin_bit_cast(unsigned,
+                              __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, kHi));
+  }
+};
+
+// Three-way maximum of scores as they come from the matrix unit; a NaN among them stays one.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
+
+// x y rounded by itself, never as part of a multiply-add.
+__device__ __forceinline__ float product(float x, float y) {
+#pragma clang fp contract(off)
+  float r = x * y;
+  asm("" : "+v"(r));
+  return r;
+}
+
+// Largest / sum over the two lanes of a row.
+__device__ __forceinline__ float pair_max(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+constexpr int tile_tokens(int D) { return D > 128 ? 32 : 64; }
+// Wavefronts of a workgroup.
+constexpr int tile_waves(int D) { return D > 128 ? 4 : 8; }
+constexpr int tile_rows(int D) { return 32 * tile_waves(D); }
+
+// 16-byte pieces of a token's row in LDS lie at piece ^ swizzle(token): the reads of a wavefront, 16
+// tokens at one piece (keys) or 4 tokens by 64 bytes (values, turned), then touch every bank alike.
+template <int D> __device__ __forceinline__ int swizzle(int token) {
+  return D > 64 ? (token & 3) << 2 | (token >> 2 & 3) : (token >> 1 & 1) << 2 | (token >> 2 & 3);
+}
+
+// Segment s of the packed rows: 0 before the first request, 1 .. B the requests, B + 1 behind the
+// last.  `edge(s)` is its first token; any memory gives edges within [0, N].
+__device__ __forceinline__ int edge(const TileAttentionArgs& a, int s) {
+  if (s <= 0) return 0;
+  if (s > a.B + 1) return a.N;
+  const int o = a.offsets[s - 1];
+  return o < 0 ? 0 : (o > a.N ? a.N : o);
+}
+
+// A tile of rows.  The tiles of segment s are numbers edge(s) * group / rows + s and up, which leaves
+// room for its last, partial one: a tile is found from its number without a list.
+struct RowTile {
+  int seg;                // 0 or B + 1: rows of no request, zeroed
+  int start;              // first token of the segment
+  int rows, live;         // rows of the segment, those that attend
+  int r0;                 // first row of the tile; rows: none
+  int pos0;               // position of the segment's first token
+  int len;                // tokens of the request
+  int nsink, first, tiles;  // token tiles: [0, nsink), then [first, ...): `tiles` in all
+};
+
+template <int D, bool kPaged>
+__device__ __forceinline__ RowTile row_tile(const TileAttentionArgs& a, int vt) {
+  constexpr int kRows = tile_rows(D), kTok = tile_tokens(D);
+  const int lane = threadIdx.x & 63;
+  // largest segment whose first number is not past vt: 64 probes at a time
+  int lo = 0, n = a.B + 2;
+  while (n > 1) {
+    const int step = (n + 63) >> 6, at = lo + lane * step;
+    const bool ok = lane * step < n &&
+                    (int64_t)edge(a, at) * a.group / kRows + at <= vt;
+    const int hits = 64 - __builtin_clzll(__ballot(ok) | 1);
+    lo += (hits - 1) * step;
+    const int left = n - (hits - 1) * step;
+    n = left < step ? left : step;
+  }
+  RowTile t{};
+  t.seg = __builtin_amdgcn_readfirstlane(lo);
+  t.start = __builtin_amdgcn_readfirstlane(edge(a, t.seg));
+  const int end = __builtin_amdgcn_readfirstlane(edge(a, t.seg + 1));
+  const int toks = end > t.start ? end - t.start : 0;
+  t.rows = toks * a.group;
+  const int count = (t.rows + kRows - 1) / kRows;
+  const int nth = vt - (int)((int64_t)t.start * a.group / kRows) - t.seg;
+  // the last rows see the most tokens and come first
+  t.r0 = nth < count ? (count - 1 - nth) * kRows : t.rows;
+  if (t.seg == 0 || t.seg == a.B + 1) return t;
+  t.live = t.rows;
+  t.len = toks;
+  if constexpr (kPaged) {
+    const int b = t.seg - 1, cap = a.max_pages * a.c.page_size;
+    const int len = __builtin_amdgcn_readfirstlane(a.seq_lens[b]);
+    t.len = len < 0 ? 0 : (len > cap ? cap : len);
+    t.pos0 = t.len - toks;
+    t.live = (toks < a.max_q ? toks : a.max_q) * a.group;
+  }
+  const int r1 = t.r0 + kRows < t.live ? t.r0 + kRows : t.live;
+  if (t.r0 >= r1) return t;
+  const int lo_pos = t.pos0 + t.r0 / a.group, upto = t.pos0 + (r1 - 1) / a.group + 1;
+  if (upto <= 0) return t;
+  const int64_t from = a.window > 0 ? (int64_t)lo_pos - a.window + 1 : 0;
+  t.first = (from < 0 ? 0 : (int)from) / kTok;
+  const int sinks = a.sinks < upto ? a.sinks : upto;
+  t.nsink = (sinks + kTok - 1) / kTok;
+  t.nsink = t.nsink < t.first ? t.nsink : t.first;
+  t.tiles = t.nsink + (upto + kTok - 1) / kTok - t.first;
+  return t;
+}
+
+// Token tiles of one split, and how many splits have some.
+constexpr int kMinTiles = 4;
+__device__ __forceinline__ int per_split(const RowTile& t, int splits) {
+  const int per = (t.tiles + splits - 1) / splits;
+  return per < kMinTiles ? kMinTiles : per;
+}
+
+// Where the head's output row of row r of a segment lies.
+__device__ __forceinline__ int64_t out_row(const TileAttentionArgs& a, const RowTile& t, int h,
+                                           int r) {
+  return ((int64_t)t.start + r / a.group) * a.heads * a.group + h * a.group + r % a.group;
+}
+
+// A block of 32 cached tokens: where it is and its exponents.
+struct Block {
+  int64_t ph;
+  int sub;
+  bool mapped;
+};
+__device__ __forceinline__ int page_id(const TileAttentionArgs& a, const int32_t* table, int block) {
+  const int pi = kv_page_of(a.c, block);
+  return __builtin_amdgcn_readfirstlane(pi < a.max_pages ? table[pi] : -1);
+}
+__device__ __forceinline__ Block block_at(const TileAttentionArgs& a, int h, int block, int page) {
+  const bool mapped = page >= 0 && page < a.c.num_pages;
+  return Block{(int64_t)(mapped ? page : 0) * a.c.heads + h,
+               block - kv_page_of(a.c, block) * (a.c.page_size / kKvBlock), mapped};
+}
+
+// One (tile of rows, head, split).
+template <typename T, int D, bool kPaged>
+__global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_attention_kernel(
+    TileAttentionArgs a) {
+  using P = std::conditional_t<kPaged, Fp16, T>;  // type of probabilities and values
+  constexpr int kThreads = 64 * tile_waves(D);
+  constexpr int kTok = tile_tokens(D), kHalves = kTok / 32;
+  constexpr int kRowBytes = 2 * D, kTileBytes = kTok * kRowBytes;
+  constexpr int kPieces = kTok * D / 8;  // 16-byte pieces of a tile in LDS
+  constexpr int kLoads = kPaged ? (kPieces / 2 + kThreads - 1) / kThreads : kPieces / kThreads;
+  constexpr int kDimTiles = D / 32, kSteps = D / 16;
+  // of two 16-bit values: their exponents, and what carries exponents of all ones into the signs
+  constexpr unsigned kExps = P::kExp * 0x10001u, kCarry = (0x8000u - P::kExp) * 0x10001u;
+  __shared__ __attribute__((aligned(1024))) char lds[2][2][kTileBytes];  // [buffer][k, v]
+
+  // Workgroups that follow each other go to different XCDs; a head's stay on the same ones.
+  const int h = blockIdx.x % a.heads;
+  const unsigned rest = blockIdx.x / a.heads;
+  const int split = rest % a.splits;
+  const RowTile t = row_tile<D, kPaged>(a, rest / a.splits);
+  if (t.r0 >= t.rows) return;
+  const int per = per_split(t, a.splits);
+  const int i0 = split * per;
+  if (split > 0 && i0 >= t.tiles) return;
+  const int i1 = i0 + per < t.tiles ? i0 + per : t.tiles;
+  const int active = (t.tiles + per - 1) / per;
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 31, hh = lane >> 5;
+  const int w0 = t.r0 + wave * 32;  // the wavefront's rows
+  const int row = w0 + n;
+  const bool live = row < t.live;
+  const int pos = live ? t.pos0 + row / a.group : -1;
+  // positions of the wavefront's rows; lo > hi: none
+  const int w1 = w0 + 32 < t.live ? w0 + 32 : t.live;
+  const int lo_pos = w0 < t.live ? t.pos0 + w0 / a.group : 0;
+  const int hi_pos = w0 < t.live ? t.pos0 + (w1 - 1) / a.group : -1;
+
+  // queries as the second operand: dims 16 m + 8 hh + i of row n
+  u32x4 q[kSteps];
+  {
+    const int64_t at = ((int64_t)t.start + row / a.group) * a.qs.token +
+                       (int64_t)(h * a.group + row % a.group) * a.qs.head;
+    const char* p = (const char*)a.q + at * 2 + hh * 16;
+#pragma unroll
+    for (int m = 0; m < kSteps; ++m)
+      q[m] = live ? (u32x4) * (const u32x4_a2*)(p + m * 32) : u32x4{0, 0, 0, 0};
+  }
+
+  f32x16 o[kDimTiles];
+#pragma unroll
+  for (int c = 0; c < kDimTiles; ++c)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[c][e] = 0.f;
+  float mx = kNoMax, l = 0.f;
+  bool large = false;
+
+  // ---- tokens on their way: a tile's pieces in registers
+  u32x4 kr[kLoads], vr[kLoads];
+  const int32_t* table = kPaged ? a.page_table + (int64_t)(t.seg - 1) * a.max_pages : nullptr;
+  auto first_block = [&](int i) {  // 32-token block of list entry i
+    return (i < t.nsink ? i : t.first + i - t.nsink) * kHalves;
+  };
+  // of the tile in registers: exponents, references of the values' units, and what is mapped
+  int ek[kHalves], vref[kHalves], ref = 0;
+  float vscale[kHalves];
+  bool mapped[kHalves], any_ref = false;
+  int pages[kHalves];  // ids of the tile after it
+#pragma unroll
+  for (int x = 0; x < kHalves; ++x) {
+    ek[x] = vref[x] = 0;
+    pages[x] = -1;
+    vscale[x] = 1.f;
+    mapped[x] = true;
+  }
+  auto fetch_pages = [&](int i) {
+    if constexpr (kPaged) {
+#pragma unroll
+      for (int x = 0; x < kHalves; ++x)
+        pages[x] = page_id(a, table, __builtin_amdgcn_readfirstlane(first_block(i) + x));
+    }
+  };
+  auto load = [&](int i) {
+    const int block0 = __builtin_amdgcn_readfirstlane(first_block(i));
+    if constexpr (kPaged) {
+      Block bl[kHalves];
+      float ks[kHalves], vs[kHalves];
+#pragma unroll
+      for (int x = 0; x < kHalves; ++x) {
+        bl[x] = block_at(a, h, block0 + x, pages[x]);
+        mapped[x] = bl[x].mapped;
+        const int64_t at = bl[x].ph * (a.c.page_size / kKvBlock) + bl[x].sub;
+        ks[x] = mapped[x] ? a.c.k_scale[at] : 1.f;
+        vs[x] = mapped[x] ? a.c.v_scale[at] : 1.f;
+      }
+#pragma unroll
+      for (int y = 0; y < kLoads; ++y) {
+        const int c = threadIdx.x + y * kThreads;  // 16 codes: of block c / 2D
+        kr[y] = vr[y] = u32x4{0, 0, 0, 0};
+        if (c >= kPieces / 2) continue;
+        const int x = __builtin_amdgcn_readfirstlane(c / (2 * D));
+        const int u = c % (2 * D);
+        const Block& w = bl[kHalves > 1 && x ? kHalves - 1 : 0];
+        if (!w.mapped) continue;
+        const int64_t base = w.ph * a.c.page_size * D;
+        // keys: slab u / 128, token u / 4 of it, dims 16 (u % 4) and up
+        kr[y] = *(const u32x4*)(a.c.k + base + (int64_t)(u >> 7) * a.c.page_size * 64 +
+                                w.sub * (kKvBlock * 64) + (u & 127) * 16);
+        vr[y] = *(const u32x4*)(a.c.v + base + (int64_t)w.sub * kKvBlock * D + u * 16);
+      }
+#pragma unroll
+      for (int x = 0; x < kHalves; ++x) {
+        ek[x] = __builtin_amdgcn_readfirstlane(kv_exp_of(ks[x]));
+        const int ev = __builtin_amdgcn_readfirstlane(kv_exp_of(vs[x]));
+        if (!any_ref || ev - ref < kRefLo || ev - ref > kRefHi) ref = ev - 1;
+        any_ref = true;
+        vref[x] = ref;
+        vscale[x] = kv_pow2(ev - ref);
+      }
+    } else {
+#pragma unroll
+      for (int y = 0; y < kLoads; ++y) {
+        const int c = threadIdx.x + y * kThreads;
+        const int tok = block0 * 32 + c / (D / 8);
+        kr[y] = vr[y] = u32x4{0, 0, 0, 0};
+        if (tok < t.len) {
+          const int64_t at = (int64_t)t.start + tok;
+          const int off = c % (D / 8) * 16;
+          kr[y] = *(const u32x4_a2*)((const char*)a.k + (at * a.ks.token + h * a.ks.head) * 2 + off);
+          vr[y] = *(const u32x4_a2*)((const char*)a.v + (at * a.vs.token + h * a.vs.head) * 2 + off);
+        }
+      }
+    }
+  };
+  // registers to LDS
+  auto store = [&](int buf) {
+    char* kl = lds[buf][0];
+    char* vl = lds[buf][1];
+#pragma unroll
+    for (int y = 0; y < kLoads; ++y) {
+      const int c = threadIdx.x + y * kThreads;
+      if constexpr (kPaged) {
+        if (c >= kPieces / 2) continue;
+        const int x = __builtin_amdgcn_readfirstlane(c / (2 * D)), u = c % (2 * D);
+        // keys: token 16 j + 8 s + 4 h + i goes to row 16 s + 8 j + 4 h + i
+        const int tok = (u & 127) >> 2, r = (tok & 7) | (tok & 8) << 1 | (tok & 16) >> 1;
+        const int at = x * 32 + r, piece = (u >> 7) * 8 + (u & 3) * 2;
+        u32x4 w[2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e >> 1][2 * (e & 1)] = T::template widen<false>(kr[y][e], 1.f);
+          w[e >> 1][2 * (e & 1) + 1] = T::template widen<true>(kr[y][e], 1.f);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *(u32x4*)(kl + at * kRowBytes + ((piece + e) ^ swizzle<D>(at)) * 16) = w[e];
+        // values: [block][dim][4 groups of eight tokens]
+        const int dim = (u >> 6) * 32 + (u >> 2 & 15) * 2, g = u & 3;
+        const float sc = vscale[kHalves > 1 && x ? kHalves - 1 : 0];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e >> 1][2 * (e & 1)] = Fp16::widen<false>(vr[y][e], sc);
+          w[e >> 1][2 * (e & 1) + 1] = Fp16::widen<true>(vr[y][e], sc);
+        }
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          *(u32x4*)(vl + ((x * D + dim + f) * 4 + (g ^ ((dim + f) >> 2 & 3))) * 16) = w[f];
+      } else {
+        const int tok = c / (D / 8), piece = c % (D / 8);
+        const int at = tok * kRowBytes + (piece ^ swizzle<D>(tok)) * 16;
+        *(u32x4*)(kl + at) = kr[y];
+        *(u32x4*)(vl + at) = vr[y];
+      }
+    }
+  };
+
+  // ---- LDS addresses of the operands
+  const int kat = n * kRowBytes + (hh ^ swizzle<D>(n)) * 16;  // piece 2 m + hh: xor 32 m
+  auto key = [&](const char* kl, int half, int m) {
+    return *(const u32x4*)(kl + half * 32 * kRowBytes + (kat ^ (32 * m)));
+  };
+  // values of step s (16 slots) and dims 32 c: [lane's dim][its eight tokens]
+  auto value = [&](const char* vl, int s, int c) {
+    if constexpr (kPaged) {
+      const int g = 2 * (s & 1) + hh;
+      return *(const u32x4*)(vl + (((s >> 1) * D + 32 * c + n) * 4 + (g ^ (n >> 2 & 3))) * 16);
+    } else {
+      const int u = lane & 15;
+      u32x4 r;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int tok = 16 * s + 8 * x + 4 * hh + (u >> 2);
+        const int piece = 4 * c + (lane >> 4 & 1) * 2 + (u >> 1 & 1);
+        const char* p = vl + tok * kRowBytes + (piece ^ swizzle<D>(tok)) * 16 + (u & 1) * 8;
+        const u32x2 w = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                       (__attribute__((address_space(3))) i16x4*)(char*)p));
+        r[2 * x] = w[0];
+        r[2 * x + 1] = w[1];
+      }
+      return r;
+    }
+  };
+  // token of score e of a half
+  auto token = [&](int half, int e) {
+    return kPaged ? 32 * half + 16 * (e >> 2 & 1) + 8 * (e >> 3) + 4 * hh + (e & 3)
+                  : 32 * half + 8 * (e >> 2) + 4 * hh + (e & 3);
+  };
+
+  // A half's infinities and NaN, into the rows that see their tokens.  Rare, and so without haste.
+  auto sees = [&](int j) {
+    return j <= pos && (a.window == 0 || pos - j < a.window || j < a.sinks);
+  };
+  auto add_special = [&](f32x16(&to)[kDimTiles], const char* vl, int half, int j0, bool is_mapped) {
+#pragma unroll 1
+    for (int u = 0; u < 32; ++u) {
+      const bool see = is_mapped && sees(j0 + 32 * half + u);
+      if (!__any(see)) continue;
+#pragma unroll
+      for (int c = 0; c < kDimTiles; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int dim = 32 * c + 8 * (e >> 2) + 4 * hh + (e & 3), tok = 32 * half + u;
+          const char* p;
+          if constexpr (kPaged)
+            p = vl + ((half * D + dim) * 4 + ((u >> 2 & 3) ^ (dim >> 2 & 3))) * 16 +
+                (u >> 4) * 8 + (u & 3) * 2;
+          else
+            p = vl + tok * kRowBytes + ((dim >> 3) ^ swizzle<D>(tok)) * 16 + (dim & 7) * 2;
+          const unsigned v = *(const unsigned short*)p;
+          if (see && (v & P::kExp) == P::kExp) to[c][e] += P::value(v);
+        }
+    }
+  };
+
+  int unit = 0;  // the output sums' power of two
+  if (i0 < i1) {
+    fetch_pages(i0);
+    load(i0);
+    if (i0 + 1 < i1) fetch_pages(i0 + 1);
+  }
+  for (int i = i0; i < i1; ++i) {
+    const int buf = (i - i0) & 1;
+    store(buf);
+    // what the tile in LDS is, before the registers go to the next
+    int ek_now[kHalves], vref_now[kHalves];
+    bool mapped_now[kHalves], all_mapped = true;
+#pragma unroll
+    for (int x = 0; x < kHalves; ++x) {
+      ek_now[x] = ek[x];
+      vref_now[x] = vref[x];
+      mapped_now[x] = mapped[x];
+      all_mapped &= mapped[x];
+    }
+    if (i + 1 < i1) {
+      load(i + 1);
+      if (i + 2 < i1) fetch_pages(i + 2);
+    }
+    __syncthreads();
+    const char* kl = lds[buf][0];
+    const char* vl = lds[buf][1];
+    const int j0 = first_block(i) * 32;
+    // nothing for any of the wavefront's rows
+    if (j0 > hi_pos) continue;
+    if (a.window > 0 && j0 >= a.sinks && (int64_t)j0 + kTok - 1 <= (int64_t)lo_pos - a.window)
+      continue;
+
+    f32x16 sc[kHalves];
+#pragma unroll
+    for (int x = 0; x < kHalves; ++x) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sc[x][e] = 0.f;
+#pragma unroll
+      for (int m = 0; m < kSteps; ++m) sc[x] = T::mfma(key(kl, x, m), q[m], sc[x]);
+    }
+
+    // masks: only where some row does not see the whole tile
+    const bool whole = all_mapped && j0 + kTok - 1 <= lo_pos &&
+                       (a.window == 0 || hi_pos - j0 < a.window || j0 + kTok <= a.sinks);
+    bool clean = true;
+    if (!whole) {
+#pragma unroll
+      for (int x = 0; x < kHalves; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = j0 + token(x, e);
+          sc[x][e] = mapped_now[x] && sees(j) ? sc[x][e] : -__builtin_inff();
+        }
+      // exponents of all ones among the values
+      unsigned bad = 0;
+#pragma unroll
+      for (int s = 0; s < 2 * kHalves; ++s)
+#pragma unroll
+        for (int c = 0; c < kDimTiles; ++c) {
+          const u32x4 w = value(vl, s, c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            bad |= (w[e] & kExps) + kCarry;
+        }
+      clean = !__any((bad & 0x80008000u) != 0);
+    }
+
+    // running maximum
+    float cs[kHalves], top = -__builtin_inff();
+#pragma unroll
+    for (int x = 0; x < kHalves; ++x) {
+      cs[x] = kPaged ? a.scale_log2 * kv_pow2(ek_now[x]) : a.scale_log2;
+      float m = max3(sc[x][0], sc[x][1], sc[x][2]);
+#pragma unroll
+      for (int e = 3; e < 15; e += 2) m = max3(m, sc[x][e], sc[x][e + 1]);
+      m = product(max3(m, sc[x][15], sc[x][15]), cs[x]);
+      top = x == 0 ? m : __builtin_elementwise_maximum(top, m);
+    }
+    if (__any(top - mx > kPLimit - kPShift)) {
+      const float m = fmaxf(mx, pair_max(top));
+      large = __any(fabsf(m) > kLarge && m != kNoMax);
+      const float f = __builtin_amdgcn_exp2f(mx - m);
+      mx = m;
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < kDimTiles; ++c) o[c] *= f;
+    }
+    u32x4 p[2 * kHalves];
+#pragma unroll
+    for (int x = 0; x < kHalves; ++x) {
+      if (large) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sc[x][e] = product(sc[x][e], cs[x]) - mx + kPShift;
+      } else {
+        const float bias = kPShift - mx;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sc[x][e] = fmaf(sc[x][e], cs[x], bias);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        sc[x][e] = __builtin_amdgcn_exp2f(sc[x][e]);
+        l += sc[x][e];
+      }
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) p[2 * x + (e >> 3)][(e & 7) >> 1] = P::pack(sc[x][e], sc[x][e + 1]);
+    }
+
+    // outputs
+#pragma unroll
+    for (int x = 0; x < kHalves; ++x) {
+      if constexpr (kPaged) {
+        if (vref_now[x] != unit) {
+          const float f = kv_pow2(unit - vref_now[x]);
+          unit = vref_now[x];
+#pragma unroll
+          for (int c = 0; c < kDimTiles; ++c) o[c] *= f;
+        }
+      }
+      if (clean) {
+#pragma unroll
+        for (int s = 2 * x; s < 2 * x + 2; ++s)
+#pragma unroll
+          for (int c = 0; c < kDimTiles; ++c) o[c] = P::mfma(value(vl, s, c), p[s], o[c]);
+      } else {
+#pragma unroll
+        for (int s = 2 * x; s < 2 * x + 2; ++s)
+#pragma unroll
+          for (int c = 0; c < kDimTiles; ++c) {
+            u32x4 w = value(vl, s, c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] &= ~(((((w[e] & kExps) + kCarry) >> 15) & 0x10001u) * 0xffffu);
+            o[c] = P::mfma(w, p[s], o[c]);
+          }
+        add_special(o, vl, x, j0, mapped_now[x]);
+      }
+    }
+  }
+
+  // results: lane (n, hh) holds row n, dims 32 c + 8 q + 4 hh + i
+  l = pair_sum(l);
+  const bool none = l == 0.f || !live;
+  const float f = none ? 0.f : kv_pow2(unit) / l;
+#pragma unroll
+  for (int c = 0; c < kDimTiles; ++c)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[c][e] = none ? 0.f : o[c][e] * f;
+  if (active > 1) {
+    const int64_t rows = (int64_t)a.N * a.heads * a.group;
+    const int64_t at = split * rows + out_row(a, t, h, row);
+    if (row < t.rows) {
+#pragma unroll
+      for (int c = 0; c < kDimTiles; ++c)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *(f32x4*)(a.part_o + at * D + 32 * c + 8 * g + 4 * hh) =
+              f32x4{o[c][4 * g], o[c][4 * g + 1], o[c][4 * g + 2], o[c][4 * g + 3]};
+      if (hh == 0) a.part_ml[at] = none ? float2{-__builtin_inff(), 0.f} : float2{mx, l};
+    }
+    return;
+  }
+  char* to = (char*)a.out + out_row(a, t, h, row) * kRowBytes;
+#pragma unroll
+  for (int c = 0; c < kDimTiles; ++c)
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      // the two lanes of a row exchange halves: 16 bytes each
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const unsigned x = T::pack(o[c][4 * g + 2 * e], o[c][4 * g + 2 * e + 1]);
+        const unsigned y = T::pack(o[c][4 * g + 4 + 2 * e], o[c][4 * g + 5 + 2 * e]);
+        const auto z = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        w[e] = z[0];
+        w[2 + e] = z[1];
+      }
+      if (row < t.rows) *(u32x4*)(to + (32 * c + 8 * g + 8 * hh) * 2) = w;
+    }
+}
+
+// Joins the splits of the tiles that had more than one, in order: D / 4 lanes a row.
+template <typename T, int D, bool kPaged>
+__global__ __launch_bounds__(256) void tile_join_kernel(TileAttentionArgs a) {
+  constexpr int kLanes = D / 4, kRows = 256 / kLanes, kParts = tile_rows(D) / kRows;
+  const int part = blockIdx.x % kParts;
+  const unsigned rest = blockIdx.x / kParts;
+  const int h = rest % a.heads;
+  const RowTile t = row_tile<D, kPaged>(a, rest / a.heads);
+  const int per = per_split(t, a.splits);
+  const int active = (t.tiles + per - 1) / per;
+  const int row = t.r0 + part * kRows + threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+  if (active <= 1 || row >= t.rows) return;
+  const int64_t rows = (int64_t)a.N * a.heads * a.group, at = out_row(a, t, h, row);
+  float m = -__builtin_inff(), l = 0.f;
+  f32x4 x{0, 0, 0, 0};
+  for (int i = 0; i < active; i += 8) {
+    float2 ml[8];
+    f32x4 o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int j = i + k < active ? i + k : i;
+      ml[k] = a.part_ml[j * rows + at];
+      o[k] = *(const f32x4*)(a.part_o + (j * rows + at) * D + d);
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
+    const float z = top == -__builtin_inff() ? 0.f : top;
+    const float f = __builtin_amdgcn_exp2f(m - z);
+    x *= f;
+    l *= f;
+    m = top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i + k < active) {
+        // 0 for a split that saw nothing
+        const float w = __builtin_amdgcn_exp2f(ml[k].x - z) * ml[k].y;
+        l += w;
+        x += w * o[k];
+      }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *(u32x2*)((char*)a.out + (at * D + d) * 2) =
+      u32x2{T::pack(x[0] * inv, x[1] * inv), T::pack(x[2] * inv, x[3] * inv)};
+}
+
+// Numbers of row tiles (see RowTile).
+int64_t tile_numbers(const TileAttentionArgs& a, int dim) {
+  return (int64_t)a.N * a.group / tile_rows(dim) + a.B + 2;
+}
+
+}  // namespace
+
+size_t tile_attention_plan(TileAttentionArgs* a, int dim, bool paged) {
+  const int64_t cap = paged ? (int64_t)a->max_pages * a->c.page_size : a->N;
+  if (a->window >= cap + a->N) a->window = 0;
+  const int tok = tile_tokens(dim);
+  int64_t tiles = (cap + tok - 1) / tok;
+  if (a->window > 0) {
+    const int64_t seen = ((int64_t)a->window + tile_rows(dim) / a->group) / tok + 2 +
+                         ((int64_t)a->sinks + tok - 1) / tok;
+    tiles = seen < tiles ? seen : tiles;
+  }
+  // As many splits as find a place on the card at once, of at least kMinTiles tiles.
+  int64_t row_tiles = (int64_t)a->N * a->group / tile_rows(dim);
+  const int64_t least = a->B < a->N ? a->B : a->N;  // every request has one
+  row_tiles = row_tiles < least ? least : row_tiles;
+  const int64_t pairs = row_tiles * a->heads;
+  int64_t splits = pairs > 0 ? 256 / pairs : 1;
+  const int64_t most = tiles / kMinTiles;
+  splits = splits > most ? most : splits;
+  splits = splits < 1 ? 1 : splits;
+  a->splits = (int)splits;
+  if (splits == 1) return 0;
+  return (size_t)splits * a->N * a->heads * a->group * (dim + 2) * sizeof(float);
+}
+
+__int128 tile_attention_threads(const TileAttentionArgs& a, int dim) {
+  // the join's workgroups have 256 threads for 256 / (dim / 4) rows
+  const int64_t join = a.splits > 1 ? (int64_t)tile_rows(dim) * (dim / 4) : 0;
+  const int64_t main = (int64_t)a.splits * 64 * tile_waves(dim);
+  return __int128(tile_numbers(a, dim)) * a.heads * (main > join ? main : join);
+}
+
+void tile_attention_place(TileAttentionArgs* a, int dim, void* workspace) {
+  const size_t rows = (size_t)a->N * a->heads * a->group;
+  a->part_o = (float*)workspace;
+  a->part_ml = (float2*)(a->part_o + (size_t)a->splits * rows * dim);
+}
+
+namespace {
+
+template <typename T, int D, bool kPaged>
+hipError_t launch_dim(const TileAttentionArgs& a, hipStream_t st) {
+  const int64_t groups = tile_numbers(a, D) * a.heads;
+  hipLaunchKernelGGL((tile_attention_kernel<T, D, kPaged>), dim3((unsigned)(groups * a.splits)),
+                     dim3(64 * tile_waves(D)), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  constexpr int kParts = tile_rows(D) / (256 / (D / 4));
+  hipLaunchKernelGGL((tile_join_kernel<T, D, kPaged>), dim3((unsigned)(groups * kParts)), dim3(256),
+                     0, st, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool kPaged>
+hipError_t launch_type(const TileAttentionArgs& a, int dim, hipStream_t st) {
+  if (dim == 64) return launch_dim<T, 64, kPaged>(a, st);
+  if (dim == 128) return launch_dim<T, 128, kPaged>(a, st);
+  return launch_dim<T, 256, kPaged>(a, st);
+}
+
+template <bool kPaged>
+hipError_t launch(const TileAttentionArgs& a, int dim, KvType type, hipStream_t st) {
+  if (a.N <= 0) return hipSuccess;
+  return type == kFp16 ? launch_type<Fp16, kPaged>(a, dim, st)
+                       : launch_type<Bf16, kPaged>(a, dim, st);
+}
+
+}  // namespace
+
+hipError_t launch_prompt_attention(const TileAttentionArgs& a, int dim, KvType type,
+                                   hipStream_t st) {
+  return launch<false>(a, dim, type, st);
+}
+
+hipError_t launch_chunk_attention(const TileAttentionArgs& a, int dim, KvType type,
+                                  hipStream_t st) {
+  return launch<true>(a, dim, type, st);
+}
+
+}  // namespace sfx

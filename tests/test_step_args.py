@@ -281,3 +281,132 @@ def test_gradients_are_refused():
     with torch.no_grad():
         assert sfx._heads(x, "q", 2, 64, -1) == x.shape
     assert sfx._heads(x.detach(), "q", 2, 64, -1) == x.shape
+
+
+# ------------------------------------------------------------------ packed batches
+def reserve(B=1, mp=2, ps=64, np_=4, tokens=P, table=P, held=P, free=P, nf=P, ws=None, nws=0):
+    return sfx.load().sfx_pages_reserve(B, mp, ps, np_, tokens, table, held, free, nf, None, ws, nws,
+                                        None)
+
+
+def layout(B=1, N=1, mp=2, ps=64, np_=4, table=P, start=P, count=P, off=P, slots=P):
+    return sfx.load().sfx_step_layout(B, N, mp, ps, np_, table, start, count, off, None, None, None,
+                                      slots, None)
+
+
+def write_slots(c, N=1, slots=P, k=P, v=P, ty=0):
+    return sfx.load().sfx_kv_write_slots(ctypes.byref(c) if c else None, N, slots, k, None, v, None,
+                                         ty, None)
+
+
+def packed(c, B=1, N=1, max_q=1, H=4, mp=2, table=P, lens=P, off=P, q=P, out=P, ty=0, scale=0.1,
+           window=0, sinks=0, ws=None, nws=0):
+    return sfx.load().sfx_kv_attention_packed(ctypes.byref(c) if c else None, B, N, max_q, H, mp,
+                                              table, lens, off, q, None, out, ty, scale, window,
+                                              sinks, ws, nws, None)
+
+
+def prompt(B=1, N=1, H=4, Hk=2, D=128, off=P, q=P, k=P, v=P, out=P, ty=0, scale=0.1, window=0,
+           sinks=0, ws=None, nws=0):
+    return sfx.load().sfx_prompt_attention(B, N, H, Hk, D, off, q, None, k, None, v, None, out, ty,
+                                           scale, window, sinks, ws, nws, None)
+
+
+def test_bad_reserve():
+    for kw in (dict(B=-1), dict(mp=-1), dict(np_=-1), dict(ps=0), dict(ps=-64), dict(tokens=None),
+               dict(table=None), dict(held=None), dict(free=None), dict(nf=None)):
+        assert reserve(**kw) == sfx.EINVAL, kw
+    assert reserve(B=1 << 16, mp=1 << 16) == sfx.ECAPACITY
+    assert reserve(B=0, tokens=None, table=None, held=None, free=None, nf=None) == sfx.OK
+    L, n = sfx.load(), ctypes.c_size_t()
+    size = L.sfx_pages_reserve_workspace_bytes
+    assert size(1, 1, None) == sfx.EINVAL and size(-1, 1, ctypes.byref(n)) == sfx.EINVAL
+    assert size(1 << 16, 1 << 16, ctypes.byref(n)) == sfx.ECAPACITY
+    assert size(32, 32, ctypes.byref(n)) == sfx.OK and n.value == 0
+    assert size(4096, 256, ctypes.byref(n)) == sfx.OK and n.value > 0
+    assert reserve(B=4096, mp=256) == sfx.EINVAL                       # no workspace
+    assert reserve(B=4096, mp=256, ws=P, nws=n.value - 1) == sfx.EINVAL
+    assert reserve(B=4096, mp=256, ws=ctypes.c_void_p(72), nws=n.value) == sfx.EINVAL
+
+
+def test_bad_layout():
+    for kw in (dict(B=-1), dict(N=-1), dict(mp=-1), dict(ps=0), dict(np_=-1), dict(table=None),
+               dict(start=None), dict(count=None), dict(off=None)):
+        assert layout(**kw) == sfx.EINVAL, kw
+
+
+def test_bad_write_slots():
+    for kw, code in BAD_CACHE:
+        assert write_slots(cache(**kw)) == getattr(sfx, code), kw
+    for kw in (dict(N=-1), dict(slots=None), dict(k=None), dict(v=None), dict(ty=3), dict(ty=-1)):
+        assert write_slots(cache(), **kw) == sfx.EINVAL, kw
+    assert write_slots(None) == sfx.EINVAL
+    assert write_slots(cache(kv_heads=1 << 20), N=1 << 30) == sfx.ECAPACITY
+    assert write_slots(cache(kv_heads=2 ** 31 - 1), N=2 ** 31 - 1) == sfx.ECAPACITY
+    assert write_slots(cache(), N=0, slots=None, k=None, v=None) == sfx.OK
+
+
+def test_bad_packed_attention():
+    for kw, code in BAD_CACHE:
+        assert packed(cache(**kw)) == getattr(sfx, code), kw
+    for kw in (dict(B=-1), dict(N=-1), dict(max_q=-1), dict(mp=-1), dict(H=3), dict(H=0),
+               dict(table=None), dict(lens=None), dict(off=None), dict(q=None), dict(out=None),
+               dict(ty=2), dict(ty=5), dict(scale=0.0), dict(scale=float("nan")),
+               dict(scale=float("inf")), dict(window=-1), dict(sinks=-1),
+               dict(out=ctypes.c_void_p(72))):
+        assert packed(cache(), **kw) == sfx.EINVAL, kw
+    assert packed(None) == sfx.EINVAL
+    assert packed(cache(), mp=1 << 26) == sfx.ECAPACITY
+    assert packed(cache(), N=1 << 30) == sfx.ECAPACITY
+    assert packed(cache(kv_heads=2 ** 30), N=1, H=2 ** 30, B=1 << 24) == sfx.ECAPACITY
+    assert packed(cache(), N=0, lens=None, off=None, q=None, out=None) == sfx.OK
+    n = ctypes.c_size_t()
+    size = sfx.load().sfx_kv_attention_packed_workspace_bytes
+    c = cache()
+    assert size(ctypes.byref(c), 1, 500, 500, 4, 512, 0, 0, None) == sfx.EINVAL
+    assert size(ctypes.byref(c), 1, 500, 500, 4, 512, 0, 0, ctypes.byref(n)) == sfx.OK
+    assert n.value > 0  # few rows over a long table are split
+    for kw in (dict(), dict(ws=P, nws=n.value - 1), dict(ws=ctypes.c_void_p(72), nws=n.value)):
+        assert packed(c, N=500, max_q=500, mp=512, **kw) == sfx.EINVAL, kw
+
+
+def test_bad_prompt_attention():
+    for kw in (dict(B=-1), dict(N=-1), dict(H=3), dict(H=0), dict(Hk=0), dict(Hk=-2), dict(D=96),
+               dict(D=0), dict(off=None), dict(q=None), dict(k=None), dict(v=None), dict(out=None),
+               dict(ty=2), dict(ty=-1), dict(scale=0.0), dict(scale=-1.0),
+               dict(scale=float("nan")), dict(scale=2.0 ** 65), dict(window=-1), dict(sinks=-1),
+               dict(out=ctypes.c_void_p(72))):
+        assert prompt(**kw) == sfx.EINVAL, kw
+    assert prompt(N=1 << 30) == sfx.ECAPACITY
+    assert prompt(B=2 ** 31 - 1) == sfx.ECAPACITY
+    assert prompt(N=0, off=None, q=None, k=None, v=None, out=None) == sfx.OK
+    n = ctypes.c_size_t()
+    size = sfx.load().sfx_prompt_attention_workspace_bytes
+    assert size(1, 4000, 1, 1, 128, 0, 0, None) == sfx.EINVAL
+    assert size(1, 4000, 1, 1, 128, 0, 0, ctypes.byref(n)) == sfx.OK and n.value > 0
+    for kw in (dict(), dict(ws=P, nws=n.value - 1), dict(ws=ctypes.c_void_p(72), nws=n.value)):
+        assert prompt(N=4000, H=1, Hk=1, **kw) == sfx.EINVAL, kw
+
+
+def test_python_refusals_of_packed_calls():
+    import torch
+
+    for a in ((-1, 64), (4, 0), (2 ** 31, 64)):
+        with pytest.raises(ValueError):
+            sfx.PagePool(*a, device="cpu")
+    pool = sfx.PagePool(4, 64, device="cpu")
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        pool.reserve(i[None], i, i)
+    with pytest.raises(TypeError):
+        pool.layout(i[None], i, i, 1)
+    with pytest.raises(TypeError):
+        sfx.PagePool(4, 64, buffers=(torch.zeros(4, dtype=torch.int32), i))
+    c = sfx.KVCache(2, 64, 2, 64, device="cpu")
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        c.write_slots(x, x, i.long())
+    with pytest.raises(TypeError):
+        c.attend_packed(x, i[None], i, i)
+    with pytest.raises(TypeError):
+        sfx.attend_prompt(x, x, x, i)
