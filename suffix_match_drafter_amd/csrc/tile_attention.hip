@@ -27,9 +27,8 @@
 // values' range fp16 does not hold.  Each weight's rounding is its own, so their error in a sum of
 // many tokens is below the result's own rounding.  Denominators add the unrounded weights in fp32.
 //
-// Infinities and NaN among the values reach only the rows that see their token: a tile that some row
-// does not see in full is searched for them, and where there are any they are taken out of the
-// product and added to the rows that see them.
+// Infinities and NaN among the values reach only the rows that see their token: they are left out of
+// a tile that some row does not see in full, and added at the end to the rows that see them.
 #include "tile_attention.h"
 
 #include <hip/hip_bf16.h>
@@ -150,6 +149,7 @@ struct RowTile {
   int r0;                 // first row of the tile; rows: none
   int pos0;               // position of the segment's first token
   int len;                // tokens of the request
+  int lo_pos, hi_pos;     // positions of the tile's rows
   int nsink, first, tiles;  // token tiles: [0, nsink), then [first, ...): `tiles` in all
 };
 
@@ -190,9 +190,11 @@ __device__ __forceinline__ RowTile row_tile(const TileAttentionArgs& a, int vt) 
   }
   const int r1 = t.r0 + kRows < t.live ? t.r0 + kRows : t.live;
   if (t.r0 >= r1) return t;
-  const int lo_pos = t.pos0 + t.r0 / a.group, upto = t.pos0 + (r1 - 1) / a.group + 1;
+  t.lo_pos = t.pos0 + t.r0 / a.group;
+  t.hi_pos = t.pos0 + (r1 - 1) / a.group;
+  const int upto = t.hi_pos + 1;
   if (upto <= 0) return t;
-  const int64_t from = a.window > 0 ? (int64_t)lo_pos - a.window + 1 : 0;
+  const int64_t from = a.window > 0 ? (int64_t)t.lo_pos - a.window + 1 : 0;
   t.first = (from < 0 ? 0 : (int)from) / kTok;
   const int sinks = a.sinks < upto ? a.sinks : upto;
   t.nsink = (sinks + kTok - 1) / kTok;
@@ -206,6 +208,11 @@ constexpr int kMinTiles = 4;
 __device__ __forceinline__ int per_split(const RowTile& t, int splits) {
   const int per = (t.tiles + splits - 1) / splits;
   return per < kMinTiles ? kMinTiles : per;
+}
+
+// Bytes of a dword that are e4m3 NaNs, as 0x80 flags.
+__device__ __forceinline__ unsigned nan_bytes(unsigned w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
 // Where the head's output row of row r of a segment lies.
@@ -244,6 +251,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
   // of two 16-bit values: their exponents, and what carries exponents of all ones into the signs
   constexpr unsigned kExps = P::kExp * 0x10001u, kCarry = (0x8000u - P::kExp) * 0x10001u;
   __shared__ __attribute__((aligned(1024))) char lds[2][2][kTileBytes];  // [buffer][k, v]
+  __shared__ int special;
 
   // Workgroups that follow each other go to different XCDs; a head's stay on the same ones.
   const int h = blockIdx.x % a.heads;
@@ -354,19 +362,18 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
 #pragma unroll
       for (int y = 0; y < kLoads; ++y) {
         const int c = threadIdx.x + y * kThreads;
-        const int tok = block0 * 32 + c / (D / 8);
-        kr[y] = vr[y] = u32x4{0, 0, 0, 0};
-        if (tok < t.len) {
-          const int64_t at = (int64_t)t.start + tok;
-          const int off = c % (D / 8) * 16;
-          kr[y] = *(const u32x4_a2*)((const char*)a.k + (at * a.ks.token + h * a.ks.head) * 2 + off);
-          vr[y] = *(const u32x4_a2*)((const char*)a.v + (at * a.vs.token + h * a.vs.head) * 2 + off);
-        }
+        int tok = block0 * 32 + c / (D / 8);
+        tok = tok < t.len ? tok : t.len - 1;  // past the end: seen by no row
+        const int64_t at = (int64_t)t.start + tok;
+        const int off = c % (D / 8) * 16;
+        kr[y] = *(const u32x4_a2*)((const char*)a.k + (at * a.ks.token + h * a.ks.head) * 2 + off);
+        vr[y] = *(const u32x4_a2*)((const char*)a.v + (at * a.vs.token + h * a.vs.head) * 2 + off);
       }
     }
   };
-  // registers to LDS
-  auto store = [&](int buf) {
+  // Registers to LDS.  Of a tile that some row does not see in full the infinities and NaN among the
+  // values are left out (0 times one would be NaN in every row) and dealt with at the end.
+  auto store = [&](int buf, bool clean) {
     char* kl = lds[buf][0];
     char* vl = lds[buf][1];
 #pragma unroll
@@ -390,6 +397,16 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
         // values: [block][dim][4 groups of eight tokens]
         const int dim = (u >> 6) * 32 + (u >> 2 & 15) * 2, g = u & 3;
         const float sc = vscale[kHalves > 1 && x ? kHalves - 1 : 0];
+        if (clean) {
+          unsigned bad = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const unsigned nan = nan_bytes(vr[y][e]);
+            bad |= nan;
+            vr[y][e] &= ~((nan >> 7) * 255u);
+          }
+          if (__any(bad != 0)) special = 1;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           w[e >> 1][2 * (e & 1)] = Fp16::widen<false>(vr[y][e], sc);
@@ -401,6 +418,16 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
       } else {
         const int tok = c / (D / 8), piece = c % (D / 8);
         const int at = tok * kRowBytes + (piece ^ swizzle<D>(tok)) * 16;
+        if (clean) {
+          unsigned bad = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const unsigned f = ((vr[y][e] & kExps) + kCarry) & 0x80008000u;
+            bad |= f;
+            vr[y][e] &= ~((f >> 15) * 0xffffu);
+          }
+          if (__any(bad != 0)) special = 1;
+        }
         *(u32x4*)(kl + at) = kr[y];
         *(u32x4*)(vl + at) = vr[y];
       }
@@ -440,32 +467,17 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
                   : 32 * half + 8 * (e >> 2) + 4 * hh + (e & 3);
   };
 
-  // A half's infinities and NaN, into the rows that see their tokens.  Rare, and so without haste.
   auto sees = [&](int j) {
     return j <= pos && (a.window == 0 || pos - j < a.window || j < a.sinks);
   };
-  auto add_special = [&](f32x16(&to)[kDimTiles], const char* vl, int half, int j0, bool is_mapped) {
-#pragma unroll 1
-    for (int u = 0; u < 32; ++u) {
-      const bool see = is_mapped && sees(j0 + 32 * half + u);
-      if (!__any(see)) continue;
-#pragma unroll
-      for (int c = 0; c < kDimTiles; ++c)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int dim = 32 * c + 8 * (e >> 2) + 4 * hh + (e & 3), tok = 32 * half + u;
-          const char* p;
-          if constexpr (kPaged)
-            p = vl + ((half * D + dim) * 4 + ((u >> 2 & 3) ^ (dim >> 2 & 3))) * 16 +
-                (u >> 4) * 8 + (u & 3) * 2;
-          else
-            p = vl + tok * kRowBytes + ((dim >> 3) ^ swizzle<D>(tok)) * 16 + (dim & 7) * 2;
-          const unsigned v = *(const unsigned short*)p;
-          if (see && (v & P::kExp) == P::kExp) to[c][e] += P::value(v);
-        }
-    }
+  // every row of the workgroup sees the whole tile
+  auto all_see = [&](int j0) {
+    return j0 + kTok - 1 <= t.lo_pos &&
+           (a.window == 0 || t.hi_pos - j0 < a.window || j0 + kTok <= a.sinks);
   };
 
+  if (threadIdx.x == 0) special = 0;
+  __syncthreads();
   int unit = 0;  // the output sums' power of two
   if (i0 < i1) {
     fetch_pages(i0);
@@ -474,7 +486,8 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
   }
   for (int i = i0; i < i1; ++i) {
     const int buf = (i - i0) & 1;
-    store(buf);
+    const int j0 = first_block(i) * 32;
+    store(buf, !all_see(j0));
     // what the tile in LDS is, before the registers go to the next
     int ek_now[kHalves], vref_now[kHalves];
     bool mapped_now[kHalves], all_mapped = true;
@@ -492,7 +505,6 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
     __syncthreads();
     const char* kl = lds[buf][0];
     const char* vl = lds[buf][1];
-    const int j0 = first_block(i) * 32;
     // nothing for any of the wavefront's rows
     if (j0 > hi_pos) continue;
     if (a.window > 0 && j0 >= a.sinks && (int64_t)j0 + kTok - 1 <= (int64_t)lo_pos - a.window)
@@ -510,7 +522,6 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
     // masks: only where some row does not see the whole tile
     const bool whole = all_mapped && j0 + kTok - 1 <= lo_pos &&
                        (a.window == 0 || hi_pos - j0 < a.window || j0 + kTok <= a.sinks);
-    bool clean = true;
     if (!whole) {
 #pragma unroll
       for (int x = 0; x < kHalves; ++x)
@@ -519,18 +530,6 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
           const int j = j0 + token(x, e);
           sc[x][e] = mapped_now[x] && sees(j) ? sc[x][e] : -__builtin_inff();
         }
-      // exponents of all ones among the values
-      unsigned bad = 0;
-#pragma unroll
-      for (int s = 0; s < 2 * kHalves; ++s)
-#pragma unroll
-        for (int c = 0; c < kDimTiles; ++c) {
-          const u32x4 w = value(vl, s, c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            bad |= (w[e] & kExps) + kCarry;
-        }
-      clean = !__any((bad & 0x80008000u) != 0);
     }
 
     // running maximum
@@ -584,23 +583,49 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
           for (int c = 0; c < kDimTiles; ++c) o[c] *= f;
         }
       }
-      if (clean) {
 #pragma unroll
-        for (int s = 2 * x; s < 2 * x + 2; ++s)
+      for (int s = 2 * x; s < 2 * x + 2; ++s)
 #pragma unroll
-          for (int c = 0; c < kDimTiles; ++c) o[c] = P::mfma(value(vl, s, c), p[s], o[c]);
-      } else {
+        for (int c = 0; c < kDimTiles; ++c) o[c] = P::mfma(value(vl, s, c), p[s], o[c]);
+    }
+  }
+
+  // Infinities and NaN that `store` took out: added to the rows that see their tokens.
+  __syncthreads();
+  if (special) {
+    for (int i = i0; i < i1; ++i) {
+      const int j0 = first_block(i) * 32;
+      if (all_see(j0)) continue;
+#pragma unroll 1
+      for (int u = 0; u < kTok; ++u) {
+        const int j = j0 + u;
+        if (j >= t.len || !__any(sees(j))) continue;
+        const bool see = sees(j);
+        if constexpr (kPaged) {
+          const int block = __builtin_amdgcn_readfirstlane(j >> 5);
+          const Block w = block_at(a, h, block, page_id(a, table, block));
+          if (!w.mapped) continue;
+          const uint8_t* p = a.c.v + w.ph * a.c.page_size * D + (int64_t)w.sub * kKvBlock * D +
+                             (u >> 2 & 3) * 16 + (u >> 4 & 1) * 4 + (u & 3);
 #pragma unroll
-        for (int s = 2 * x; s < 2 * x + 2; ++s)
+          for (int c = 0; c < kDimTiles; ++c)
 #pragma unroll
-          for (int c = 0; c < kDimTiles; ++c) {
-            u32x4 w = value(vl, s, c);
+            for (int e = 0; e < 16; ++e) {
+              const int dim = 8 * (e >> 2) + 4 * hh + (e & 3);
+              if (see && (p[c * 1024 + (dim >> 1) * 64 + (dim & 1) * 8] & 127) == 127)
+                o[c][e] = __builtin_nanf("");
+            }
+        } else {
+          const unsigned short* p = (const unsigned short*)a.v +
+                                    (((int64_t)t.start + j) * a.vs.token + h * a.vs.head);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] &= ~(((((w[e] & kExps) + kCarry) >> 15) & 0x10001u) * 0xffffu);
-            o[c] = P::mfma(w, p[s], o[c]);
-          }
-        add_special(o, vl, x, j0, mapped_now[x]);
+          for (int c = 0; c < kDimTiles; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const unsigned v = p[32 * c + 8 * (e >> 2) + 4 * hh + (e & 3)];
+              if (see && (v & P::kExp) == P::kExp) o[c][e] += P::value(v);
+            }
+        }
       }
     }
   }
