@@ -14,12 +14,18 @@ struct KvAttentionArgs {
   const void* q;
   KvStrides qs;
   void* out;              // [B, T, heads * group, dim]
+  // packed rows [N, heads * group, dim] (offsets NULL: not packed): request b has those from
+  // offsets[b] to offsets[b + 1], of which the first max_q attend; T is planned for, and requests
+  // of more than T rows are left to the caller unless max_q <= T
+  const int32_t* offsets;
+  int32_t N, max_q;
   float scale_log2;       // softmax scale * log2(e)
   int32_t window, sinks;  // window 0: no window
   // plan (kv_attention_plan)
   int32_t chunks;           // workgroups over the rows of one request and head
   int32_t splits;           // workgroups over the tokens
-  int32_t tiles_per_split;  // 32-token tiles of one split
+  int32_t tiles_per_split;  // 32-token tiles of one split (packed: by each request's own tiles)
+  bool zero;                // packed: no other call zeroes the rows of no request
   float* part_o;            // [splits][B * heads * T * group][dim]  (splits > 1)
   float2* part_ml;          // [splits][B * heads * T * group]: maximum, sum
 };

@@ -138,19 +138,34 @@ __device__ __forceinline__ float group_sum(float x) {
 // What rows [r0, r0 + n) of request b look at: tiles [0, nsink) for the sinks, then
 // [first, last).  Tile i of the list is i < nsink ? i : first + i - nsink.
 struct Span {
+  int start;  // packed: the request's first row, and how many rows it has
+  int count;
   int pos0;  // position of the first of the newest tokens
   int rows;  // live rows of the request and head
   int lo_pos, hi_pos;
   int nsink, first, tiles;
 };
 
+template <bool kPacked>
 __device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int r0, int n) {
   Span s{};
   const int cap = a.max_pages * a.c.page_size;
-  int len = a.seq_lens[b], nq = a.q_lens ? a.q_lens[b] : a.T;
+  int len = a.seq_lens[b], nq;
   len = len < 0 ? 0 : (len > cap ? cap : len);
-  nq = nq < 0 ? 0 : (nq > a.T ? a.T : nq);
-  s.pos0 = len - nq;
+  if constexpr (kPacked) {
+    int from = a.offsets[b], to = a.offsets[b + 1];
+    from = from < 0 ? 0 : (from > a.N ? a.N : from);
+    to = to < from ? from : (to > a.N ? a.N : to);
+    s.start = from;
+    s.count = to - from;
+    s.pos0 = len - s.count;
+    nq = s.count < a.max_q ? s.count : a.max_q;
+    if (nq > a.T) nq = 0;  // another call's
+  } else {
+    nq = a.q_lens ? a.q_lens[b] : a.T;
+    nq = nq < 0 ? 0 : (nq > a.T ? a.T : nq);
+    s.pos0 = len - nq;
+  }
   s.rows = nq * a.group;
   const int r1 = r0 + n < s.rows ? r0 + n : s.rows;
   if (r0 >= r1) return s;
@@ -166,6 +181,35 @@ __device__ __forceinline__ Span span_of(const KvAttentionArgs& a, int b, int r0,
   s.nsink = s.nsink < s.first ? s.nsink : s.first;
   s.tiles = s.nsink + (end + kKvBlock - 1) / kKvBlock - s.first;
   return s;
+}
+
+// Tiles of one split.  Packed calls cut each request's own tiles into equal parts of at least four a
+// wavefront; the others cut the table's width.
+template <bool kPacked>
+__device__ __forceinline__ int per_split(const KvAttentionArgs& a, const Span& s) {
+  if constexpr (!kPacked) return a.tiles_per_split;
+  const int per = (s.tiles + a.splits - 1) / a.splits;
+  return per < 4 * kWaves ? 4 * kWaves : per;
+}
+
+// Where the output row of row `row` of request b and head h lies.
+template <bool kPacked>
+__device__ __forceinline__ int64_t out_row(const KvAttentionArgs& a, const Span& s, int b, int h,
+                                           int row) {
+  const int64_t token = kPacked ? (int64_t)s.start + row / a.group
+                                : (int64_t)b * a.T + row / a.group;
+  return token * a.c.heads * a.group + h * a.group + row % a.group;
+}
+
+// Zeroes head h's rows of tokens [from, to), every `step`-th.
+template <int D>
+__device__ void zero_rows(const KvAttentionArgs& a, int h, int64_t from, int64_t to, int64_t step) {
+  constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+  const int per = a.group * kPieces;
+  for (int64_t t = from; t < to; t += step)
+    for (int i = threadIdx.x; i < per; i += 64 * kWaves)
+      *(u32x4*)((char*)a.out + ((t * a.c.heads + h) * a.group * (int64_t)kPieces + i) * 16) =
+          u32x4{0, 0, 0, 0};
 }
 
 // Block number of list entry i; its page id (-1: unmapped), read through the scalar cache.
@@ -232,8 +276,9 @@ __device__ __forceinline__ unsigned nan_bytes(unsigned w) {
 constexpr int waves_per_simd(int D, int RT) { return D * RT <= 128 ? 3 : (D * RT <= 384 ? 2 : 1); }
 
 // One (chunk, split): RT 16-row tiles by the split's tokens.
-template <typename T, int D, int RT>
-__global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attention_kernel(KvAttentionArgs a) {
+template <typename T, int D, int RT, bool kPacked>
+__global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attention_kernel(
+    KvAttentionArgs a) {
   constexpr int kSlabs = D / 64, kVc = D / 32;
   constexpr int kPiece = D < 128 ? D : 128;  // dims of one pass of the final reduction
   __shared__ float red[kWaves][16][kPiece + 4];
@@ -254,11 +299,24 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
   if (b64 >= a.B) return;
   const int b = (int)b64;
   const int r0 = chunk * RT * 16, all_rows = a.T * a.group;
-  const Span s = span_of(a, b, r0, RT * 16);
-  const int i0 = split * a.tiles_per_split;
+  const Span s = span_of<kPacked>(a, b, r0, RT * 16);
+  if constexpr (kPacked) {
+    if (a.zero && split == 0 && chunk == 0) {
+      // rows past max_q, and this request's share of those of no request
+      zero_rows<D>(a, h, (int64_t)s.start + a.max_q, (int64_t)s.start + s.count, 1);
+      int lo = a.offsets[0], hi = a.offsets[a.B];
+      lo = lo < 0 ? 0 : (lo > a.N ? a.N : lo);
+      hi = hi < lo ? lo : (hi > a.N ? a.N : hi);
+      zero_rows<D>(a, h, b, lo, a.B);
+      zero_rows<D>(a, h, (int64_t)hi + b, a.N, a.B);
+    }
+    if (r0 >= s.rows) return;
+  }
+  const int per = per_split<kPacked>(a, s);
+  const int i0 = split * per;
   if (split > 0 && i0 >= s.tiles) return;
-  const int i1 = i0 + a.tiles_per_split < s.tiles ? i0 + a.tiles_per_split : s.tiles;
-  const int active = (s.tiles + a.tiles_per_split - 1) / a.tiles_per_split;
+  const int i1 = i0 + per < s.tiles ? i0 + per : s.tiles;
+  const int active = (s.tiles + per - 1) / per;
 
   // queries as the second operand: dims 64 j + 16 g + 8 f + i of row n
   typename T::Vec q[RT][2 * kSlabs];
@@ -269,9 +327,10 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
     const int t = row / a.group;
     const bool live = row < s.rows;
     pos[rt] = live ? s.pos0 + t : -1;
-    const char* p = (const char*)a.q +
-                    (b * a.qs.batch + t * a.qs.token + (h * a.group + row % a.group) * a.qs.head) *
-                        2 + g * 32;
+    const int64_t from = kPacked ? ((int64_t)s.start + t) * a.qs.token
+                                 : b * a.qs.batch + t * a.qs.token;
+    const char* p =
+        (const char*)a.q + (from + (h * a.group + row % a.group) * a.qs.head) * 2 + g * 32;
 #pragma unroll
     for (int m = 0; m < 2 * kSlabs; ++m) {
       const u32x4 w = live ? (u32x4) * (const u32x4_a2*)(p + (m >> 1) * 128 + (m & 1) * 16)
@@ -509,7 +568,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
       constexpr int kPer = kPiece / 16;  // dims of one thread
       const int rr = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * kPer;
       const int row = r0 + rt * 16 + rr;
-      if (row < all_rows) {
+      if (row < (kPacked ? s.rows : all_rows)) {
         float mm = sm[0][rt * 16 + rr], ll = 0.f;
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, sm[w][rt * 16 + rr]);
@@ -538,9 +597,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
             *(f32x4*)(a.part_o + at * D + d + e) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
           if (d == 0) a.part_ml[at] = none ? float2{-__builtin_inff(), 0.f} : float2{mm, ll};
         } else {
-          const int64_t at =
-              ((int64_t)b * a.T + row / a.group) * a.c.heads * a.group + h * a.group +
-              row % a.group;
+          const int64_t at = out_row<kPacked>(a, s, b, h, row);
           unsigned* p = (unsigned*)((char*)a.out + (at * D + d) * 2);
 #pragma unroll
           for (int e = 0; e < kPer; e += 2) p[e / 2] = T::pack(x[e], x[e + 1]);
@@ -556,7 +613,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D, RT)) void kv_attenti
 // its loads again and again (10 us for 64 splits of 65 rows, 4 with all of a workgroup on a row).
 // A split brings its maximum and its sum apart: as one logarithm the sum would be rounded to the
 // maximum's step, 4% of a split's weight at scores of 2^20 and all of it at 2^28.
-template <typename T, int D, int kGroups>
+template <typename T, int D, int kGroups, bool kPacked>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chunk_rows) {
   constexpr int kLanes = D / 4, kRows = 256 / kLanes / kGroups;
   __shared__ f32x4 xs[kRows][kGroups][kLanes];
@@ -570,8 +627,9 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chu
   const int row = live ? (int)(at % all_rows) : 0;
   const int h = live ? (int)(at / all_rows % a.c.heads) : 0;
   const int b = live ? (int)(at / all_rows / a.c.heads) : 0;
-  const Span s = span_of(a, b, row / chunk_rows * chunk_rows, chunk_rows);
-  const int active = live ? (s.tiles + a.tiles_per_split - 1) / a.tiles_per_split : 0;
+  const Span s = span_of<kPacked>(a, b, row / chunk_rows * chunk_rows, chunk_rows);
+  const int per = per_split<kPacked>(a, s);
+  const int active = live && !(kPacked && row >= s.rows) ? (s.tiles + per - 1) / per : 0;
   float m = -__builtin_inff(), l = 0.f;
   f32x4 x{0, 0, 0, 0};
   for (int i = group; active > 1 && i < active; i += 8 * kGroups) {
@@ -622,8 +680,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttentionArgs a, int chu
   }
   if (active <= 1) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t out =
-      ((int64_t)b * a.T + row / a.group) * a.c.heads * a.group + h * a.group + row % a.group;
+  const int64_t out = out_row<kPacked>(a, s, b, h, row);
   typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
   *(u32x2*)((char*)a.out + (out * D + d) * 2) =
       u32x2{T::pack(x[0] * inv, x[1] * inv), T::pack(x[2] * inv, x[3] * inv)};
@@ -695,32 +752,40 @@ void kv_attention_place(KvAttentionArgs* a, int dim, void* workspace) {
 
 namespace {
 
-template <typename T, int D>
-hipError_t launch_dim(const KvAttentionArgs& a, hipStream_t st) {
+template <typename T, int D, bool kPacked>
+hipError_t launch_rows(const KvAttentionArgs& a, hipStream_t st) {
   int chunks = 0;
   const int rt = row_tiles(a, D, &chunks);
   const dim3 grid((unsigned)grid_of(a));
   const dim3 block(64 * kWaves);
   if (rt == 1)
-    hipLaunchKernelGGL((kv_attention_kernel<T, D, 1>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((kv_attention_kernel<T, D, 1, kPacked>), grid, block, 0, st, a);
   if (rt == 2)
-    hipLaunchKernelGGL((kv_attention_kernel<T, D, 2>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((kv_attention_kernel<T, D, 2, kPacked>), grid, block, 0, st, a);
   if constexpr (D <= 128)
-    if (rt == 3) hipLaunchKernelGGL((kv_attention_kernel<T, D, 3>), grid, block, 0, st, a);
+    if (rt == 3)
+      hipLaunchKernelGGL((kv_attention_kernel<T, D, 3, kPacked>), grid, block, 0, st, a);
   if constexpr (D <= 64)
-    if (rt == 4) hipLaunchKernelGGL((kv_attention_kernel<T, D, 4>), grid, block, 0, st, a);
+    if (rt == 4)
+      hipLaunchKernelGGL((kv_attention_kernel<T, D, 4, kPacked>), grid, block, 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t rows = (int64_t)a.B * a.c.heads * a.T * a.group;
   // all of a workgroup on a row where there are many splits (then there are few rows)
   constexpr int kWide = 256 / (D / 4);
   if (a.splits > 4)
-    hipLaunchKernelGGL((kv_join_kernel<T, D, kWide>), dim3((unsigned)rows), dim3(256), 0, st, a,
-                       rt * 16);
+    hipLaunchKernelGGL((kv_join_kernel<T, D, kWide, kPacked>), dim3((unsigned)rows), dim3(256), 0,
+                       st, a, rt * 16);
   else
-    hipLaunchKernelGGL((kv_join_kernel<T, D, 1>), dim3((unsigned)((rows * (D / 4) + 255) / 256)),
-                       dim3(256), 0, st, a, rt * 16);
+    hipLaunchKernelGGL((kv_join_kernel<T, D, 1, kPacked>),
+                       dim3((unsigned)((rows * (D / 4) + 255) / 256)), dim3(256), 0, st, a,
+                       rt * 16);
   return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t launch_dim(const KvAttentionArgs& a, hipStream_t st) {
+  return a.offsets ? launch_rows<T, D, true>(a, st) : launch_rows<T, D, false>(a, st);
 }
 
 template <typename T>

@@ -170,17 +170,47 @@ int tile_plan(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads, int32_t h
   return SFX_OK;
 }
 
+// Requests of at most this many rows (tokens x query heads of a group) go to the kernel whose
+// wavefronts share out the tokens instead of the rows.
+constexpr int kFewRows = 128;
+
+struct PackedArgs {
+  KvAttentionArgs few;  // requests of few rows; few.T == 0: none
+  TileAttentionArgs many;
+  bool has_many;
+};
+
 int packed_plan(const sfx_kv_cache* cache, int32_t B, int32_t N, int32_t max_q, int32_t q_heads,
                 int32_t max_pages, const int32_t* page_table, int32_t window, int32_t sinks,
-                TileAttentionArgs* a, size_t* bytes) {
-  int rc = check_cache(cache, B, N, max_pages, page_table, &a->c);
+                PackedArgs* p, size_t* bytes) {
+  TileAttentionArgs& m = p->many;
+  int rc = check_cache(cache, B, N, max_pages, page_table, &m.c);
   if (!rc) rc = check_heads(q_heads, cache->kv_heads, window, sinks);
   if (rc) return rc;
   if (max_q < 0) return fail(SFX_EINVAL, "negative max_q=%d", max_q);
-  a->max_pages = max_pages;
-  a->max_q = max_q < N ? max_q : N;
-  a->page_table = page_table;
-  return tile_plan(B, N, q_heads, cache->kv_heads, cache->head_dim, window, sinks, true, a, bytes);
+  m.max_pages = max_pages;
+  m.max_q = max_q < N ? max_q : N;
+  m.page_table = page_table;
+  const int group = q_heads / cache->kv_heads;
+  int few = kFewRows / group;
+  few = few < m.max_q ? few : m.max_q;
+  if (B == 0 || N == 0) few = 0;
+  m.few = few;
+  p->has_many = m.max_q > few || few == 0;
+  size_t few_bytes = 0, many_bytes = 0;
+  if (p->has_many)
+    rc = tile_plan(B, N, q_heads, cache->kv_heads, cache->head_dim, window, sinks, true, &m,
+                   &many_bytes);
+  if (!rc && few > 0) {
+    rc = attention_plan(cache, B, few, q_heads, max_pages, page_table, window, sinks, &p->few,
+                        &few_bytes);
+    p->few.N = N;
+    p->few.max_q = m.max_q;
+    p->few.zero = !p->has_many;
+  }
+  // one after the other on one stream: they share the workspace
+  *bytes = few_bytes > many_bytes ? few_bytes : many_bytes;
+  return rc;
 }
 
 int prompt_plan(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
@@ -192,27 +222,31 @@ int prompt_plan(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads, int32_t
   return tile_plan(B, N, q_heads, kv_heads, head_dim, window, sinks, false, a, bytes);
 }
 
-// What both attentions of packed rows check beyond the plan, and their common fields.
-int tile_args(const int32_t* offsets, const void* q, const int64_t* q_strides, void* out,
-              int32_t type, float scale, int32_t dim, size_t bytes, void* workspace,
-              size_t workspace_bytes, TileAttentionArgs* a) {
+// What both attentions of packed rows check beyond the plan.
+int check_rows(int32_t N, const int32_t* offsets, const void* q, const void* out, int32_t type,
+               float scale, size_t bytes, const void* workspace, size_t workspace_bytes) {
   int rc = check_type(type, false);
   if (rc) return rc;
   if (!(scale >= 1.f / kMaxScale && scale <= kMaxScale))
     return fail(SFX_EINVAL, "scale=%g outside [2^-64, 2^64]", (double)scale);
-  if (a->N == 0) return SFX_OK;
+  if (N == 0) return SFX_OK;
   if (!offsets || !q || !out) return fail(SFX_EINVAL, "NULL array argument");
   if ((uintptr_t)out & 15) return fail(SFX_EINVAL, "out must be aligned to 16 bytes");
   if (bytes > 0 && (!workspace || workspace_bytes < bytes || ((uintptr_t)workspace & 15)))
     return fail(SFX_EINVAL, "workspace of %zu bytes (16-byte aligned) needed, %zu given", bytes,
                 workspace ? workspace_bytes : (size_t)0);
+  return SFX_OK;
+}
+
+// The fields that both kernels' arguments have.
+template <typename Args>
+void fill_rows(Args* a, const int32_t* offsets, const void* q, KvStrides qs, void* out,
+               float scale) {
   a->offsets = offsets;
   a->q = q;
-  a->qs = packed_strides(q_strides, (int64_t)a->heads * a->group, dim);
+  a->qs = qs;
   a->out = out;
   a->scale_log2 = scale * 1.4426950408889634f;
-  if (bytes > 0) tile_attention_place(a, dim, workspace);
-  return SFX_OK;
 }
 
 int check_pages(int32_t B, int32_t max_pages, int32_t page_size, int32_t num_pages) {
@@ -401,9 +435,9 @@ int sfx_kv_attention_packed_workspace_bytes(const sfx_kv_cache* cache, int32_t B
                                             int32_t max_q, int32_t q_heads, int32_t max_pages,
                                             int32_t window, int32_t sinks, size_t* bytes) {
   if (!bytes) return fail(SFX_EINVAL, "bytes is NULL");
-  TileAttentionArgs a{};
+  PackedArgs p{};
   static const int32_t none = 0;  // the plan does not look at the table
-  return packed_plan(cache, B, N, max_q, q_heads, max_pages, &none, window, sinks, &a, bytes);
+  return packed_plan(cache, B, N, max_q, q_heads, max_pages, &none, window, sinks, &p, bytes);
 }
 
 int sfx_kv_attention_packed(const sfx_kv_cache* cache, int32_t B, int32_t N, int32_t max_q,
@@ -412,18 +446,30 @@ int sfx_kv_attention_packed(const sfx_kv_cache* cache, int32_t B, int32_t N, int
                             const int64_t* q_strides, void* out, int32_t type, float scale,
                             int32_t window, int32_t sinks, void* workspace,
                             size_t workspace_bytes, void* stream) {
-  TileAttentionArgs a{};
+  PackedArgs p{};
   size_t bytes = 0;
-  int rc = packed_plan(cache, B, N, max_q, q_heads, max_pages, page_table, window, sinks, &a,
+  int rc = packed_plan(cache, B, N, max_q, q_heads, max_pages, page_table, window, sinks, &p,
                        &bytes);
-  if (!rc)
-    rc = tile_args(offsets, q, q_strides, out, type, scale, cache->head_dim, bytes, workspace,
-                   workspace_bytes, &a);
+  if (!rc) rc = check_rows(N, offsets, q, out, type, scale, bytes, workspace, workspace_bytes);
   if (rc || N == 0) return rc;
   if (B > 0 && !seq_lens) return fail(SFX_EINVAL, "NULL array argument");
-  a.seq_lens = seq_lens;
-  HIP_OR_RETURN(launch_chunk_attention(a, cache->head_dim, kv_type(type), (hipStream_t)stream),
-                "packed attention launch");
+  const KvStrides qs = packed_strides(q_strides, q_heads, cache->head_dim);
+  if (p.has_many) {
+    TileAttentionArgs& a = p.many;
+    fill_rows(&a, offsets, q, qs, out, scale);
+    a.seq_lens = seq_lens;
+    if (a.splits > 1) tile_attention_place(&a, cache->head_dim, workspace);
+    HIP_OR_RETURN(launch_chunk_attention(a, cache->head_dim, kv_type(type), (hipStream_t)stream),
+                  "packed attention launch");
+  }
+  if (p.few.T > 0) {
+    KvAttentionArgs& a = p.few;
+    fill_rows(&a, offsets, q, qs, out, scale);
+    a.seq_lens = seq_lens;
+    if (a.splits > 1) kv_attention_place(&a, cache->head_dim, workspace);
+    HIP_OR_RETURN(launch_kv_attention(a, cache->head_dim, kv_type(type), (hipStream_t)stream),
+                  "packed attention launch");
+  }
   return SFX_OK;
 }
 
@@ -444,11 +490,11 @@ int sfx_prompt_attention(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads
   TileAttentionArgs a{};
   size_t bytes = 0;
   int rc = prompt_plan(B, N, q_heads, kv_heads, head_dim, window, sinks, &a, &bytes);
-  if (!rc)
-    rc = tile_args(offsets, q, q_strides, out, type, scale, head_dim, bytes, workspace,
-                   workspace_bytes, &a);
+  if (!rc) rc = check_rows(N, offsets, q, out, type, scale, bytes, workspace, workspace_bytes);
   if (rc || N == 0) return rc;
   if (!k || !v) return fail(SFX_EINVAL, "NULL array argument");
+  fill_rows(&a, offsets, q, packed_strides(q_strides, q_heads, head_dim), out, scale);
+  if (bytes > 0) tile_attention_place(&a, head_dim, workspace);
   a.k = k;
   a.v = v;
   a.ks = packed_strides(k_strides, kv_heads, head_dim);

@@ -21,6 +21,7 @@ struct TileAttentionArgs {
   // chunks: the cache
   KvCache c;
   int32_t max_pages, max_q;    // rows of a request from max_q on are zero
+  int32_t few;                 // requests of 1 to `few` rows (tokens) are another call's
   const int32_t* page_table;
   const int32_t* seq_lens;
   // plan (tile_attention_plan)

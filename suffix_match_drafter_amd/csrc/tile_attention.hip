@@ -186,7 +186,12 @@ __device__ __forceinline__ RowTile row_tile(const TileAttentionArgs& a, int vt) 
     const int len = __builtin_amdgcn_readfirstlane(a.seq_lens[b]);
     t.len = len < 0 ? 0 : (len > cap ? cap : len);
     t.pos0 = t.len - toks;
-    t.live = (toks < a.max_q ? toks : a.max_q) * a.group;
+    const int attend = toks < a.max_q ? toks : a.max_q;
+    t.live = attend * a.group;
+    if (a.few > 0 && attend <= a.few) {
+      t.r0 = t.rows;
+      return t;
+    }
   }
   const int r1 = t.r0 + kRows < t.live ? t.r0 + kRows : t.live;
   if (t.r0 >= r1) return t;
@@ -736,7 +741,8 @@ size_t tile_attention_plan(TileAttentionArgs* a, int dim, bool paged) {
   }
   // As many splits as find a place on the card at once, of at least kMinTiles tiles.
   int64_t row_tiles = (int64_t)a->N * a->group / tile_rows(dim);
-  const int64_t least = a->B < a->N ? a->B : a->N;  // every request has one
+  // every request has one (where those of few rows are left out, most of the rows are of others)
+  const int64_t least = a->few > 0 ? 1 : (a->B < a->N ? a->B : a->N);
   row_tiles = row_tiles < least ? least : row_tiles;
   const int64_t pairs = row_tiles * a->heads;
   int64_t splits = pairs > 0 ? 256 / pairs : 1;
