@@ -188,7 +188,7 @@ int packed_plan(const sfx_kv_cache* cache, int32_t B, int32_t N, int32_t max_q, 
   if (!rc) rc = check_heads(q_heads, cache->kv_heads, window, sinks);
   if (rc) return rc;
   if (max_q < 0) return fail(SFX_EINVAL, "negative max_q=%d", max_q);
-  m.max_pages = max_pages;
+  m.max_pages = cache->num_pages > 0 ? max_pages : 0;  // no pages: no tokens
   m.max_q = max_q < N ? max_q : N;
   m.page_table = page_table;
   const int group = q_heads / cache->kv_heads;

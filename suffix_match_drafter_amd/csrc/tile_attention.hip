@@ -21,7 +21,7 @@
 //         one piece, as the cache has them (chunks, whose keys' rows are permuted to match).
 //
 // Softmax.  As in kv_attention.hip: one pass, running maximum m per row in base 2, P = 2^(s - m + 8),
-// m moves only once a score passes m + 7, scores past 2^16 rounded as m is.  P is rounded to the
+// m moves only once weights pass 2^15 in sum, scores past 2^16 are rounded as m is.  P is rounded to the
 // values' type (the matrix unit takes operands of one type): fp16 over the cache and for fp16 prompts,
 // where weights down to 2^-22 of the largest keep 11 bits; bf16, 8 bits, for bf16 prompts, whose
 // values' range fp16 does not hold.  Each weight's rounding is its own, so their error in a sum of
@@ -41,7 +41,7 @@ namespace sfx {
 namespace {
 
 constexpr float kPShift = 8.f;   // P = 2^(s - m + kPShift)
-constexpr float kPLimit = 15.f;  // m moves when some s - m + kPShift passes this
+constexpr float kSumLimit = 32768.f;  // m moves when a lane's weights of 32 tokens pass this in sum
 constexpr float kNoMax = -3e38f;  // below every score, finite
 constexpr float kLarge = 65536.f;  // |m| from which s and m are rounded alike before the difference
 constexpr int kRefLo = -5, kRefHi = 7;  // block exponent minus reference: code * 2^that is normal
@@ -124,12 +124,6 @@ constexpr int tile_tokens(int D) { return D > 128 ? 32 : 64; }
 // Wavefronts of a workgroup.
 constexpr int tile_waves(int D) { return D > 128 ? 4 : 8; }
 constexpr int tile_rows(int D) { return 32 * tile_waves(D); }
-
-// 16-byte pieces of a token's row in LDS lie at piece ^ swizzle(token): the reads of a wavefront, 16
-// tokens at one piece (keys) or 4 tokens by 64 bytes (values, turned), then touch every bank alike.
-template <int D> __device__ __forceinline__ int swizzle(int token) {
-  return D > 64 ? (token & 3) << 2 | (token >> 2 & 3) : (token >> 1 & 1) << 2 | (token >> 2 & 3);
-}
 
 // Segment s of the packed rows: 0 before the first request, 1 .. B the requests, B + 1 behind the
 // last.  `edge(s)` is its first token; any memory gives edges within [0, N].
@@ -226,20 +220,12 @@ __device__ __forceinline__ int64_t out_row(const TileAttentionArgs& a, const Row
   return ((int64_t)t.start + r / a.group) * a.heads * a.group + h * a.group + r % a.group;
 }
 
-// A block of 32 cached tokens: where it is and its exponents.
-struct Block {
-  int64_t ph;
-  int sub;
-  bool mapped;
-};
-__device__ __forceinline__ int page_id(const TileAttentionArgs& a, const int32_t* table, int block) {
-  const int pi = kv_page_of(a.c, block);
-  return __builtin_amdgcn_readfirstlane(pi < a.max_pages ? table[pi] : -1);
-}
-__device__ __forceinline__ Block block_at(const TileAttentionArgs& a, int h, int block, int page) {
-  const bool mapped = page >= 0 && page < a.c.num_pages;
-  return Block{(int64_t)(mapped ? page : 0) * a.c.heads + h,
-               block - kv_page_of(a.c, block) * (a.c.page_size / kKvBlock), mapped};
+// Page id of a block of 32 cached tokens; -1 where it is unmapped or past the table.  (Calls without any
+// pages have no tokens.)  Unmapped blocks are read as page 0's and not seen.
+__device__ __forceinline__ int page_of(const TileAttentionArgs& a, const int32_t* table, int block) {
+  const int pi = kv_page_of(a.c, block), last = a.max_pages - 1;
+  const int id = table[pi < last ? pi : last];
+  return pi > last || (unsigned)id >= (unsigned)a.c.num_pages ? -1 : id;
 }
 
 // One (tile of rows, head, split).
@@ -249,13 +235,20 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
   using P = std::conditional_t<kPaged, Fp16, T>;  // type of probabilities and values
   constexpr int kThreads = 64 * tile_waves(D);
   constexpr int kTok = tile_tokens(D), kHalves = kTok / 32;
-  constexpr int kRowBytes = 2 * D, kTileBytes = kTok * kRowBytes;
   constexpr int kPieces = kTok * D / 8;  // 16-byte pieces of a tile in LDS
   constexpr int kLoads = kPaged ? (kPieces / 2 + kThreads - 1) / kThreads : kPieces / kThreads;
   constexpr int kDimTiles = D / 32, kSteps = D / 16;
   // of two 16-bit values: their exponents, and what carries exponents of all ones into the signs
   constexpr unsigned kExps = P::kExp * 0x10001u, kCarry = (0x8000u - P::kExp) * 0x10001u;
-  __shared__ __attribute__((aligned(1024))) char lds[2][2][kTileBytes];  // [buffer][k, v]
+  // LDS: keys by token, values by token (prompts) or by block and dim, four groups of eight tokens
+  // each (chunks).  The rows' padding spreads what a wavefront reads at once over all banks: 16 rows
+  // at one 16-byte piece, or 4 tokens by 64 bytes.
+  constexpr int kKeyRow = 2 * D + 16, kKeyHalf = 32 * kKeyRow;
+  constexpr int kValueRow = kPaged ? 80 : 2 * D + 64;
+  constexpr int kValueHalf = (kPaged ? D : 32) * kValueRow;
+  constexpr int kValueSlots = kHalves > 1 ? 2 : 3;
+  __shared__ __attribute__((aligned(16))) char lds_k[2][kHalves * kKeyHalf];
+  __shared__ __attribute__((aligned(16))) char lds_v[kValueSlots][kHalves * kValueHalf];
   __shared__ int special;
 
   // Workgroups that follow each other go to different XCDs; a head's stay on the same ones.
@@ -299,95 +292,114 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[c][e] = 0.f;
   float mx = kNoMax, l = 0.f;
-  bool large = false;
+  bool large = false;        // scores are rounded as the maximum is
+  float limit = kSumLimit;  // of a lane's weights of 32 tokens; with large scores any is too much
 
-  // ---- tokens on their way: a tile's pieces in registers
+  // ---- tokens on their way: a tile's pieces in registers.  Keys are a tile ahead of the values.
   u32x4 kr[kLoads], vr[kLoads];
   const int32_t* table = kPaged ? a.page_table + (int64_t)(t.seg - 1) * a.max_pages : nullptr;
   auto first_block = [&](int i) {  // 32-token block of list entry i
-    return (i < t.nsink ? i : t.first + i - t.nsink) * kHalves;
+    return __builtin_amdgcn_readfirstlane((i < t.nsink ? i : t.first + i - t.nsink) * kHalves);
   };
-  // of the tile in registers: exponents, references of the values' units, and what is mapped
-  int ek[kHalves], vref[kHalves], ref = 0;
+  // Of cached tokens: what is known of 64 blocks, one a lane, in the order of the list, and of the 64
+  // after them.  Pages are asked for a batch ahead and scales half a batch, so that a tile takes what
+  // it needs from the lanes and waits for nothing.
+  int pages = -1, packed = 0;    // packed: exponents + 64 of keys and values, place in the page
+  int pages_next = -1, sub_next = 0;
+  float ks_next = 1.f, vs_next = 1.f;
+  const int per_page = a.c.page_size / kKvBlock;
+  auto ask_pages = [&](int q) {  // q: list position of the batch's first block, from i0 on
+    int i = i0 + (q + lane) / kHalves;
+    i = i < i1 ? i : i1 - 1;
+    const int block = (i < t.nsink ? i : t.first + i - t.nsink) * kHalves + (q + lane) % kHalves;
+    pages_next = page_of(a, table, block);
+    sub_next = block - kv_page_of(a.c, block) * per_page;
+  };
+  auto ask_scales = [&]() {
+    const int64_t at = ((int64_t)(pages_next < 0 ? 0 : pages_next) * a.c.heads + h) * per_page + sub_next;
+    ks_next = a.c.k_scale[at];
+    vs_next = a.c.v_scale[at];
+  };
+  auto take_batch = [&]() {
+    pages = pages_next;
+    packed = (kv_exp_of(ks_next) + 64) | (kv_exp_of(vs_next) + 64) << 8 | sub_next << 16;
+  };
+  // Of a tile, as its keys are loaded: its blocks' pages and the rest.
+  struct Info {
+    int page[kHalves], packed[kHalves];
+    int vref[kHalves];  // the unit in which the values lie in LDS
+  };
+  Info now{}, next{}, before{};  // of the tile whose weights are made, the one behind it, the last
+  int ref = 0;                   // the values' reference exponent, in the order of their tiles
   float vscale[kHalves];
-  bool mapped[kHalves], any_ref = false;
-  int pages[kHalves];  // ids of the tile after it
+  bool any_ref = false;
+  // a thread's pieces of a tile of 16-bit tokens
+  const bool far = a.ks.token >= 1 << 23 || a.vs.token >= 1 << 23;  // past 32-bit offsets
+  auto load_rows = [&](u32x4(&r)[kLoads], const void* from, const KvStrides& s, int i) {
+    const int j0 = first_block(i) * 32, last = t.len - 1 - j0;
+    const char* p = (const char*)from + (((int64_t)t.start + j0) * s.token + h * s.head) * 2;
 #pragma unroll
-  for (int x = 0; x < kHalves; ++x) {
-    ek[x] = vref[x] = 0;
-    pages[x] = -1;
-    vscale[x] = 1.f;
-    mapped[x] = true;
-  }
-  auto fetch_pages = [&](int i) {
-    if constexpr (kPaged) {
-#pragma unroll
-      for (int x = 0; x < kHalves; ++x)
-        pages[x] = page_id(a, table, __builtin_amdgcn_readfirstlane(first_block(i) + x));
+    for (int y = 0; y < kLoads; ++y) {
+      const int c = threadIdx.x + y * kThreads, off = c % (D / 8) * 16, tok = c / (D / 8);
+      const unsigned u = tok < last ? tok : last;  // those past the end are seen by no row
+      r[y] = far ? *(const u32x4_a2*)(p + u * s.token * 2 + off)
+                 : *(const u32x4_a2*)(p + (u * (unsigned)(s.token * 2) + off));
     }
   };
-  auto load = [&](int i) {
-    const int block0 = __builtin_amdgcn_readfirstlane(first_block(i));
+  // a thread's pieces of a tile of codes: 16 codes each, of block c / 2D
+  auto piece = [&](int y) {
+    const int c = threadIdx.x + y * kThreads;
+    return kPieces / 2 % kThreads ? c % (kPieces / 2) : c;  // too many threads load twice
+  };
+  const int64_t page_bytes = (int64_t)a.c.heads * a.c.page_size * D;
+  const int64_t head_bytes = (int64_t)h * a.c.page_size * D;
+  auto load_codes = [&](u32x4(&r)[kLoads], const uint8_t* codes, const Info& f, bool val) {
+#pragma unroll
+    for (int y = 0; y < kLoads; ++y) {
+      const int x = kHalves > 1 ? __builtin_amdgcn_readfirstlane(piece(y) / (2 * D)) : 0;
+      const int page = x ? f.page[kHalves - 1] : f.page[0];
+      const int sub = (x ? f.packed[kHalves - 1] : f.packed[0]) >> 16;
+      const uint8_t* p = codes + head_bytes + (page < 0 ? 0 : page) * page_bytes +
+                         sub * (kKvBlock * (val ? D : 64));
+      // keys: slab u / 128, token u / 4 of it, dims 16 (u % 4) and up
+      const unsigned u = piece(y) % (2 * D);
+      r[y] = *(const u32x4*)(p + (val ? u * 16 : (u >> 7) * (a.c.page_size * 64u) + (u & 127) * 16));
+    }
+  };
+  auto load_k = [&](Info& f, int i) {
     if constexpr (kPaged) {
-      Block bl[kHalves];
-      float ks[kHalves], vs[kHalves];
-#pragma unroll
-      for (int x = 0; x < kHalves; ++x) {
-        bl[x] = block_at(a, h, block0 + x, pages[x]);
-        mapped[x] = bl[x].mapped;
-        const int64_t at = bl[x].ph * (a.c.page_size / kKvBlock) + bl[x].sub;
-        ks[x] = mapped[x] ? a.c.k_scale[at] : 1.f;
-        vs[x] = mapped[x] ? a.c.v_scale[at] : 1.f;
-      }
-#pragma unroll
-      for (int y = 0; y < kLoads; ++y) {
-        const int c = threadIdx.x + y * kThreads;  // 16 codes: of block c / 2D
-        kr[y] = vr[y] = u32x4{0, 0, 0, 0};
-        if (c >= kPieces / 2) continue;
-        const int x = __builtin_amdgcn_readfirstlane(c / (2 * D));
-        const int u = c % (2 * D);
-        const Block& w = bl[kHalves > 1 && x ? kHalves - 1 : 0];
-        if (!w.mapped) continue;
-        const int64_t base = w.ph * a.c.page_size * D;
-        // keys: slab u / 128, token u / 4 of it, dims 16 (u % 4) and up
-        kr[y] = *(const u32x4*)(a.c.k + base + (int64_t)(u >> 7) * a.c.page_size * 64 +
-                                w.sub * (kKvBlock * 64) + (u & 127) * 16);
-        vr[y] = *(const u32x4*)(a.c.v + base + (int64_t)w.sub * kKvBlock * D + u * 16);
+      const int q = (i - i0) * kHalves;
+      if ((q & 63) == 0) {
+        take_batch();
+        ask_pages(q + 64);
+      } else if ((q & 63) == 32) {
+        ask_scales();
       }
 #pragma unroll
       for (int x = 0; x < kHalves; ++x) {
-        ek[x] = __builtin_amdgcn_readfirstlane(kv_exp_of(ks[x]));
-        const int ev = __builtin_amdgcn_readfirstlane(kv_exp_of(vs[x]));
-        if (!any_ref || ev - ref < kRefLo || ev - ref > kRefHi) ref = ev - 1;
-        any_ref = true;
-        vref[x] = ref;
-        vscale[x] = kv_pow2(ev - ref);
+        f.page[x] = __builtin_amdgcn_readlane(pages, (q & 63) + x);
+        f.packed[x] = __builtin_amdgcn_readlane(packed, (q & 63) + x);
       }
+      load_codes(kr, a.c.k, f, false);
     } else {
-#pragma unroll
-      for (int y = 0; y < kLoads; ++y) {
-        const int c = threadIdx.x + y * kThreads;
-        int tok = block0 * 32 + c / (D / 8);
-        tok = tok < t.len ? tok : t.len - 1;  // past the end: seen by no row
-        const int64_t at = (int64_t)t.start + tok;
-        const int off = c % (D / 8) * 16;
-        kr[y] = *(const u32x4_a2*)((const char*)a.k + (at * a.ks.token + h * a.ks.head) * 2 + off);
-        vr[y] = *(const u32x4_a2*)((const char*)a.v + (at * a.vs.token + h * a.vs.head) * 2 + off);
-      }
+      load_rows(kr, a.k, a.ks, i);
     }
   };
-  // Registers to LDS.  Of a tile that some row does not see in full the infinities and NaN among the
-  // values are left out (0 times one would be NaN in every row) and dealt with at the end.
-  auto store = [&](int buf, bool clean) {
-    char* kl = lds[buf][0];
-    char* vl = lds[buf][1];
+  auto load_v = [&](Info& f, int i) {
+    if constexpr (kPaged)
+      load_codes(vr, a.c.v, f, true);
+    else
+      load_rows(vr, a.v, a.vs, i);
+  };
+  // Registers to LDS.
+  auto store_k = [&](char* kl) {
 #pragma unroll
     for (int y = 0; y < kLoads; ++y) {
       const int c = threadIdx.x + y * kThreads;
       if constexpr (kPaged) {
-        if (c >= kPieces / 2) continue;
+        if (kPieces / 2 % kThreads && c >= kPieces / 2) continue;
         const int x = __builtin_amdgcn_readfirstlane(c / (2 * D)), u = c % (2 * D);
-        // keys: token 16 j + 8 s + 4 h + i goes to row 16 s + 8 j + 4 h + i
+        // token 16 j + 8 s + 4 h + i goes to row 16 s + 8 j + 4 h + i
         const int tok = (u & 127) >> 2, r = (tok & 7) | (tok & 8) << 1 | (tok & 16) >> 1;
         const int at = x * 32 + r, piece = (u >> 7) * 8 + (u & 3) * 2;
         u32x4 w[2];
@@ -398,8 +410,32 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          *(u32x4*)(kl + at * kRowBytes + ((piece + e) ^ swizzle<D>(at)) * 16) = w[e];
-        // values: [block][dim][4 groups of eight tokens]
+          *(u32x4*)(kl + at * kKeyRow + (piece + e) * 16) = w[e];
+      } else {
+        const int tok = c / (D / 8), piece = c % (D / 8);
+        *(u32x4*)(kl + tok * kKeyRow + piece * 16) = kr[y];
+      }
+    }
+  };
+  // Of a tile that some row does not see in full the infinities and NaN among the values are left
+  // out (0 times one would be NaN in every row) and dealt with at the end.
+  auto store_v = [&](char* vl, Info& f, bool clean) {
+    if constexpr (kPaged)
+#pragma unroll
+      for (int x = 0; x < kHalves; ++x) {
+        const int ev = (f.packed[x] >> 8 & 255) - 64;
+        if (!any_ref || ev - ref < kRefLo || ev - ref > kRefHi) ref = ev - 1;
+        any_ref = true;
+        f.vref[x] = ref;
+        vscale[x] = kv_pow2(ev - ref);
+      }
+#pragma unroll
+    for (int y = 0; y < kLoads; ++y) {
+      const int c = threadIdx.x + y * kThreads;
+      if constexpr (kPaged) {
+        if (kPieces / 2 % kThreads && c >= kPieces / 2) continue;
+        const int x = __builtin_amdgcn_readfirstlane(c / (2 * D)), u = c % (2 * D);
+        // [block][dim][4 groups of eight tokens]
         const int dim = (u >> 6) * 32 + (u >> 2 & 15) * 2, g = u & 3;
         const float sc = vscale[kHalves > 1 && x ? kHalves - 1 : 0];
         if (clean) {
@@ -412,6 +448,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
           }
           if (__any(bad != 0)) special = 1;
         }
+        u32x4 w[2];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           w[e >> 1][2 * (e & 1)] = Fp16::widen<false>(vr[y][e], sc);
@@ -419,10 +456,9 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
         }
 #pragma unroll
         for (int f = 0; f < 2; ++f)
-          *(u32x4*)(vl + ((x * D + dim + f) * 4 + (g ^ ((dim + f) >> 2 & 3))) * 16) = w[f];
+          *(u32x4*)(vl + (x * D + dim + f) * kValueRow + g * 16) = w[f];
       } else {
         const int tok = c / (D / 8), piece = c % (D / 8);
-        const int at = tok * kRowBytes + (piece ^ swizzle<D>(tok)) * 16;
         if (clean) {
           unsigned bad = 0;
 #pragma unroll
@@ -433,33 +469,29 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
           }
           if (__any(bad != 0)) special = 1;
         }
-        *(u32x4*)(kl + at) = kr[y];
-        *(u32x4*)(vl + at) = vr[y];
+        *(u32x4*)(vl + tok * kValueRow + piece * 16) = vr[y];
       }
     }
   };
 
-  // ---- LDS addresses of the operands
-  const int kat = n * kRowBytes + (hh ^ swizzle<D>(n)) * 16;  // piece 2 m + hh: xor 32 m
-  auto key = [&](const char* kl, int half, int m) {
-    return *(const u32x4*)(kl + half * 32 * kRowBytes + (kat ^ (32 * m)));
+  // ---- operands of 32 tokens from LDS
+  auto key = [&](const char* kl, int m) {
+    return *(const u32x4*)(kl + n * kKeyRow + hh * 16 + m * 32);
   };
-  // values of step s (16 slots) and dims 32 c: [lane's dim][its eight tokens]
-  auto value = [&](const char* vl, int s, int c) {
+  // number g: of step g / kDimTiles (16 slots) and dims 32 (g % kDimTiles): [lane's dim][its tokens]
+  auto value = [&](const char* vl, int g) {
+    const int s = g / kDimTiles, c = g % kDimTiles;
     if constexpr (kPaged) {
-      const int g = 2 * (s & 1) + hh;
-      return *(const u32x4*)(vl + (((s >> 1) * D + 32 * c + n) * 4 + (g ^ (n >> 2 & 3))) * 16);
+      return *(const u32x4*)(vl + n * kValueRow + hh * 16 + s * 32 + c * 32 * kValueRow);
     } else {
-      const int u = lane & 15;
+      const char* p = vl + (4 * hh + (lane >> 2 & 3)) * kValueRow + (lane >> 4 & 1) * 32 +
+                      (lane & 3) * 8 + s * 16 * kValueRow + c * 64;
       u32x4 r;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int tok = 16 * s + 8 * x + 4 * hh + (u >> 2);
-        const int piece = 4 * c + (lane >> 4 & 1) * 2 + (u >> 1 & 1);
-        const char* p = vl + tok * kRowBytes + (piece ^ swizzle<D>(tok)) * 16 + (u & 1) * 8;
         const u32x2 w = __builtin_bit_cast(
             u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                       (__attribute__((address_space(3))) i16x4*)(char*)p));
+                       (__attribute__((address_space(3))) i16x4*)(char*)(p + x * 8 * kValueRow)));
         r[2 * x] = w[0];
         r[2 * x + 1] = w[1];
       }
@@ -467,12 +499,12 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
     }
   };
   // token of score e of a half
-  auto token = [&](int half, int e) {
-    return kPaged ? 32 * half + 16 * (e >> 2 & 1) + 8 * (e >> 3) + 4 * hh + (e & 3)
-                  : 32 * half + 8 * (e >> 2) + 4 * hh + (e & 3);
+  auto token = [&](int e) {
+    return kPaged ? 16 * (e >> 2 & 1) + 8 * (e >> 3) + 4 * hh + (e & 3)
+                  : 8 * (e >> 2) + 4 * hh + (e & 3);
   };
 
-  auto sees = [&](int j) {
+  auto sees = [&](int j, int pos) {
     return j <= pos && (a.window == 0 || pos - j < a.window || j < a.sinks);
   };
   // every row of the workgroup sees the whole tile
@@ -484,115 +516,205 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
   if (threadIdx.x == 0) special = 0;
   __syncthreads();
   int unit = 0;  // the output sums' power of two
-  if (i0 < i1) {
-    fetch_pages(i0);
-    load(i0);
-    if (i0 + 1 < i1) fetch_pages(i0 + 1);
-  }
-  for (int i = i0; i < i1; ++i) {
-    const int buf = (i - i0) & 1;
-    const int j0 = first_block(i) * 32;
-    store(buf, !all_see(j0));
-    // what the tile in LDS is, before the registers go to the next
-    int ek_now[kHalves], vref_now[kHalves];
-    bool mapped_now[kHalves], all_mapped = true;
-#pragma unroll
-    for (int x = 0; x < kHalves; ++x) {
-      ek_now[x] = ek[x];
-      vref_now[x] = vref[x];
-      mapped_now[x] = mapped[x];
-      all_mapped &= mapped[x];
-    }
-    if (i + 1 < i1) {
-      load(i + 1);
-      if (i + 2 < i1) fetch_pages(i + 2);
-    }
-    __syncthreads();
-    const char* kl = lds[buf][0];
-    const char* vl = lds[buf][1];
-    // nothing for any of the wavefront's rows
-    if (j0 > hi_pos) continue;
-    if (a.window > 0 && j0 >= a.sinks && (int64_t)j0 + kTok - 1 <= (int64_t)lo_pos - a.window)
-      continue;
 
-    f32x16 sc[kHalves];
+  // ---- work on 32 tokens.  Operands are read kAhead steps before they are used.
+  constexpr int kAhead = 3;
+  u32x4 kf[kAhead + 1], vf[kAhead + 1];
+  struct Weights {
+    u32x4 w[2];
+  };
+  auto read_ahead = [&](const char* kl, const char* vl) {
 #pragma unroll
-    for (int x = 0; x < kHalves; ++x) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sc[x][e] = 0.f;
-#pragma unroll
-      for (int m = 0; m < kSteps; ++m) sc[x] = T::mfma(key(kl, x, m), q[m], sc[x]);
+    for (int g = 0; g < kAhead; ++g) {
+      kf[g] = key(kl, g);
+      vf[g] = value(vl, g);
     }
-
-    // masks: only where some row does not see the whole tile
-    const bool whole = all_mapped && j0 + kTok - 1 <= lo_pos &&
-                       (a.window == 0 || hi_pos - j0 < a.window || j0 + kTok <= a.sinks);
-    if (!whole) {
+  };
+  // In one go, so that the matrix unit waits for nothing: scores of the 32 tokens behind (keys kl),
+  // outputs of the 32 before (values vl, weights pb), and the weights pc of these, against the running
+  // maximum as it is.  No weight passes kSumLimit unless their sum does, so the sum tells whether the
+  // maximum has to move.  kl2, vl2: whose operands are read ahead at the end (NULL: none).
+  auto step = [&](const char* kl, const char* vl, const f32x16& s, f32x16& sn, const Weights& pb,
+                  Weights& pc, float cs, const char* kl2, const char* vl2) {
+    const float bias = kPShift - mx;
+    float add[2] = {0.f, 0.f};
 #pragma unroll
-      for (int x = 0; x < kHalves; ++x)
+    for (int e = 0; e < 16; ++e) sn[e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int j = j0 + token(x, e);
-          sc[x][e] = mapped_now[x] && sees(j) ? sc[x][e] : -__builtin_inff();
-        }
+    for (int g = 0; g < kSteps; ++g) {
+      constexpr int kRing = kAhead + 1;
+      const int ga = g + kAhead;
+      if (ga < kSteps) {
+        kf[ga % kRing] = key(kl, ga);
+        vf[ga % kRing] = value(vl, ga);
+      } else if (kl2) {
+        kf[ga % kRing] = key(kl2, ga - kSteps);
+        vf[ga % kRing] = value(vl2, ga - kSteps);
+      }
+      sn = T::mfma(kf[g % kRing], q[g], sn);
+      o[g % kDimTiles] = P::mfma(vf[g % kRing], pb.w[g / kDimTiles], o[g % kDimTiles]);
+#pragma unroll
+      for (int e = 16 * g / kSteps + (16 * g / kSteps & 1); e < 16 * (g + 1) / kSteps + (kSteps > 8 && !(g & 1)); e += 2) {
+        const float u = __builtin_amdgcn_exp2f(fmaf(s[e], cs, bias));
+        const float v = __builtin_amdgcn_exp2f(fmaf(s[e + 1], cs, bias));
+        add[0] += u;
+        add[1] += v;
+        unsigned w = P::pack(u, v);
+        // made here, not where it is needed
+        asm volatile("" : "+v"(w), "+v"(add[0]), "+v"(add[1]));
+        pc.w[e >> 3][(e & 7) >> 1] = w;
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-
-    // running maximum
-    float cs[kHalves], top = -__builtin_inff();
+    return add[0] + add[1];
+  };
+  // The same with the maximum brought up to date; scores that are large are rounded as it is.
+  auto weights_moved = [&](const f32x16& s, float cs, float& sum) {
+    float top = max3(s[0], s[1], s[2]);
 #pragma unroll
-    for (int x = 0; x < kHalves; ++x) {
-      cs[x] = kPaged ? a.scale_log2 * kv_pow2(ek_now[x]) : a.scale_log2;
-      float m = max3(sc[x][0], sc[x][1], sc[x][2]);
-#pragma unroll
-      for (int e = 3; e < 15; e += 2) m = max3(m, sc[x][e], sc[x][e + 1]);
-      m = product(max3(m, sc[x][15], sc[x][15]), cs[x]);
-      top = x == 0 ? m : __builtin_elementwise_maximum(top, m);
-    }
-    if (__any(top - mx > kPLimit - kPShift)) {
+    for (int e = 3; e < 15; e += 2) top = max3(top, s[e], s[e + 1]);
+    top = product(max3(top, s[15], s[15]), cs);
+    if (__any(top - mx > 0.f)) {
       const float m = fmaxf(mx, pair_max(top));
       large = __any(fabsf(m) > kLarge && m != kNoMax);
+      limit = large ? -1.f : kSumLimit;
       const float f = __builtin_amdgcn_exp2f(mx - m);
       mx = m;
       l *= f;
 #pragma unroll
       for (int c = 0; c < kDimTiles; ++c) o[c] *= f;
     }
-    u32x4 p[2 * kHalves];
+    Weights r;
+    sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < kHalves; ++x) {
-      if (large) {
+    for (int e = 0; e < 16; e += 2) {
+      float u[2];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sc[x][e] = product(sc[x][e], cs[x]) - mx + kPShift;
-      } else {
-        const float bias = kPShift - mx;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sc[x][e] = fmaf(sc[x][e], cs[x], bias);
+      for (int k = 0; k < 2; ++k) {
+        u[k] = large ? product(s[e + k], cs) - mx + kPShift : fmaf(s[e + k], cs, kPShift - mx);
+        u[k] = __builtin_amdgcn_exp2f(u[k]);
+        sum += u[k];
       }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        sc[x][e] = __builtin_amdgcn_exp2f(sc[x][e]);
-        l += sc[x][e];
-      }
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) p[2 * x + (e >> 3)][(e & 7) >> 1] = P::pack(sc[x][e], sc[x][e + 1]);
+      r.w[e >> 3][(e & 7) >> 1] = P::pack(u[0], u[1]);
     }
+    return r;
+  };
+  auto to_unit = [&](int to) {
+    if (kPaged && to != unit) {
+      const float f = kv_pow2(unit - to);
+      unit = to;
+#pragma unroll
+      for (int c = 0; c < kDimTiles; ++c) o[c] *= f;
+    }
+  };
 
-    // outputs
+  // ---- the loop
+  int ks = 0, vs = 0;  // tile i's slots
+  auto turn = [&](int s, int n) { return s + 1 == n ? 0 : s + 1; };
+  if (i0 < i1) {
+    if constexpr (kPaged) {
+      ask_pages(0);
+      ask_scales();
+    }
+    load_k(now, i0);
+    load_v(now, i0);
+    store_k(lds_k[0]);
+    if (i0 + 1 < i1) load_k(next, i0 + 1);
+    // what the first outputs are made of: nothing
+    for (int c = threadIdx.x; c < kValueHalf / 16; c += kThreads)
+      *(u32x4*)(lds_v[kValueSlots - 1] + (kHalves - 1) * kValueHalf + c * 16) = u32x4{0, 0, 0, 0};
+  }
+  // Tile i's values and tile i + 1's keys to LDS, those behind them on their way.  The slots are not
+  // read by wavefronts that are still in the last round: they are past its barrier.
+  auto bring = [&](int i, Info& after) {
+    bool clean = !all_see(first_block(i) * 32);
+    if constexpr (kPaged)
+#pragma unroll
+      for (int x = 0; x < kHalves; ++x) clean |= now.page[x] < 0;
+    store_v(lds_v[vs], now, clean);
+    if (i + 1 < i1) {
+      store_k(lds_k[ks ^ 1]);
+      load_v(next, i + 1);
+      if (i + 2 < i1) load_k(after, i + 2);
+    }
+  };
+  __syncthreads();
+  // the wavefront's own tiles end earlier than the workgroup's
+  int iw = i1;
+  while (iw > i0 && first_block(iw - 1) * 32 > hi_pos) --iw;
+  f32x16 sc[2];  // of this half and the next
+  Weights p[2];  // of the last half and this
+#pragma unroll
+  for (int e = 0; e < 16; ++e) sc[0][e] = 0.f;
+#pragma unroll
+  for (int m = 0; m < kSteps; ++m) sc[0] = T::mfma(key(lds_k[0], m), q[m], sc[0]);
+  p[1].w[0] = p[1].w[1] = u32x4{0, 0, 0, 0};
+  if constexpr (kHalves > 1)
+    read_ahead(lds_k[0] + kKeyHalf, lds_v[kValueSlots - 1] + kValueHalf);
+  for (int i = i0; i < iw; ++i) {
+    const int j0 = first_block(i) * 32;
+    const char *k_now = lds_k[ks], *k_next = lds_k[ks ^ 1], *v_now = lds_v[vs];
+    const char* v_last = lds_v[vs == 0 ? kValueSlots - 1 : vs - 1];
+    Info after{};
+    bring(i, after);
 #pragma unroll
     for (int x = 0; x < kHalves; ++x) {
-      if constexpr (kPaged) {
-        if (vref_now[x] != unit) {
-          const float f = kv_pow2(unit - vref_now[x]);
-          unit = vref_now[x];
-#pragma unroll
-          for (int c = 0; c < kDimTiles; ++c) o[c] *= f;
-        }
+      const int jx = j0 + 32 * x;
+      const float cs = kPaged ? a.scale_log2 * kv_pow2((now.packed[x] & 255) - 64) : a.scale_log2;
+      f32x16& s = sc[kHalves > 1 ? x : 0];
+      f32x16& sn = sc[kHalves > 1 ? 1 - x : 1];
+      Weights& pb = p[kHalves > 1 ? 1 - x : 1];
+      Weights& pc = p[kHalves > 1 ? x : 0];
+      if (x == kHalves - 1) {
+        __syncthreads();
+        read_ahead(k_next, kHalves > 1 ? v_now : v_last);
       }
+      to_unit(x > 0 ? now.vref[x > 0 ? x - 1 : 0] : before.vref[kHalves - 1]);
+      const bool mapped = !kPaged || now.page[x] >= 0;
+      const bool whole = mapped && jx + 31 <= lo_pos &&
+                         (a.window == 0 || hi_pos - jx < a.window || jx + 32 <= a.sinks);
+      if (!whole) {
+        int at = pos;
+        asm("" : "+v"(at));  // keeps what follows out of the other path's registers
 #pragma unroll
-      for (int s = 2 * x; s < 2 * x + 2; ++s)
-#pragma unroll
-        for (int c = 0; c < kDimTiles; ++c) o[c] = P::mfma(value(vl, s, c), p[s], o[c]);
+        for (int e = 0; e < 16; ++e)
+          s[e] = mapped && sees(jx + token(e), at) ? s[e] : -__builtin_inff();
+      }
+      float sum;
+      if constexpr (kHalves == 1)
+        sum = step(k_next, v_last, s, sn, pb, pc, cs, nullptr, nullptr);
+      else if (x == 0)
+        sum = step(k_now + kKeyHalf, v_last + kValueHalf, s, sn, pb, pc, cs, nullptr, nullptr);
+      else
+        sum = step(k_next, v_now, s, sn, pb, pc, cs, k_next + kKeyHalf, v_now + kValueHalf);
+      if (__any(sum > limit)) pc = weights_moved(s, cs, sum);
+      l += sum;
+      if constexpr (kHalves == 1) {
+        s = sn;
+        pb = pc;
+      }
     }
+    ks ^= 1;
+    vs = turn(vs, kValueSlots);
+    before = now;
+    now = next;
+    next = after;
+  }
+  if (i0 < iw) {  // the last outputs
+    to_unit(before.vref[kHalves - 1]);
+    const char* vl = lds_v[vs == 0 ? kValueSlots - 1 : vs - 1] + (kHalves - 1) * kValueHalf;
+#pragma unroll
+    for (int g = 0; g < kSteps; ++g)
+      o[g % kDimTiles] = P::mfma(value(vl, g), p[1].w[g / kDimTiles], o[g % kDimTiles]);
+  }
+  for (int i = iw; i < i1; ++i) {  // for the others
+    Info after{};
+    bring(i, after);
+    __syncthreads();
+    ks ^= 1;
+    vs = turn(vs, kValueSlots);
+    now = next;
+    next = after;
   }
 
   // Infinities and NaN that `store` took out: added to the rows that see their tokens.
@@ -604,13 +726,14 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
 #pragma unroll 1
       for (int u = 0; u < kTok; ++u) {
         const int j = j0 + u;
-        if (j >= t.len || !__any(sees(j))) continue;
-        const bool see = sees(j);
+        if (j >= t.len || !__any(sees(j, pos))) continue;
+        const bool see = sees(j, pos);
         if constexpr (kPaged) {
           const int block = __builtin_amdgcn_readfirstlane(j >> 5);
-          const Block w = block_at(a, h, block, page_id(a, table, block));
-          if (!w.mapped) continue;
-          const uint8_t* p = a.c.v + w.ph * a.c.page_size * D + (int64_t)w.sub * kKvBlock * D +
+          const int page = __builtin_amdgcn_readfirstlane(page_of(a, table, block));
+          if (page < 0) continue;
+          const int sub = block - kv_page_of(a.c, block) * per_page;
+          const uint8_t* p = a.c.v + head_bytes + page * page_bytes + sub * (kKvBlock * D) +
                              (u >> 2 & 3) * 16 + (u >> 4 & 1) * 4 + (u & 3);
 #pragma unroll
           for (int c = 0; c < kDimTiles; ++c)
@@ -657,7 +780,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
     }
     return;
   }
-  char* to = (char*)a.out + out_row(a, t, h, row) * kRowBytes;
+  char* to = (char*)a.out + out_row(a, t, h, row) * (2 * D);
 #pragma unroll
   for (int c = 0; c < kDimTiles; ++c)
 #pragma unroll
