@@ -334,7 +334,6 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
   float vscale[kHalves];
   bool any_ref = false;
   // a thread's pieces of a tile of 16-bit tokens
-  const bool far = a.ks.token >= 1 << 23 || a.vs.token >= 1 << 23;  // past 32-bit offsets
   auto load_rows = [&](u32x4(&r)[kLoads], const void* from, const KvStrides& s, int i) {
     const int j0 = first_block(i) * 32, last = t.len - 1 - j0;
     const char* p = (const char*)from + (((int64_t)t.start + j0) * s.token + h * s.head) * 2;
@@ -342,8 +341,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
     for (int y = 0; y < kLoads; ++y) {
       const int c = threadIdx.x + y * kThreads, off = c % (D / 8) * 16, tok = c / (D / 8);
       const unsigned u = tok < last ? tok : last;  // those past the end are seen by no row
-      r[y] = far ? *(const u32x4_a2*)(p + u * s.token * 2 + off)
-                 : *(const u32x4_a2*)(p + (u * (unsigned)(s.token * 2) + off));
+      r[y] = *(const u32x4_a2*)(p + u * (uint64_t)(s.token * 2) + off);
     }
   };
   // a thread's pieces of a tile of codes: 16 codes each, of block c / 2D
