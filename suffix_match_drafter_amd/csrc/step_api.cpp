@@ -417,7 +417,7 @@ int sfx_kv_write_slots(const sfx_kv_cache* cache, int32_t N, const int64_t* slot
   if (rc || N == 0) return rc;
   if (!slots || !k || !v) return fail(SFX_EINVAL, "NULL array argument");
   a.N = N;
-  a.window = kv_slot_window(N);
+  a.window = kv_slot_window(N, cache->kv_heads);
   if (kv_slot_threads(N, a.window, cache->kv_heads) > kMaxThreads)
     return fail(SFX_ECAPACITY, "N=%d is too large for one call", N);
   a.slots = slots;

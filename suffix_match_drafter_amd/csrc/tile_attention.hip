@@ -151,21 +151,24 @@ template <int D, bool kPaged>
 __device__ __forceinline__ RowTile row_tile(const TileAttentionArgs& a, int vt) {
   constexpr int kRows = tile_rows(D), kTok = tile_tokens(D);
   const int lane = threadIdx.x & 63;
-  // largest segment whose first number is not past vt: 64 probes at a time
-  int lo = 0, n = a.B + 2;
-  while (n > 1) {
+  // Largest segment whose first number is not past vt: 64 probes at a time, the last of neighbours,
+  // whose edges are the segment's own.
+  int lo = 0, n = a.B + 2, e = 0, hits;
+  for (;;) {
     const int step = (n + 63) >> 6, at = lo + lane * step;
-    const bool ok = lane * step < n &&
-                    (int64_t)edge(a, at) * a.group / kRows + at <= vt;
-    const int hits = 64 - __builtin_clzll(__ballot(ok) | 1);
+    e = edge(a, at);
+    const bool ok = lane * step < n && (int64_t)e * a.group / kRows + at <= vt;
+    hits = 64 - __builtin_clzll(__ballot(ok) | 1);
+    if (step == 1) break;
     lo += (hits - 1) * step;
     const int left = n - (hits - 1) * step;
     n = left < step ? left : step;
   }
   RowTile t{};
-  t.seg = __builtin_amdgcn_readfirstlane(lo);
-  t.start = __builtin_amdgcn_readfirstlane(edge(a, t.seg));
-  const int end = __builtin_amdgcn_readfirstlane(edge(a, t.seg + 1));
+  t.seg = __builtin_amdgcn_readfirstlane(lo + hits - 1);
+  t.start = __builtin_amdgcn_readlane(e, hits - 1);
+  const int end = hits < 64 ? __builtin_amdgcn_readlane(e, hits & 63)
+                            : __builtin_amdgcn_readfirstlane(edge(a, t.seg + 1));
   const int toks = end > t.start ? end - t.start : 0;
   t.rows = toks * a.group;
   const int count = (t.rows + kRows - 1) / kRows;
