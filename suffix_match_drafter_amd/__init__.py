@@ -967,16 +967,18 @@ class PagePool:
         N = int(rows)
         if N >> 31:
             _too_large(N)
-        shapes = ((B + 1,), (B,), (N,), (N,), (N,))
         if out is None:
-            if stream is None:
-                out = StepLayout(*[start.new_empty(s) for s in shapes[:4]],
-                                 start.new_empty(N, dtype=torch.int64))
-            else:
-                out = StepLayout(*[_empty(s, torch.int64 if k == 4 else torch.int32, self.device,
-                                          stream) for k, s in enumerate(shapes)])
-        to = [_array(t, name, s, torch.int64 if name == "slots" else torch.int32, i)
-              for t, name, s in zip(out, StepLayout._fields, shapes)]
+            # one allocation for all five, the 64-bit one first
+            sizes = (2 * N, B + 1, B, N, N)
+            new = start.new_empty(4 * N + 2 * B + 1) if stream is None else \
+                _empty((4 * N + 2 * B + 1,), torch.int32, self.device, stream)
+            slots, off, seq, req, pos = new.split(sizes)
+            out = StepLayout(off, seq, req, pos, slots.view(torch.int64))
+            p = new.data_ptr()
+            to = (p + 8 * N, p + 8 * N + 4 * B + 4, p + 8 * (N + B) + 4, p + 12 * N + 8 * B + 4, p)
+        else:
+            to = [_array(t, name, (n,), torch.int64 if name == "slots" else torch.int32, i)
+                  for t, name, n in zip(out, StepLayout._fields, (B + 1, B, N, N, N))]
         _check(load().sfx_step_layout(B, N, pages, self.page_size, self.num_pages, tab, st, ct,
                                       *to, _raw_stream(stream, i)))
         return out
