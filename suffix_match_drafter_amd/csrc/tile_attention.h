@@ -26,6 +26,7 @@ struct TileAttentionArgs {
   const int32_t* seq_lens;
   // plan (tile_attention_plan)
   int32_t splits;              // workgroups over the tokens of one tile of rows
+  int32_t least;               // token tiles that a split has at least
   float* part_o;               // [splits][N * heads * group][dim]  (splits > 1)
   float2* part_ml;             // [splits][N * heads * group]: maximum, sum
 };
