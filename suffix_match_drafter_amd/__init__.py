@@ -948,6 +948,8 @@ class PagePool:
             missing = torch.empty_like(held) if stream is None else \
                 _empty((B,), torch.int32, self.device, stream)
         to = _array(missing, "missing", (B,), torch.int32, i)
+        if B and (to == h or to == tk or h == tk):
+            raise ValueError("held, tokens and missing must be tensors of their own")
         L = load()
         ws, n = _workspace(self._bytes, (B, pages), L.sfx_pages_reserve_workspace_bytes,
                            self.device, stream)

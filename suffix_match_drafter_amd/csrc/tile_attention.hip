@@ -722,7 +722,12 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
   if (special) {
     for (int i = i0; i < i1; ++i) {
       const int j0 = first_block(i) * 32;
-      if (all_see(j0)) continue;
+      bool left_out = !all_see(j0);
+      if constexpr (kPaged)
+#pragma unroll
+        for (int x = 0; x < kHalves; ++x)
+          left_out |= __builtin_amdgcn_readfirstlane(page_of(a, table, j0 / 32 + x)) < 0;
+      if (!left_out) continue;
 #pragma unroll 1
       for (int u = 0; u < kTok; ++u) {
         const int j = j0 + u;

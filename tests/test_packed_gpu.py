@@ -322,6 +322,24 @@ def test_unmapped_pages_and_nan(S, rows):
     assert again[hit].isnan().all() and torch.equal(again[~hit], out[~hit])
 
 
+@pytest.mark.parametrize("rows", [1, 140])
+@pytest.mark.parametrize("nan_page,gone", [(4, 5), (5, 4)])
+def test_nan_beside_an_unmapped_page(S, rows, nan_page, gone):
+    """A NaN value that every row sees, next to a page that is not mapped and holds NaN as well: the
+    first reaches them all, the second nobody."""
+    rng = np.random.default_rng(rows)
+    plain, model = filled(S, rng, 20, 32, 1, 64)
+    table = np.arange(20)[None].copy()
+    table[0, gone] = -1
+    q = dev(rng.standard_normal((rows, 1, 64))).half()
+    args = (q, i32(table), i32([600]), i32([0, rows]))
+    want = plain.attend_packed(*args)
+    model.code["v"][[nan_page, gone], 0, 3, 7] = 127
+    out = upload(S, model).attend_packed(*args)
+    assert out[:, :, 7].isnan().all()
+    assert out[:, :, :7].equal(want[:, :, :7]) and out[:, :, 8:].equal(want[:, :, 8:])
+
+
 def test_as_the_padded_call(S):
     """Requests of one length: the padded attention's results, within both roundings."""
     import torch

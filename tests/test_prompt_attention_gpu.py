@@ -99,6 +99,18 @@ def test_against_model(S, case, dtype):
     compare(out, q, k, v, offsets, window, sinks)
 
 
+@pytest.mark.parametrize("B", [61, 62, 63, 64, 65, 300, 5000])
+def test_many_requests(S, B):
+    """Requests of no to a few rows, found by one, two or three rounds of probes."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 4, B)
+    lens[B // 2] = 150
+    offsets = np.concatenate([[0], np.cumsum(lens)]) + 5
+    q, k, v = make(rng, int(offsets[-1]) + 9, 1, 3, 64, "float16")
+    out = S.attend_prompt(q, k, v, i32(offsets))
+    compare(out, q, k, v, offsets)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_split_by_tokens(S, dim):
     """Few rows, many tokens: parts of one row tile joined (some tiles have one part only)."""
@@ -224,6 +236,13 @@ def test_strides(S):
                        for t in (want_q, want_k, want_v))):
         assert not args[0].is_contiguous()
         assert torch.equal(S.attend_prompt(*args, i32([0, 50, n])), want)
+    # rows 32 MB apart
+    far = torch.empty((2 ** 24 + 8) * (n - 1) + 8 * dim, dtype=torch.bfloat16, device="cuda")
+    parts = []
+    for t, at in ((want_q, 0), (want_k, 4 * dim), (want_v, 6 * dim)):
+        parts.append(far.as_strided(t.shape, (2 ** 24 + 8, dim, 1), at))
+        parts[-1].copy_(t)
+    assert torch.equal(S.attend_prompt(*parts, i32([0, 50, n])), want)
     one_k, one_v = want_k[:, :1].expand(n, 2, dim), want_v[:, :1].expand(n, 2, dim)
     shared = S.attend_prompt(want_q, one_k, one_v, i32([0, 50, n]))
     dense = S.attend_prompt(want_q, one_k.contiguous(), one_v.contiguous(), i32([0, 50, n]))
