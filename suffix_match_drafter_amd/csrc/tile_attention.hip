@@ -134,8 +134,9 @@ __device__ __forceinline__ int edge(const TileAttentionArgs& a, int s) {
   return o < 0 ? 0 : (o > a.N ? a.N : o);
 }
 
-// A tile of rows.  The tiles of segment s are numbers edge(s) * group / rows + s and up, which leaves
-// room for its last, partial one: a tile is found from its number without a list.
+// A tile of rows, found from its number without a list.  In calls of many requests the tiles of segment
+// s are numbers edge(s) * group / rows + s and up, which leaves room for its last, partial one; in
+// those of up to 62 they have no gaps.
 struct RowTile {
   int seg;                // 0 or B + 1: rows of no request, zeroed
   int start;              // first token of the segment
@@ -151,30 +152,57 @@ template <int D, bool kPaged>
 __device__ __forceinline__ RowTile row_tile(const TileAttentionArgs& a, int vt) {
   constexpr int kRows = tile_rows(D), kTok = tile_tokens(D);
   const int lane = threadIdx.x & 63;
-  // Largest segment whose first number is not past vt: 64 probes at a time, the last of neighbours,
-  // whose edges are the segment's own.
-  int lo = 0, n = a.B + 2, e = 0, hits;
-  for (;;) {
-    const int step = (n + 63) >> 6, at = lo + lane * step;
-    e = edge(a, at);
-    const bool ok = lane * step < n && (int64_t)e * a.group / kRows + at <= vt;
-    hits = 64 - __builtin_clzll(__ballot(ok) | 1);
-    if (step == 1) break;
-    lo += (hits - 1) * step;
-    const int left = n - (hits - 1) * step;
-    n = left < step ? left : step;
-  }
   RowTile t{};
-  t.seg = __builtin_amdgcn_readfirstlane(lo + hits - 1);
-  t.start = __builtin_amdgcn_readlane(e, hits - 1);
-  const int end = hits < 64 ? __builtin_amdgcn_readlane(e, hits & 63)
-                            : __builtin_amdgcn_readfirstlane(edge(a, t.seg + 1));
+  int end, nth;  // nth: which of the segment's tiles; the last rows see the most tokens and come first
+  if (a.B <= 62) {
+    // A lane a segment: the running sum of the tiles numbers them without gaps, the rows of no
+    // request last.  The workgroups that have work are then the first ones, and where they are just as
+    // many as the card has places each finds one (with gaps 16 requests of 512 rows over 8192 tokens,
+    // 256 workgroups, took 586 us: some had to wait for others).
+    const int seg = lane < a.B ? lane + 1 : (lane == a.B ? 0 : lane);
+    const int from = edge(a, seg), to = edge(a, seg + 1);
+    int toks = lane < a.B + 2 && to > from ? to - from : 0;
+    if constexpr (kPaged)
+      if (lane < a.B && a.few > 0 && (toks < a.max_q ? toks : a.max_q) <= a.few) toks = 0;
+    const int count = (int)(((int64_t)toks * a.group + kRows - 1) / kRows);
+    int sum = count;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(sum, o);
+      if (lane >= o) sum += x;
+    }
+    const uint64_t behind = __ballot(sum > vt);
+    if (behind == 0) return t;
+    const int at = __builtin_ctzll(behind);
+    t.seg = __builtin_amdgcn_readlane(seg, at);
+    t.start = __builtin_amdgcn_readlane(from, at);
+    end = __builtin_amdgcn_readlane(to, at);
+    nth = __builtin_amdgcn_readlane(sum, at) - 1 - vt;
+  } else {
+    // Largest segment whose first number (see RowTile) is not past vt: 64 probes at a time, the last
+    // of neighbours, whose edges are the segment's own.
+    int lo = 0, n = a.B + 2, e = 0, hits;
+    for (;;) {
+      const int step = (n + 63) >> 6, at = lo + lane * step;
+      e = edge(a, at);
+      const bool ok = lane * step < n && (int64_t)e * a.group / kRows + at <= vt;
+      hits = 64 - __builtin_clzll(__ballot(ok) | 1);
+      if (step == 1) break;
+      lo += (hits - 1) * step;
+      const int left = n - (hits - 1) * step;
+      n = left < step ? left : step;
+    }
+    t.seg = __builtin_amdgcn_readfirstlane(lo + hits - 1);
+    t.start = __builtin_amdgcn_readlane(e, hits - 1);
+    end = hits < 64 ? __builtin_amdgcn_readlane(e, hits & 63)
+                    : __builtin_amdgcn_readfirstlane(edge(a, t.seg + 1));
+    const int count =
+        end > t.start ? (int)(((int64_t)(end - t.start) * a.group + kRows - 1) / kRows) : 0;
+    nth = count - 1 - (vt - (int)((int64_t)t.start * a.group / kRows) - t.seg);
+  }
   const int toks = end > t.start ? end - t.start : 0;
   t.rows = toks * a.group;
-  const int count = (t.rows + kRows - 1) / kRows;
-  const int nth = vt - (int)((int64_t)t.start * a.group / kRows) - t.seg;
-  // the last rows see the most tokens and come first
-  t.r0 = nth < count ? (count - 1 - nth) * kRows : t.rows;
+  t.r0 = nth >= 0 ? nth * kRows : t.rows;
   if (t.seg == 0 || t.seg == a.B + 1) return t;
   t.live = t.rows;
   t.len = toks;
