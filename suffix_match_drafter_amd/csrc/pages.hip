@@ -10,8 +10,13 @@
 // page that moves is one item x < max(R, A) with one source and one destination, found by binary
 // search in the running sums; nothing depends on the order in which items run.
 //
+// Measured: 32 requests 4.1 us, bounded by dependent steps of one workgroup; 1024 requests of which a
+// quarter ends and another comes in (some 60000 pages move) 4.6 us for the sums and 5.3 for the
+// moves.
+//
 // Layout.  offsets = running sum of the counts.  Every workgroup makes the whole sum for itself (it
-// reads B counts from L2, which costs less than a launch) and looks its own rows up in it.
+// reads B counts from L2, which costs less than a launch) and looks its own rows up in it.  Measured:
+// 64 requests of 17 rows 3.4 us, 256 requests of 20000 rows 4.3 us.
 #include "pages.h"
 
 namespace sfx {
@@ -21,8 +26,10 @@ namespace {
 constexpr int kThreads = 1024, kWaveCount = kThreads / 64;
 // Requests whose running sums one workgroup keeps in LDS.
 constexpr int kLdsRequests = 4096;
-// Table entries up to which one workgroup moves all pages itself.
-constexpr int64_t kOneGroupEntries = 16384;
+// Table entries up to which one workgroup moves all pages itself.  With a quarter of the requests
+// ending and another coming in, a call of 33000 entries takes 8.4 us so and 12.3 in two launches, one
+// of 65000 14.7 and 12.1, one of 540000 81 and 12.2.
+constexpr int64_t kOneGroupEntries = 40960;
 
 // Inclusive running sum over the workgroup; `total` receives the whole.  Sums stay below 2^31.
 __device__ __forceinline__ int scan(int x, int* waves, int& total) {

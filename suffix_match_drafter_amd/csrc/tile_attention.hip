@@ -6,11 +6,18 @@
 //   out_t = sum_j softmax_j(scale q_t . k_j) v_j,    zero for a row that sees nothing.
 //
 // Decomposition.  The rows of a request and head of keys and values (tokens x query heads of its
-// group, the heads of a token next to each other) are cut into tiles of 32 rows a wavefront; a
-// workgroup takes one tile by all tokens that its rows see, or by one of `splits` equal parts of them
-// where there are few tiles.  Tokens come in tiles of 64 (32 at 256 dims), brought from memory through
-// registers into one of two LDS buffers while the other is worked on: one barrier a tile.  Codes of
-// the cache become 16-bit operands on that way, once for the whole workgroup.
+// group, the heads of a token next to each other) are cut into tiles of 32 rows a wavefront, 256 a
+// workgroup (128 at 256 dims); a workgroup takes one tile by all tokens that its rows see, or by one
+// of `splits` equal parts of them where there are few tiles.  Tokens come in tiles of 64 (32 at 256
+// dims), brought from memory through registers into one of two LDS buffers while the other is worked
+// on: one barrier a tile.  Codes of the cache become 16-bit operands on that way, once for the whole
+// workgroup, and their page ids and scales are fetched 64 blocks at a time, one a lane (with scalar
+// loads and branches for every tile a chunk of 2048 tokens over 32768 took 1280 us, so 1030).
+//
+// The loop works on three sets of 32 tokens at once: scores of the next, weights of these, outputs of
+// the last.  None waits for another, so the vector instructions of the weights run beside the
+// products (8 products of 32 cycles with 48 vector instructions between them take 338 cycles), and
+// operands are read from LDS three products ahead.
 //
 // Per 32 tokens, with the 32x32x16 matrix instructions (lane = 32 h + n):
 //   S^T = K Q^T: rows are tokens, columns query rows, so lane (n, h) gets the scores of query
@@ -29,6 +36,13 @@
 //
 // Infinities and NaN among the values reach only the rows that see their token: they are left out of
 // a tile that some row does not see in full, and added at the end to the rows that see them.
+//
+// Measured (8 heads of keys and values of 128, 4 query heads each, bf16): two prompts of 8192 tokens
+// 1045 us, 1050 TFLOP/s, where a library product of 8192^3 reaches 1345; a chunk of 2048 tokens over
+// 32768 cached ones 1025 to 1060 us, 945 to 975 TFLOP/s; 16 prompts of 128 to 2048 tokens 266 to 280
+// us.  Bound by the matrix unit (busy half of the cycles) and by power: the clock falls from 2.1 to
+// 1.9 GHz as the unit is kept busier.  Workgroups of four wavefronts, two a CU: 1178 us instead of
+// 1055 for the two prompts; a higher priority for half the wavefronts: no difference.
 #include "tile_attention.h"
 
 #include <hip/hip_bf16.h>
@@ -581,17 +595,21 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
       }
       sn = T::mfma(kf[g % kRing], q[g], sn);
       o[g % kDimTiles] = P::mfma(vf[g % kRing], pb.w[g / kDimTiles], o[g % kDimTiles]);
+      // two weights or more at a time: every second step's where there are more steps than pairs
+      constexpr int kPairs = kSteps < 8 ? kSteps : 8;
+      if (g % (kSteps / kPairs) == 0)
 #pragma unroll
-      for (int e = 16 * g / kSteps + (16 * g / kSteps & 1); e < 16 * (g + 1) / kSteps + (kSteps > 8 && !(g & 1)); e += 2) {
-        const float u = __builtin_amdgcn_exp2f(fmaf(s[e], cs, bias));
-        const float v = __builtin_amdgcn_exp2f(fmaf(s[e + 1], cs, bias));
-        add[0] += u;
-        add[1] += v;
-        unsigned w = P::pack(u, v);
-        // made here, not where it is needed
-        asm volatile("" : "+v"(w), "+v"(add[0]), "+v"(add[1]));
-        pc.w[e >> 3][(e & 7) >> 1] = w;
-      }
+        for (int e = 16 / kPairs * (g * kPairs / kSteps); e < 16 / kPairs * (g * kPairs / kSteps + 1);
+             e += 2) {
+          const float u = __builtin_amdgcn_exp2f(fmaf(s[e], cs, bias));
+          const float v = __builtin_amdgcn_exp2f(fmaf(s[e + 1], cs, bias));
+          add[0] += u;
+          add[1] += v;
+          unsigned w = P::pack(u, v);
+          // made here, not where it is needed
+          asm volatile("" : "+v"(w), "+v"(add[0]), "+v"(add[1]));
+          pc.w[e >> 3][(e & 7) >> 1] = w;
+        }
       __builtin_amdgcn_sched_barrier(0);
     }
     return add[0] + add[1];
