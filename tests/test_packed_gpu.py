@@ -267,6 +267,23 @@ def test_long_and_split(S, dim, rows):
             compare(out, model, q, table, lens, offsets, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("B", [62, 63, 200])
+def test_many_requests(S, B):
+    """Single tokens and drafts around two chunks, some requests without rows."""
+    rng = np.random.default_rng(B)
+    page, heads, group, dim = 32, 2, 2, 64
+    rows = rng.integers(0, 4, B)
+    rows[3], rows[B - 2] = 210, 150
+    lens = np.maximum(rows, rng.integers(1, 300, B))
+    width = 300 // page + 1
+    cache, model = filled(S, rng, B * width, page, heads, dim)
+    table = rng.permutation(B * width).reshape(B, width)
+    offsets = 2 + np.concatenate([[0], np.cumsum(rows)])
+    q = dev(rng.standard_normal((int(offsets[-1]) + 3, heads * group, dim))).half()
+    out = cache.attend_packed(q, i32(table), i32(lens), i32(offsets))
+    compare(out, model, q, table, lens.tolist(), offsets)
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 @pytest.mark.parametrize("rows", [1, 20, 200])
 def test_exponents_far_apart(S, rows, dtype):
