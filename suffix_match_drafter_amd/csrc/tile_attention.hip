@@ -38,9 +38,9 @@
 // a tile that some row does not see in full, and added at the end to the rows that see them.
 //
 // Measured (8 heads of keys and values of 128, 4 query heads each, bf16): two prompts of 8192 tokens
-// 1045 us, 1050 TFLOP/s, where a library product of 8192^3 reaches 1345; a chunk of 2048 tokens over
-// 32768 cached ones 1025 to 1060 us, 945 to 975 TFLOP/s; 16 prompts of 128 to 2048 tokens 266 to 280
-// us.  Bound by the matrix unit (busy half of the cycles) and by power: the clock falls from 2.1 to
+// 1045 to 1108 us by the card, 990 to 1050 TFLOP/s, where a library product of 8192^3 reaches 1345; a
+// chunk of 2048 tokens over 32768 cached ones 1025 to 1086 us, 920 to 975 TFLOP/s; 16 prompts of 128 to
+// 2048 tokens 266 to 286 us.  Bound by the matrix unit (busy half of the cycles) and by power: the clock falls from 2.1 to
 // 1.9 GHz as the unit is kept busier.  Workgroups of four wavefronts, two a CU: 1178 us instead of
 // 1055 for the two prompts; a higher priority for half the wavefronts: no difference.
 #include "tile_attention.h"
