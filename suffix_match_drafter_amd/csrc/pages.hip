@@ -266,7 +266,7 @@ __global__ __launch_bounds__(kThreads) void layout_kernel(LayoutArgs a) {
     }
     pos = start + (int)(row - from);
     const int pi = pos / a.page_size;
-    if (pi < a.max_pages) {
+    if (a.slots && pi < a.max_pages) {  // there may be no table for the others
       const int page = a.page_table[(int64_t)b * a.max_pages + pi];
       if (page >= 0 && page < a.num_pages) slot = (int64_t)page * a.page_size + pos % a.page_size;
     }
