@@ -549,7 +549,9 @@ int sfx_pages_reserve(int32_t B, int32_t max_pages, int32_t page_size, int32_t n
  *   request, position [N], slots [N]: of each row, page_table[b, position / page_size] * page_size
  *   + position % page_size; -1 for rows of no request, slots also where the page is outside
  *   [0, num_pages) or past max_pages.
- * The last four may be NULL; page_table is read for slots only. */
+ * The last four may be NULL; page_table is read for slots only.  No output may share memory with
+ * another array of the call: SFX_EINVAL (lengths are advanced from one call to the next in two sets of
+ * arrays, or by a copy of seq_lens to start). */
 int sfx_step_layout(int32_t B, int32_t N, int32_t max_pages, int32_t page_size, int32_t num_pages,
                     const int32_t* page_table, const int32_t* start, const int32_t* count,
                     int32_t* offsets, int32_t* seq_lens, int32_t* request, int32_t* position,

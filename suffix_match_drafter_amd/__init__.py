@@ -960,7 +960,9 @@ class PagePool:
 
     def layout(self, page_table, start, count, rows, out=None, stream=None):
         """sfx_step_layout: the layout of a packed batch of `rows` rows (those past the counts' sum
-        belong to no request) with count[b] new tokens from position start[b] on."""
+        belong to no request) with count[b] new tokens from position start[b] on.  Nothing of
+        ``out`` may share memory with the inputs (start is not the last layout's seq_lens if that
+        is where the new ones go)."""
         i = self._index
         _on(i)
         tab, B, pages = self._table(page_table)

@@ -5,6 +5,9 @@
 // They need no context.  Host code checks the arguments it can see, derives the launch plan from
 // the shapes alone (never from device memory) and enqueues kernels.
 #include "../../include/sfx.h"
+
+#include <initializer_list>
+
 #include "errors.h"
 #include "kv_attention.h"
 #include "kv_cache.h"
@@ -253,6 +256,27 @@ void fill_rows(Args* a, const int32_t* offsets, const void* q, KvStrides qs, voi
   a->scale_log2 = scale * 1.4426950408889634f;
 }
 
+// An array of a call, as long as the call may read or write it.
+struct Span {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+
+// The first `written` of the arrays are written: they share no memory with any other.  Workgroups
+// read the inputs at any time, also after others have stored their outputs.
+int check_apart(std::initializer_list<Span> arrays, int written) {
+  const Span* s = arrays.begin();
+  const int n = (int)arrays.size();
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      const uintptr_t a = (uintptr_t)s[i].p, b = (uintptr_t)s[j].p;
+      if (a && b && s[i].bytes && s[j].bytes && a < b + s[j].bytes && b < a + s[i].bytes)
+        return fail(SFX_EINVAL, "%s and %s share memory", s[i].name, s[j].name);
+    }
+  return SFX_OK;
+}
+
 int check_pages(int32_t B, int32_t max_pages, int32_t page_size, int32_t num_pages) {
   if (B < 0 || max_pages < 0 || num_pages < 0)
     return fail(SFX_EINVAL, "negative shape B=%d max_pages=%d num_pages=%d", B, max_pages,
@@ -406,6 +430,13 @@ int sfx_step_layout(int32_t B, int32_t N, int32_t max_pages, int32_t page_size, 
     return fail(SFX_EINVAL, "NULL array argument");
   if (layout_threads(N) > kMaxThreads)
     return fail(SFX_ECAPACITY, "N=%d is too large for one call", N);
+  const size_t b = (size_t)B * 4, n = (size_t)N;
+  rc = check_apart({{"offsets", offsets, b + 4}, {"seq_lens", seq_lens, b},
+                    {"request", request, n * 4}, {"position", position, n * 4},
+                    {"slots", slots, n * 8}, {"start", start, b}, {"count", count, b},
+                    {"page_table", slots ? page_table : nullptr, b * max_pages}},
+                   5);
+  if (rc) return rc;
   const LayoutArgs a{B,     N,       max_pages, page_size, num_pages, page_table, start,
                      count, offsets, seq_lens,  request,   position,  slots};
   HIP_OR_RETURN(launch_layout(a, (hipStream_t)stream), "step layout launch");

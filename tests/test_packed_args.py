@@ -1,0 +1,51 @@
+"""What the calls of packed batches refuse beyond single arguments: memory that is shared, sizes at the
+end of their range, a pool's buffers exchanged (CPU: addresses are compared, never read)."""
+import ctypes
+
+import pytest
+
+import suffix_match_drafter_amd as sfx
+
+
+def ptr(x):
+    return None if x is None else ctypes.c_void_p(x)
+
+
+def error():
+    return sfx.load().sfx_last_error().decode()
+
+
+# ------------------------------------------------------------------ the layout
+LAYOUT = dict(table=1 << 20, start=2 << 20, count=3 << 20, offsets=4 << 20, seq_lens=5 << 20,
+              request=6 << 20, position=7 << 20, slots=8 << 20)
+
+
+def layout(B=10, N=100, mp=3, **at):
+    a = dict(LAYOUT, **at)
+    return sfx.load().sfx_step_layout(B, N, mp, 64, 30, *(ptr(a[n]) for n in LAYOUT), None)
+
+
+@pytest.mark.parametrize("out", ["offsets", "seq_lens", "request", "position", "slots"])
+@pytest.mark.parametrize("other", ["table", "start", "count", "seq_lens", "request", "slots"])
+def test_layout_refuses_shared_memory(out, other):
+    """The same array twice, and two that meet in one element."""
+    if out == other:
+        return
+    size = dict(table=120, start=40, count=40, offsets=44, seq_lens=40, request=400, position=400,
+                slots=800)
+    for at in (LAYOUT[other], LAYOUT[other] + size[other] - 4, LAYOUT[other] - size[out] + 4):
+        assert layout(**{out: at}) == sfx.EINVAL, at
+        assert "share memory" in error()
+
+
+def test_layout_takes_neighbours():
+    """Arrays right behind each other, and no table beside a call without slots, are not refused for
+    it: such a call ends at the launch, of which the CPU knows nothing."""
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("the call would run")
+    at = LAYOUT["start"]
+    for kw in (dict(seq_lens=at + 40), dict(seq_lens=at - 40), dict(slots=at + 40),
+               dict(slots=None, request=LAYOUT["table"])):
+        assert layout(**kw) not in (sfx.OK, sfx.EINVAL, sfx.ECAPACITY), kw
