@@ -927,6 +927,20 @@ class PagePool:
         self._index = self.free.get_device()
         self._bytes = {}  # workspace sizes of reserve's shapes
 
+    # what reserve and layout hand to the library unchecked
+    _FIXED = ("free", "num_free", "num_pages", "page_size", "device", "_index", "_bytes")
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and name in self.__dict__:
+            raise AttributeError(f"{name} stays as it was made; write into the tensor, or make "
+                                 "another PagePool")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        if name in self._FIXED:
+            raise AttributeError(f"{name} stays as it was made")
+        super().__delattr__(name)
+
     def _table(self, page_table):
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
             raise ValueError("page_table must be [B, pages]")

@@ -49,3 +49,20 @@ def test_layout_takes_neighbours():
     for kw in (dict(seq_lens=at + 40), dict(seq_lens=at - 40), dict(slots=at + 40),
                dict(slots=None, request=LAYOUT["table"])):
         assert layout(**kw) not in (sfx.OK, sfx.EINVAL, sfx.ECAPACITY), kw
+
+
+# ------------------------------------------------------------------ the pool
+@pytest.mark.parametrize("name", ["free", "num_free", "num_pages", "page_size", "device", "_index",
+                                  "_bytes"])
+def test_a_pool_keeps_its_buffers(name):
+    """reserve hands their addresses and sizes on unchecked: another list would be written past its
+    end, or misread."""
+    pool = sfx.PagePool(8, 64, device="cpu")
+    was = getattr(pool, name)
+    with pytest.raises(AttributeError, match=name):
+        setattr(pool, name, was)
+    with pytest.raises(AttributeError, match=name):
+        delattr(pool, name)
+    assert getattr(pool, name) is was
+    pool.note = "other attributes are the caller's"
+    pool.note = "and can change"
