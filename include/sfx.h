@@ -535,7 +535,8 @@ int sfx_verify(int32_t B, int32_t k, int32_t V, const void* logits, int64_t batc
  * held, num_free ([1], clamped to [0, num_pages]) and page_table are updated; entries of free_pages from
  * num_free on mean nothing.  Ids are moved as they are.  A new pool has free_pages = 0, 1, ... and
  * num_free = num_pages; a finished request has tokens 0.
- * workspace: sfx_pages_reserve_workspace_bytes (may be 0), aligned to 16 bytes. */
+ * workspace: sfx_pages_reserve_workspace_bytes (may be 0), aligned to 16 bytes.
+ * No two arrays of the call may share memory (SFX_EINVAL); only missing may be tokens itself. */
 int sfx_pages_reserve_workspace_bytes(int32_t B, int32_t max_pages, size_t* bytes);
 int sfx_pages_reserve(int32_t B, int32_t max_pages, int32_t page_size, int32_t num_pages,
                       const int32_t* tokens, int32_t* page_table, int32_t* held,

@@ -413,6 +413,14 @@ int sfx_pages_reserve(int32_t B, int32_t max_pages, int32_t page_size, int32_t n
   if (bytes > 0 && (!workspace || workspace_bytes < bytes || ((uintptr_t)workspace & 15)))
     return fail(SFX_EINVAL, "workspace of %zu bytes (16-byte aligned) needed, %zu given", bytes,
                 workspace ? workspace_bytes : (size_t)0);
+  const size_t b = (size_t)B * 4;
+  // missing in the place of tokens is fine: the thread that writes one is the last to read the other
+  const int32_t* miss = missing == tokens ? nullptr : missing;
+  rc = check_apart({{"page_table", page_table, b * max_pages}, {"held", held, b},
+                    {"free_pages", free_pages, (size_t)num_pages * 4}, {"num_free", num_free, 4},
+                    {"missing", miss, b}, {"workspace", workspace, bytes}, {"tokens", tokens, b}},
+                   6);
+  if (rc) return rc;
   const ReserveArgs a{B,    max_pages,  page_size, num_pages, tokens, page_table,
                       held, free_pages, num_free,  missing,   (int32_t*)workspace};
   HIP_OR_RETURN(launch_reserve(a, (hipStream_t)stream), "pages reserve launch");

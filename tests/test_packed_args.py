@@ -66,3 +66,42 @@ def test_a_pool_keeps_its_buffers(name):
     assert getattr(pool, name) is was
     pool.note = "other attributes are the caller's"
     pool.note = "and can change"
+
+
+RESERVE = dict(tokens=1 << 20, table=2 << 20, held=3 << 20, free=4 << 20, num_free=5 << 20,
+               missing=6 << 20, ws=7 << 20)
+
+
+def reserve(B=10, mp=3, pages=30, nws=1 << 18, **at):
+    a = dict(RESERVE, **at)
+    return sfx.load().sfx_pages_reserve(B, mp, 64, pages, *(ptr(a[n]) for n in RESERVE), nws, None)
+
+
+@pytest.mark.parametrize("B,mp", [(10, 3), (5000, 3)])
+@pytest.mark.parametrize("one", ["table", "held", "free", "num_free", "missing", "ws"])
+@pytest.mark.parametrize("other", list(RESERVE))
+def test_reserve_refuses_shared_memory(one, other, B, mp):
+    """The same array twice, and two that meet in one element."""
+    size = dict(tokens=4 * B, table=4 * B * mp, held=4 * B, free=120, num_free=4, missing=4 * B,
+                ws=16 + 12 * B)
+    if one == other or ("ws" in (one, other) and B <= 4096):   # small calls use no workspace
+        return
+    at = [RESERVE[other], RESERVE[other] + size[other] - 4, RESERVE[other] - size[one] + 4]
+    if (one, other) == ("missing", "tokens"):
+        at = at[1:]   # the very same array is not refused: see below
+    for x in at:
+        if one == "ws" and x % 16:
+            continue
+        assert reserve(B, mp, **{one: x}) == sfx.EINVAL, x
+        assert "share memory" in error()
+
+
+def test_reserve_takes_neighbours():
+    """Arrays right behind each other, and missing in the place of tokens, end at the launch only."""
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("the call would run")
+    for kw in (dict(held=RESERVE["tokens"] + 40), dict(num_free=RESERVE["free"] + 120),
+               dict(missing=RESERVE["tokens"]), dict(missing=None), dict(ws=RESERVE["table"])):
+        assert reserve(**kw) not in (sfx.OK, sfx.EINVAL, sfx.ECAPACITY), kw

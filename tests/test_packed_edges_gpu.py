@@ -49,3 +49,45 @@ def test_layout_of_one_output(S, wanted):
     torch.cuda.synchronize()
     assert offsets.tolist() == want["offsets"].tolist()
     assert out.tolist() == want[wanted].tolist()
+
+
+# ------------------------------------------------------------------ the pages
+@pytest.mark.parametrize("B", [5, 5000])
+def test_missing_in_the_place_of_tokens(S, B):
+    """The C call may leave what is missing where the lengths stood."""
+    import torch
+
+    rng = np.random.default_rng(B)
+    page, width, pages = 16, 3, B
+    tokens = rng.integers(0, width * page + 20, B)
+    table, held = np.full((B, width), -1, np.int32), np.zeros(B, np.int32)
+    free = rng.permutation(pages).astype(np.int32)
+    want = M.reserve(table, held, free, pages, tokens, page, pages)
+    t, h, f, n, k = i32(table), i32(held), i32(free), i32([pages]), i32(tokens)
+    size = ctypes.c_size_t()
+    assert S.load().sfx_pages_reserve_workspace_bytes(B, width, ctypes.byref(size)) == S.OK
+    ws = torch.empty(max(size.value, 16), dtype=torch.uint8, device="cuda")
+    rc = S.load().sfx_pages_reserve(B, width, page, pages, k.data_ptr(), t.data_ptr(), h.data_ptr(),
+                                    f.data_ptr(), n.data_ptr(), k.data_ptr(), ws.data_ptr(),
+                                    size.value, None)
+    assert rc == S.OK
+    torch.cuda.synchronize()
+    assert np.array_equal(t.cpu().numpy(), want[0]) and h.tolist() == want[1].tolist()
+    assert int(n) == want[3] and f[:want[3]].tolist() == want[2][:want[3]].tolist()
+    assert k.tolist() == want[4].tolist()
+
+
+def test_held_and_tokens_of_one_array(S):
+    """Tensors that overlap without being the same are refused as well."""
+    x = i32(np.zeros(9))
+    table = i32(np.full((8, 2), -1))
+    pool = S.PagePool(4, 64)
+    for kw in (dict(held=x[:8], tokens=x[1:]), dict(held=x[:8], tokens=i32(np.ones(8)),
+                                                  missing=x[1:])):
+        with pytest.raises(S.SfxError, match="share memory"):
+            pool.reserve(table, **kw)
+    one = i32([0])
+    pool = S.PagePool(1, 64, buffers=(one, one))
+    with pytest.raises(S.SfxError, match="share memory"):
+        pool.reserve(i32([[-1]]), i32([0]), i32([1]))
+    assert one.tolist() == [0] and x.tolist() == [0] * 9
