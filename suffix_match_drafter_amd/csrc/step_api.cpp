@@ -282,6 +282,8 @@ int check_pages(int32_t B, int32_t max_pages, int32_t page_size, int32_t num_pag
     return fail(SFX_EINVAL, "negative shape B=%d max_pages=%d num_pages=%d", B, max_pages,
                 num_pages);
   if (page_size < 1) return fail(SFX_EINVAL, "page_size=%d is not positive", page_size);
+  // workgroups count requests in steps of 1024, in 32 bits
+  if (B > 0x7fffffff - 1023) return fail(SFX_ECAPACITY, "B=%d is too large for one call", B);
   return SFX_OK;
 }
 

@@ -105,3 +105,19 @@ def test_reserve_takes_neighbours():
     for kw in (dict(held=RESERVE["tokens"] + 40), dict(num_free=RESERVE["free"] + 120),
                dict(missing=RESERVE["tokens"]), dict(missing=None), dict(ws=RESERVE["table"])):
         assert reserve(**kw) not in (sfx.OK, sfx.EINVAL, sfx.ECAPACITY), kw
+
+
+# ------------------------------------------------------------------ sizes at the end of their range
+@pytest.mark.parametrize("B", [2 ** 31 - 1, 2 ** 31 - 1023])
+def test_as_many_requests_as_an_int_holds(B):
+    """Workgroups count requests in steps of 1024, which has to end below 2^31."""
+    far = {n: (i + 1) << 40 for i, n in enumerate(LAYOUT)}
+    assert layout(B=B, mp=1, **far) == sfx.ECAPACITY
+    assert "too large" in error()
+    far = {n: (i + 1) << 40 for i, n in enumerate(RESERVE)}
+    for mp in (0, 1):
+        assert reserve(B=B, mp=mp, nws=1 << 39, **far) == sfx.ECAPACITY
+        n = ctypes.c_size_t()
+        size = sfx.load().sfx_pages_reserve_workspace_bytes
+        assert size(B, mp, ctypes.byref(n)) == sfx.ECAPACITY
+        assert size(2 ** 31 - 1024, mp, ctypes.byref(n)) == sfx.OK and n.value > 3 * 4 * (2 ** 31 - 1024)
