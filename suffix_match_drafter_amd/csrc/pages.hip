@@ -101,8 +101,9 @@ __device__ __forceinline__ void move(const ReserveArgs& a, const Totals& t, cons
   if (x < t.granted) {
     const int b = find(want, a.B, x);
     a.page_table[(int64_t)b * a.max_pages + held[b] + x - (b ? want[b - 1] : 0)] = page;
-  } else if (t.num_free + x - t.granted < a.num_pages) {  // else: more pages than there are
-    a.free_pages[t.num_free + x - t.granted] = page;
+  } else {
+    const int64_t to = (int64_t)t.num_free + x - t.granted;
+    if (to < a.num_pages) a.free_pages[to] = page;  // else: more pages than there are
   }
 }
 
@@ -144,7 +145,10 @@ __device__ Totals plan(const ReserveArgs& a, int* back, int* want, int* held, in
     t.granted += total;
   }
   __syncthreads();  // every thread has read num_free
-  if (threadIdx.x == 0) *a.num_free = t.num_free + released - t.granted;
+  if (threadIdx.x == 0) {
+    const int64_t left = room - t.granted;
+    *a.num_free = left < a.num_pages ? (int)left : a.num_pages;
+  }
   __syncthreads();
   return t;
 }

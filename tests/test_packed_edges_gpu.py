@@ -91,3 +91,28 @@ def test_held_and_tokens_of_one_array(S):
     with pytest.raises(S.SfxError, match="share memory"):
         pool.reserve(i32([[-1]]), i32([0]), i32([1]))
     assert one.tolist() == [0] and x.tolist() == [0] * 9
+
+
+@pytest.mark.parametrize("B", [3, 50000])
+def test_more_pages_than_there_are(S, B):
+    """Counts that contradict each other (every page free, some held all the same): the list takes what
+    it has room for, and nothing passes its end, nor 2^31 where it is that long."""
+    import torch
+
+    tokens, held = i32(np.zeros(B)), i32(np.ones(B))
+    tokens[0] = 64 * 2
+    table = i32(np.arange(3 * B).reshape(B, 3))
+    for pages in (2 ** 31 - 1, 40):
+        whole = torch.empty(pages + 64, dtype=torch.int32, device="cuda")
+        whole[pages:] = 77
+        whole[:64] = 77
+        pool = S.PagePool(pages, 64, buffers=(whole[:pages], i32([2 ** 31 - 1])))
+        t, h = table.clone(), held.clone()
+        assert pool.reserve(t, h, tokens).tolist() == [0] * B
+        assert h.tolist() == [2] + [0] * (B - 1)
+        # the first request's second page is the first one released, the others have no room left
+        assert t[0].tolist() == [0, 3, 2] and t[1:, 0].eq(-1).all() and t[1:, 1:].equal(table[1:, 1:])
+        assert int(pool.num_free) == pages
+        assert whole[pages:].eq(77).all()
+        assert whole[:min(64, pages)].eq(77).all()
+        del pool, whole
