@@ -571,7 +571,8 @@ int sfx_kv_write_slots(const sfx_kv_cache* cache, int32_t N, const int64_t* slot
  * the n of request b stands at position seq_lens[b] - n + t.  Rows t >= max_q of a request and rows
  * of no request are zero: max_q is the most rows of a request that the call is planned for (at most
  * N; a call with few takes another path, so a tight one saves time).
- * out [N, q_heads, head_dim], dense.  Everything else is as for sfx_kv_attention. */
+ * out [N, q_heads, head_dim], dense; it may be q if q is dense, and shares no memory with it
+ * otherwise (SFX_EINVAL).  Everything else is as for sfx_kv_attention. */
 int sfx_kv_attention_packed_workspace_bytes(const sfx_kv_cache* cache, int32_t B, int32_t N,
                                             int32_t max_q, int32_t q_heads, int32_t max_pages,
                                             int32_t window, int32_t sinks, size_t* bytes);
@@ -587,7 +588,8 @@ int sfx_kv_attention_packed(const sfx_kv_cache* cache, int32_t B, int32_t N, int
  * arrays; NULL: dense), the dims of a head contiguous.  Row i of a request sees its rows j <= i; with
  * window > 0 those with j > i - window or, counted from the request's first row, j < sinks.
  *   out [N, q_heads, head_dim], dense, aligned to 16 bytes: softmax(scale * q k) v in fp32 sums;
- *   zero for rows of no request.  head_dim: 64, 128 or 256; scale in [2^-64, 2^64].
+ *   zero for rows of no request.  It may be q if q is dense, and shares no memory with q, k and v
+ *   otherwise (SFX_EINVAL).  head_dim: 64, 128 or 256; scale in [2^-64, 2^64].
  * Weights are rounded to `type` before they meet the values.
  * workspace: sfx_prompt_attention_workspace_bytes (may be 0), aligned to 16 bytes. */
 int sfx_prompt_attention_workspace_bytes(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads,

@@ -245,6 +245,43 @@ int check_rows(int32_t N, const int32_t* offsets, const void* q, const void* out
   return SFX_OK;
 }
 
+// Whether rows x heads of `dim` 16-bit values share memory with [lo, hi).
+bool rows_meet(const void* p, KvStrides s, int64_t rows, int64_t heads, int64_t dim, Wide lo,
+               Wide hi) {
+  Wide row = Wide(s.token) * 2, head = Wide(s.head) * 2, base = (uintptr_t)p, size = dim * 2;
+  if (s.head == dim) {  // a row's heads are one piece
+    size *= heads;
+    heads = 1;
+  }
+  if (row < 0) {
+    base += (rows - 1) * row;
+    row = -row;
+  }
+  if (head < 0) {
+    base += (heads - 1) * head;
+    head = -head;
+  }
+  if (lo >= base + (rows - 1) * row + (heads - 1) * head + size || hi <= base) return false;
+  for (int64_t h = 0; h < heads; ++h, base += head) {
+    // the first row that ends behind lo
+    const Wide past = lo - size - base, t = past < 0 || row == 0 ? 0 : past / row + 1;
+    if (t < rows && base + t * row < hi && base + t * row + size > lo) return true;
+  }
+  return false;
+}
+
+// out, dense, over the rows of an input: they are stored while other workgroups still read.  Only a
+// query's own place may take its result: its reader is the workgroup that stores it, or is done.
+int check_out(const void* out, int64_t N, int64_t q_heads, int64_t dim, const char* name,
+              const void* p, KvStrides s, int64_t heads, bool query) {
+  if (query && p == out && (s.head == dim || heads == 1) && (s.token == heads * dim || N == 1))
+    return SFX_OK;
+  const Wide lo = (uintptr_t)out;
+  if (rows_meet(p, s, N, heads, dim, lo, lo + Wide(N) * q_heads * dim * 2))
+    return fail(SFX_EINVAL, "out and %s share memory", name);
+  return SFX_OK;
+}
+
 // The fields that both kernels' arguments have.
 template <typename Args>
 void fill_rows(Args* a, const int32_t* offsets, const void* q, KvStrides qs, void* out,
@@ -499,6 +536,8 @@ int sfx_kv_attention_packed(const sfx_kv_cache* cache, int32_t B, int32_t N, int
   if (rc || N == 0) return rc;
   if (B > 0 && !seq_lens) return fail(SFX_EINVAL, "NULL array argument");
   const KvStrides qs = packed_strides(q_strides, q_heads, cache->head_dim);
+  rc = check_out(out, N, q_heads, cache->head_dim, "q", q, qs, q_heads, true);
+  if (rc) return rc;
   if (p.has_many) {
     TileAttentionArgs& a = p.many;
     fill_rows(&a, offsets, q, qs, out, scale);
@@ -544,6 +583,10 @@ int sfx_prompt_attention(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads
   a.v = v;
   a.ks = packed_strides(k_strides, kv_heads, head_dim);
   a.vs = packed_strides(v_strides, kv_heads, head_dim);
+  rc = check_out(out, N, q_heads, head_dim, "q", q, a.qs, q_heads, true);
+  if (!rc) rc = check_out(out, N, q_heads, head_dim, "k", k, a.ks, kv_heads, false);
+  if (!rc) rc = check_out(out, N, q_heads, head_dim, "v", v, a.vs, kv_heads, false);
+  if (rc) return rc;
   HIP_OR_RETURN(launch_prompt_attention(a, head_dim, kv_type(type), (hipStream_t)stream),
                 "prompt attention launch");
   return SFX_OK;

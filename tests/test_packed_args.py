@@ -121,3 +121,61 @@ def test_as_many_requests_as_an_int_holds(B):
         size = sfx.load().sfx_pages_reserve_workspace_bytes
         assert size(B, mp, ctypes.byref(n)) == sfx.ECAPACITY
         assert size(2 ** 31 - 1024, mp, ctypes.byref(n)) == sfx.OK and n.value > 3 * 4 * (2 ** 31 - 1024)
+
+
+# ------------------------------------------------------------------ attention
+I64x2 = ctypes.c_int64 * 2
+ROWS = dict(q=1 << 30, k=2 << 30, v=3 << 30, out=4 << 30)
+
+
+def prompt(N=50, H=4, Hk=2, D=64, qs=None, ks=None, vs=None, **at):
+    a = dict(ROWS, **at)
+    strides = [None if s is None else I64x2(*s) for s in (qs, ks, vs)]
+    return sfx.load().sfx_prompt_attention(2, N, H, Hk, D, ptr(5 << 30), ptr(a["q"]), strides[0],
+                                           ptr(a["k"]), strides[1], ptr(a["v"]), strides[2],
+                                           ptr(a["out"]), 0, 0.1, 0, 0, ptr(6 << 30), 1 << 30, None)
+
+
+def packed(N=50, H=4, max_q=50, qs=None, **at):
+    a = dict(ROWS, **at)
+    c = sfx._KvCache(4, 64, 2, 64, 10 << 30, 11 << 30, 12 << 30, 13 << 30)
+    return sfx.load().sfx_kv_attention_packed(
+        ctypes.byref(c), 2, N, max_q, H, 2, ptr(5 << 30), ptr(7 << 30), ptr(8 << 30), ptr(a["q"]),
+        None if qs is None else I64x2(*qs), ptr(a["out"]), 0, 0.1, 0, 0, ptr(6 << 30), 1 << 30, None)
+
+
+def test_attention_refuses_outputs_over_its_inputs():
+    """Rows are stored while other workgroups still read keys, values and (unless a row's result takes
+    its query's own place) queries."""
+    row = 4 * 64 * 2
+    for name, size in (("k", 50 * row // 2), ("v", 50 * row // 2)):
+        for at in (ROWS[name], ROWS[name] + size - 16, ROWS[name] - 50 * row + 16):
+            assert prompt(out=at) == sfx.EINVAL and f"out and {name} share" in error()
+    for call in (prompt, packed):
+        for at in (ROWS["q"] + 16, ROWS["q"] + row, ROWS["q"] - row, ROWS["q"] + 49 * row):
+            assert call(out=at) == sfx.EINVAL and "out and q share" in error(), at
+        # the first of two tokens' rows fits its place, the second does not; heads in another order
+        assert call(out=ROWS["q"], qs=(2 * 256, 64)) == sfx.EINVAL
+        assert call(out=ROWS["q"], qs=(64, 50 * 64)) == sfx.EINVAL
+        assert call(out=ROWS["q"], qs=(0, 64)) == sfx.EINVAL
+    # between the first token's keys and the second's is room for 2 rows of out and no more
+    gap = ROWS["k"] + row // 2
+    assert prompt(N=2, out=gap, ks=(128 + 512 - 8, 64)) == sfx.EINVAL
+
+
+def test_attention_takes_outputs_beside_its_inputs():
+    """Dense queries may be replaced by their results, and outputs may lie between the rows of the inputs
+    as long as they meet none of them: such calls end at the launch only."""
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("the call would run")
+    row = 4 * 64 * 2
+    ok = [prompt(out=ROWS["q"]), packed(out=ROWS["q"]), prompt(out=ROWS["q"], qs=(256, 64)),
+          packed(N=1, max_q=1, out=ROWS["q"], qs=(9999, 64)), prompt(out=ROWS["k"] + 50 * row // 2),
+          prompt(out=ROWS["v"] - 50 * row), packed(out=ROWS["q"] + 50 * row),
+          prompt(N=2, out=ROWS["k"] + row // 2, ks=(128 + 512, 64)),
+          prompt(N=2, out=ROWS["q"] + row, qs=(768, 64)),
+          # heads far apart, the outputs between them
+          prompt(out=ROWS["q"] + 50 * 128, qs=(64, 1 << 20))]
+    assert all(rc not in (sfx.OK, sfx.EINVAL, sfx.ECAPACITY) for rc in ok), ok

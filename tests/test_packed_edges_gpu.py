@@ -116,3 +116,56 @@ def test_more_pages_than_there_are(S, B):
         assert whole[pages:].eq(77).all()
         assert whole[:min(64, pages)].eq(77).all()
         del pool, whole
+
+
+# ------------------------------------------------------------------ attention
+def rand(seed, *shape, dtype="float16"):
+    import torch
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(getattr(torch, dtype))
+
+
+def cached(S, seed, pages, page, heads, dim, dtype="float16"):
+    """A cache with every page written, from tokens of one request."""
+    cache = S.KVCache(pages, page, heads, dim)
+    k, v = (rand(seed + i, 1, pages * page, heads, dim, dtype=dtype) for i in (0, 1))
+    cache.write(k, v, i32(np.arange(pages)[None]), i32([0]))
+    return cache
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_results_in_the_queries_place(S, dim):
+    """out = q: short requests, chunks, rows of no request, parts that are joined."""
+    import torch
+
+    for offsets, group in (([3, 4, 21, 321, 330], 4), ([0, 1, 2], 1), ([0, 30, 60, 90], 2),
+                           ([0, 700, 701], 1)):
+        N, B = offsets[-1] + 2, len(offsets) - 1
+        cache = cached(S, dim, 16 * B, 64, 1, dim)
+        table = i32(np.random.default_rng(dim).permutation(16 * B).reshape(B, 16))
+        lens, off = i32(np.maximum(np.diff(offsets), 1000 - 70 * np.arange(B))), i32(offsets)
+        q, k, v = rand(5, N, group, dim), rand(6, N, 1, dim), rand(7, N, 1, dim)
+        for max_q in (None, int(np.diff(offsets).max())):
+            want = cache.attend_packed(q, table, lens, off, max_q=max_q)
+            x = q.clone()
+            assert cache.attend_packed(x, table, lens, off, max_q=max_q, out=x) is x
+            assert torch.equal(x, want)
+        want = S.attend_prompt(q, k, v, off)
+        x = q.clone()
+        assert S.attend_prompt(x, k, v, off, out=x) is x
+        assert torch.equal(x, want)
+
+
+def test_results_over_keys_or_values(S):
+    """Refused: other workgroups still read them."""
+    q, k, v = (rand(i, 40, 2, 64) for i in range(3))
+    for bad in (k, v):
+        was = bad.clone()
+        with pytest.raises(S.SfxError, match="share memory"):
+            S.attend_prompt(q, k, v, i32([0, 40]), out=bad)
+        assert bad.equal(was)
+    wide = rand(9, 41, 2, 64)
+    with pytest.raises(S.SfxError, match="share memory"):
+        S.attend_prompt(wide[1:], k, v, i32([0, 40]), out=wide[:40])
