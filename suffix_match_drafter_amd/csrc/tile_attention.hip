@@ -27,12 +27,17 @@
 //         four tokens turned by the LDS transposed read (prompts), or eight tokens of a dim in
 //         one piece, as the cache has them (chunks, whose keys' rows are permuted to match).
 //
-// Softmax.  As in kv_attention.hip: one pass, running maximum m per row in base 2, P = 2^(s - m + 8),
-// m moves only once weights pass 2^15 in sum, scores past 2^16 are rounded as m is.  P is rounded to the
-// values' type (the matrix unit takes operands of one type): fp16 over the cache and for fp16 prompts,
-// where weights down to 2^-22 of the largest keep 11 bits; bf16, 8 bits, for bf16 prompts, whose
-// values' range fp16 does not hold.  Each weight's rounding is its own, so their error in a sum of
-// many tokens is below the result's own rounding.  Denominators add the unrounded weights in fp32.
+// Softmax.  As in kv_attention.hip: one pass, running maximum m per row in base 2,
+// P = 2^(s - m + shift), m moves only once a lane's 16 weights of 32 tokens pass 2^(shift + 7) in sum,
+// scores past 2^16 are rounded as m is.  P is rounded to the values' type (the matrix unit takes operands
+// of one type).  Over the cache and for fp16 prompts that is fp16 with a shift of 8, where weights down to
+// 2^-22 of the largest keep 11 bits and the sums of values below 2^16 stay far from fp32's end.  For bf16
+// prompts, whose values' range fp16 does not hold, it is bf16, 8 bits, with a shift that follows from
+// the number n of 32-token sets: -9 - log2(n), rounded up in log2(n), bounds a row's weights by
+// 2 n 2^(shift + 7) <= 1/2, so that no sum of finite values passes fp32's largest, which is bf16's too.
+// At the other end products with values below 2^-126 / 2^shift (2^-109 for 8192 tokens) are
+// subnormal.  Each weight's rounding is its own, so their error in a sum of many tokens is below the
+// result's own rounding.  Denominators add the unrounded weights in fp32.
 //
 // Infinities and NaN among the values reach only the rows that see their token: they are left out of
 // a tile that some row does not see in full, and added at the end to the rows that see them.
@@ -54,8 +59,9 @@ namespace sfx {
 
 namespace {
 
-constexpr float kPShift = 8.f;   // P = 2^(s - m + kPShift)
-constexpr float kSumLimit = 32768.f;  // m moves when a lane's weights of 32 tokens pass this in sum
+constexpr int kDrift = 7;  // P = 2^(s - m + shift); m moves when a lane's weights of 32 tokens pass
+                           // 2^(shift + kDrift) in sum
+constexpr int kFp16Shift = 8;
 constexpr float kNoMax = -3e38f;  // below every score, finite
 constexpr float kLarge = 65536.f;  // |m| from which s and m are rounded alike before the difference
 constexpr int kRefLo = -5, kRefHi = 7;  // block exponent minus reference: code * 2^that is normal
@@ -336,8 +342,14 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[c][e] = 0.f;
   float mx = kNoMax, l = 0.f;
-  bool large = false;        // scores are rounded as the maximum is
-  float limit = kSumLimit;  // of a lane's weights of 32 tokens; with large scores any is too much
+  bool large = false;      // scores are rounded as the maximum is
+  // weights' power of two, see the head: of bf16 such that all weights of a row stay below 1/2 in sum
+  const int sets = t.tiles * kHalves;
+  const int shift_log2 = std::is_same_v<P, Fp16>
+                             ? kFp16Shift
+                             : -(kDrift + 2 + (sets > 1 ? 32 - __builtin_clz(sets - 1) : 0));
+  const float shift = (float)shift_log2, sum_limit = kv_pow2(shift_log2 + kDrift);
+  float limit = sum_limit;  // of a lane's weights of 32 tokens; with large scores any is too much
 
   // ---- tokens on their way: a tile's pieces in registers.  Keys are a tile ahead of the values.
   u32x4 kr[kLoads], vr[kLoads];
@@ -574,11 +586,11 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
   };
   // In one go, so that the matrix unit waits for nothing: scores of the 32 tokens behind (keys kl),
   // outputs of the 32 before (values vl, weights pb), and the weights pc of these, against the running
-  // maximum as it is.  No weight passes kSumLimit unless their sum does, so the sum tells whether the
+  // maximum as it is.  No weight passes the limit unless their sum does, so the sum tells whether the
   // maximum has to move.  kl2, vl2: whose operands are read ahead at the end (NULL: none).
   auto step = [&](const char* kl, const char* vl, const f32x16& s, f32x16& sn, const Weights& pb,
                   Weights& pc, float cs, const char* kl2, const char* vl2) {
-    const float bias = kPShift - mx;
+    const float bias = shift - mx;
     float add[2] = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 16; ++e) sn[e] = 0.f;
@@ -623,7 +635,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
     if (__any(top - mx > 0.f)) {
       const float m = fmaxf(mx, pair_max(top));
       large = __any(fabsf(m) > kLarge && m != kNoMax);
-      limit = large ? -1.f : kSumLimit;
+      limit = large ? -1.f : sum_limit;
       const float f = __builtin_amdgcn_exp2f(mx - m);
       mx = m;
       l *= f;
@@ -637,7 +649,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), tile_waves(D) / 4) void tile_at
       float u[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        u[k] = large ? product(s[e + k], cs) - mx + kPShift : fmaf(s[e + k], cs, kPShift - mx);
+        u[k] = large ? product(s[e + k], cs) - mx + shift : fmaf(s[e + k], cs, shift - mx);
         u[k] = __builtin_amdgcn_exp2f(u[k]);
         sum += u[k];
       }

@@ -169,3 +169,81 @@ def test_results_over_keys_or_values(S):
     wide = rand(9, 41, 2, 64)
     with pytest.raises(S.SfxError, match="share memory"):
         S.attend_prompt(wide[1:], k, v, i32([0, 40]), out=wide[:40])
+
+
+def prompt_rows(q, k, v, lo, rows, scale, window=0):
+    """Definition in 64 bits of rows `rows` of a prompt that begins at row lo, with sum p |v| and the
+    largest |q||k| scale."""
+    import torch
+
+    group = q.shape[1] // k.shape[1]
+    kk = k.double().cpu().repeat_interleave(group, 1)
+    vv = v.double().cpu().repeat_interleave(group, 1)
+    out, mag, dots = [], [], []
+    for t in rows:
+        first = max(lo, t - window + 1) if window else lo
+        x = q[t].double().cpu()[None]
+        s = (kk[first:t + 1] * x).sum(2) * scale
+        w = (s - s.amax(0)).exp()
+        w /= w.sum(0)
+        out.append((w[:, :, None] * vv[first:t + 1]).sum(0))
+        mag.append((w[:, :, None] * vv[first:t + 1].abs()).sum(0))
+        dots.append((kk[first:t + 1].abs() * x.abs()).sum(2).amax(0) * scale)
+    return torch.stack(out), torch.stack(mag), torch.stack(dots)[:, :, None]
+
+
+def check_rows(out, q, k, v, offsets, rows, scale=None, window=0, least=0.0):
+    """`rows` of each request of a prompt call.  Tolerance: the result's rounding, eps / 2 of it; in units
+    of sum p |v| each weight's rounding to the values' type, eps / 2 (fp16: to a multiple of 2^-33 of the
+    largest below 2^-22 of it, once a token), the scores' fp32 error, (dim + 8) 2^-24 of |q||k| scale
+    and their own size, twice, and the sums', 2^-23 per 16 tokens and 64 more; `least` absolutely."""
+    import torch
+
+    eps = torch.finfo(out.dtype).eps / 2
+    dim = q.shape[2]
+    scale = dim ** -0.5 if scale is None else scale
+    for b in range(len(offsets) - 1):
+        lo, n = offsets[b], offsets[b + 1] - offsets[b]
+        mine = [lo + r for r in rows if r < n]
+        if not mine:
+            continue
+        ref, mag, dots = prompt_rows(q, k, v, lo, mine, scale, window)
+        got = out[mine].double().cpu()
+        assert torch.isfinite(got).all(), b
+        rel = eps + 2 * (dim + 8) * 2.0 ** -24 * (dots + 1) + (n / 16 + 64) * 2.0 ** -23
+        tol = eps * ref.abs() + mag * rel + least
+        if out.dtype is torch.float16:
+            tol = tol + n * 2.0 ** -33 * float(v[lo:lo + n].abs().max())
+        err = (got - ref).abs()
+        assert (err <= tol).all(), (b, (err > tol).nonzero()[:4].tolist(), float((err - tol).max()))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[1, 2, 40], [1000, 3], [9000]])
+def test_the_whole_range_of_bf16_values(S, lens, dim):
+    """Values up to the type's largest, and down to small ones: weights of any size keep sums in range."""
+    import torch
+
+    offsets = [0] + np.cumsum(lens).tolist()
+    N = offsets[-1]
+    q, k = (rand(i, N, h, dim, dtype="bfloat16") for i, h in ((1, 2), (2, 1)))
+    v = rand(3, N, 1, dim, dtype="bfloat16").clamp(-4, 4)
+    rows = [0, 1, 2, 31, 32, 39, 63, 64, 700, 999, 4095, 8191, 8999]
+    big = v * 2.0 ** 125    # up to 2^127
+    check_rows(S.attend_prompt(q, k, big, i32(offsets)), q, k, big, offsets, rows)
+    same = v.new_full(v.shape, 3e38)
+    out = S.attend_prompt(q, k, same, i32(offsets))
+    check_rows(out, q, k, same, offsets, rows)
+    # even weights are powers of two: the largest value comes out as it is
+    most = v.new_full(v.shape, torch.finfo(v.dtype).max)
+    assert S.attend_prompt(q * 0, k, most, i32(offsets)).eq(most[0, 0, 0]).all()
+    # scores that rise by less than it takes to move the maximum, then by more
+    q0, k0 = torch.zeros_like(q), torch.zeros_like(k)
+    q0[:, :, 0] = 1
+    for step in (0.004, 0.05, 0.5):
+        k0[:, 0, 0] = (torch.arange(N, device="cuda") * step).to(torch.bfloat16)
+        out = S.attend_prompt(q0, k0, big, i32(offsets), scale=1.0)
+        check_rows(out, q0, k0, big, offsets, rows, scale=1.0)
+    # small values: as long as products with the weights are normal numbers nothing is lost
+    small = v * 2.0 ** -90
+    check_rows(S.attend_prompt(q, k, small, i32(offsets)), q, k, small, offsets, rows)
