@@ -247,3 +247,221 @@ def test_the_whole_range_of_bf16_values(S, lens, dim):
     # small values: as long as products with the weights are normal numbers nothing is lost
     small = v * 2.0 ** -90
     check_rows(S.attend_prompt(q, k, small, i32(offsets)), q, k, small, offsets, rows)
+
+
+# ------------------------------------------------------------------ plans that only long inputs reach
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("lens,heads,dim", [([8192], 8, 128), ([5000, 3190], 8, 128),
+                                            ([2049, 2047, 4100], 8, 64), ([4000, 3990], 4, 256)])
+def test_prompts_cut_in_two(S, lens, heads, dim, dtype):
+    """Row tiles that fill the card just once: those that see more than 32 token tiles come in two parts,
+    the others in one.  Rows on both sides of every such border (2048 tokens at 64 and 128 dims, 1024 at
+    256), of the tiles of rows and of the second part."""
+    offsets = [0] + np.cumsum(lens).tolist()
+    N = offsets[-1]
+    size = ctypes.c_size_t()
+    assert S.load().sfx_prompt_attention_workspace_bytes(len(lens), N, heads, heads, dim, 0, 0,
+                                                         ctypes.byref(size)) == S.OK
+    assert size.value == 2 * N * heads * (dim + 2) * 4   # two parts
+    q, k, v = (rand(i, N, heads, dim, dtype=dtype) for i in range(3))
+    out = S.attend_prompt(q, k, v, i32(offsets))
+    rows = [0, 127, 128, 255, 256, 1023, 1024, 1025, 1151, 1152, 2047, 2048, 2049, 2303, 2304, 3071,
+            3999, 4095, 4096, 4999, 8191]
+    check_rows(out, q, k, v, offsets, rows)
+    # a window moves the border: 3000 tokens are 47 tiles for every row that far in
+    out = S.attend_prompt(q, k, v, i32(offsets), window=3000)
+    check_rows(out, q, k, v, offsets, rows, window=3000)
+
+
+def cached_rows(q, cache, table, length, n, lo, rows, window=0, sinks=0):
+    """Definition in 64 bits over the values that the cache holds, of rows `rows` of the n newest tokens
+    of a request (its first in row lo of q)."""
+    import torch
+
+    k, v = cache.read(table, i32([0]), i32([length]), length, dtype=torch.float32)
+    mapped = ((table[0] >= 0) & (table[0] < cache.num_pages)).cpu()
+    group = q.shape[1] // cache.kv_heads
+    kk, vv = (t[0].double().cpu().repeat_interleave(group, 1) for t in (k, v))
+    j = torch.arange(length)
+    out, mag, dots = [], [], []
+    for t in rows:
+        p = length - n + t
+        see = (j <= p) & mapped[j // cache.page_size]
+        if window:
+            see &= (j > p - window) | (j < sinks)
+        x = q[lo + t].double().cpu()[None]
+        s = (kk[see] * x).sum(2) * q.shape[2] ** -0.5
+        w = (s - s.amax(0)).exp()
+        w /= w.sum(0)
+        out.append((w[:, :, None] * vv[see]).sum(0))
+        mag.append((w[:, :, None] * vv[see].abs()).sum(0))
+        dots.append((kk[see].abs() * x.abs()).sum(2).amax(0) * q.shape[2] ** -0.5)
+    return torch.stack(out), torch.stack(mag), torch.stack(dots)[:, :, None], float(vv.abs().max())
+
+
+def check_cached(got, ref, length, dim):
+    """Tolerance: the result's rounding, eps / 2 of it; in units of sum p |v| each weight's to fp16,
+    2^-11 (below 2^-22 of the largest to a multiple of 2^-33 of it), the scores' fp32 error and the
+    sums' as for prompts."""
+    import torch
+
+    ref, mag, dots, most = ref
+    eps = torch.finfo(got.dtype).eps / 2
+    got = got.double().cpu()
+    rel = 2.0 ** -11 + 2 * (dim + 8) * 2.0 ** -24 * (dots + 1) + (length / 16 + 64) * 2.0 ** -23
+    tol = eps * ref.abs() + mag * rel + length * 2.0 ** -33 * most
+    assert torch.isfinite(got).all()
+    err = (got - ref).abs()
+    assert (err <= tol).all(), ((err > tol).nonzero()[:4].tolist(), float((err - tol).max()))
+
+
+@pytest.mark.parametrize("dim,page,group", [(64, 32, 4), (128, 64, 4), (128, 96, 2), (256, 2048, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5000, 200)])
+def test_chunks_over_many_pages(S, dim, page, group, window, sinks):
+    """A chunk whose workgroups walk thousands of tokens in one part: page ids and scales are fetched 64
+    blocks at a time, several times.  Pages without order, some unmapped."""
+    heads, length, n = 8, 7300, 2400
+    width = length // page + 2
+    cache = S.KVCache(width, page, heads, dim)
+    rng = np.random.default_rng(dim + page)
+    table = i32(rng.permutation(width)[None])
+    k, v = (rand(i, 1, length, heads, dim) for i in (1, 2))
+    # tokens of all sizes: neighbouring blocks have other exponents
+    size = (rand(3, 1, length // 32 + 1, heads, 1).float() * 2).exp2().repeat_interleave(32, 1)
+    cache.write(k, (v.float() * size[:, :length]).half(), table, i32([0]))
+    for j in ((1, 40, 70, 71, 150, 200) if width > 100 else (1,)):
+        if j < width:
+            table[0, j] = -1
+    q = rand(4, n, heads * group, dim)
+    out = cache.attend_packed(q, table, i32([length]), i32([0, n]), window=window, sinks=sinks)
+    rows = [0, 1, 63, 64, 127, 128, 700, 1500, n - 1]
+    ref = cached_rows(q, cache, table, length, n, 0, rows, window, sinks)
+    check_cached(out[rows], ref, length, dim)
+
+
+@pytest.mark.parametrize("heads,N", [(4, 9001), (9, 9000), (16, 9001), (40, 4096)])
+def test_write_slots_of_large_batches(S, heads, N):
+    """A wavefront looks at 8 to 32 tokens: stretches that begin at the last of them and end with the last
+    slot read, single tokens, gaps; as the padded write does it."""
+    import torch
+
+    dim, page = 64, 64
+    assert 4 < N * heads // 4096
+    rng = np.random.default_rng(N + heads)
+    # the first prompt's blocks all begin at rows 31, 63, ..: the last of a window of 32, or of 8
+    lens, start = [1, 30, 2050], [70, 1, 0]
+    while sum(lens) < N - 100:
+        lens.append(min(N - 100 - sum(lens), int(rng.choice([1, 1, 17, 31, 33, 300, 1500]))))
+        start.append(int(rng.integers(0, 100)))
+    B, width = len(lens), 36
+    table = rng.permutation(B * width).reshape(B, width)
+    slots = np.full(N, -1, np.int64)
+    off, at = [], 0
+    for b, n in enumerate(lens):
+        at += int(b > 2 and rng.random() < 0.2 and at + 1 + sum(lens[b:]) <= N)
+        off.append(at)
+        p = np.arange(start[b], start[b] + n)
+        slots[at:at + n] = table[b, p // page] * page + p % page
+        at += n
+    a, b = S.KVCache(B * width, page, heads, dim), S.KVCache(B * width, page, heads, dim)
+    for name in ("k", "v"):
+        fill = torch.randint(0, 120, getattr(a, name).shape, dtype=torch.uint8, device="cuda")
+        getattr(a, name).copy_(fill)
+        getattr(b, name).copy_(fill)
+        for c in (a, b):
+            getattr(c, name + "_scale").fill_(2.0 ** -9)
+    k, v = rand(1, N, heads, dim), rand(2, N, heads, dim)
+    a.write_slots(k, v, torch.from_numpy(slots).cuda())
+    for i, n in enumerate(lens):
+        b.write(k[None, off[i]:off[i] + n], v[None, off[i]:off[i] + n], i32(table[i:i + 1]),
+                i32(start[i:i + 1]))
+    for name in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
+
+
+def test_a_cache_past_4_gib(S):
+    """Pages whose codes lie past 2^32 bytes: written by slots, attended by short and long requests, as
+    the same tokens in a small cache."""
+    import torch
+
+    heads, dim, page, group, pages = 8, 128, 64, 2, 70000
+    far, near = S.KVCache(pages, page, heads, dim), S.KVCache(24, page, heads, dim)
+    assert far.k.numel() > 2 ** 32
+    last = np.arange(pages - 24, pages)
+    order = np.random.default_rng(1).permutation(24).reshape(2, 12)
+    N, lens, count = 700, [700, 300], [500, 200]
+    k, v, q = (rand(i, N, h, dim) for i, h in enumerate((heads, heads, heads * group)))
+    out = []
+    for cache, ids in ((far, last), (near, np.arange(24))):
+        table = i32(ids[order])
+        pool = S.PagePool(cache.num_pages, page)
+        for start, n in (([0, 0], [200, 100]), ([200, 100], count)):
+            lay = pool.layout(table, i32(start), i32(n), N)
+            cache.write_slots(k, v, lay.slots)
+        assert lay.seq_lens.tolist() == lens
+        out.append([cache.attend_packed(q, table, lay.seq_lens, lay.offsets),
+                    cache.attend_packed(q[:4], table, lay.seq_lens, i32([0, 1, 4]), max_q=3)])
+    for a, b in zip(*out):
+        assert torch.equal(a, b) and a.abs().sum() > 0
+    for name in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(far, name)[pages - 24:], getattr(near, name)), name
+    assert not far.k[:1000].any() and not far.v[:1000].any()
+
+
+def test_the_same_bits_every_time(S):
+    """Calls again, on another stream and beside another call of the same shapes: the same results."""
+    import torch
+
+    heads, group, dim, page = 2, 4, 128, 64
+    cache = cached(S, 3, 80, page, heads, dim, dtype="bfloat16")
+    table = i32(np.random.default_rng(2).permutation(80).reshape(4, 20))
+    offsets, lens = i32([0, 600, 617, 618, 700]), i32([1200, 900, 40, 82])
+    q, k, v = (rand(i, 700, h, dim, dtype="bfloat16") for i, h in ((1, 8), (2, heads), (3, heads)))
+    prompts = i32([0, 100, 650, 700])
+
+    def both(stream=None):
+        return (cache.attend_packed(q, table, lens, offsets, stream=stream),
+                S.attend_prompt(q, k, v, prompts, stream=stream))
+
+    want = both()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [both(st) for _ in range(5) for st in streams]
+    torch.cuda.synchronize()
+    for x in got + [both()]:
+        assert all(torch.equal(a, b) for a, b in zip(x, want))
+
+
+def test_pages_stay_within_their_arrays(S):
+    """The list of free pages, the table and the counts lie between words that nobody may write; counts that
+    cannot be are clamped."""
+    import torch
+
+    B, width, pages = 2, 4, 8
+    whole = torch.full((400,), 7, dtype=torch.int32, device="cuda")
+    at = dict(free=(64, pages), num_free=(128, 1), table=(150, B * width), held=(200, B),
+              tokens=(250, B), missing=(300, B))
+    a = {n: whole[i:i + size] for n, (i, size) in at.items()}
+    a["free"].copy_(i32(np.arange(pages)))
+    edge = torch.ones(400, dtype=torch.bool, device="cuda")
+    for i, size in at.values():
+        edge[i:i + size] = False
+    pool = S.PagePool(pages, 64, buffers=(a["free"], a["num_free"]))
+    table = a["table"].view(B, width)
+    for num_free, held, tokens, missing in ((100, [-5, 99], [256, 0], [0, 0]),
+                                            (2 ** 31 - 1, [99, 99], [0, 0], [0, 0]),
+                                            (-2 ** 31, [0, 0], [64, 64], [1, 1]),
+                                            (8, [-2 ** 31, 2 ** 31 - 1], [2 ** 31 - 1, -1],
+                                             [2 ** 25, 0])):
+        table.copy_(i32(np.arange(B * width).reshape(B, width)))
+        a["num_free"].fill_(num_free)
+        a["held"].copy_(i32(held))
+        a["tokens"].copy_(i32(tokens))
+        got = pool.reserve(table, a["held"], a["tokens"], missing=a["missing"])
+        assert got.tolist() == missing
+        assert whole[edge].eq(7).all()
+        assert 0 <= int(a["num_free"]) <= pages
+    for kw in (dict(tokens=a["held"]), dict(missing=a["held"]), dict(missing=a["tokens"])):
+        args = dict(dict(held=a["held"], tokens=a["tokens"], missing=a["missing"]), **kw)
+        with pytest.raises(ValueError, match="of their own"):
+            pool.reserve(table, **args)
