@@ -465,3 +465,65 @@ def test_pages_stay_within_their_arrays(S):
         args = dict(dict(held=a["held"], tokens=a["tokens"], missing=a["missing"]), **kw)
         with pytest.raises(ValueError, match="of their own"):
             pool.reserve(table, **args)
+
+
+@pytest.mark.parametrize("group", [100, 192, 193, 300])
+def test_many_query_heads_of_one(S, group):
+    """More query heads of a cached one than the kernel of few rows takes: single tokens and short
+    requests then are rows like any other."""
+    dim, page, lens, n = 64, 32, [70, 1, 333], [1, 1, 5]
+    cache = cached(S, group, 36, page, 1, dim)
+    table = i32(np.random.default_rng(group).permutation(36).reshape(3, 12))
+    offsets = [0, 1, 2, 7]
+    q = rand(1, 9, group, dim)
+    for max_q in (None, 5, 1):
+        out = cache.attend_packed(q, table, i32(lens), i32(offsets), max_q=max_q)
+        for b in range(3):
+            live = min(n[b], max_q or 9)
+            ref = cached_rows(q, cache, table[b:b + 1], lens[b], n[b], offsets[b], range(live))
+            check_cached(out[offsets[b]:offsets[b] + live], ref, lens[b], dim)
+            assert out[offsets[b] + live:offsets[b + 1]].eq(0).all()
+        assert out[7:].eq(0).all()
+    k, v = rand(2, 9, 1, dim), rand(3, 9, 1, dim)
+    out = S.attend_prompt(q, k, v, i32(offsets))
+    check_rows(out, q, k, v, offsets, range(5))
+
+
+def test_seventy_thousand_requests(S):
+    """Single tokens, requests without any and two longer ones, as the padded calls do them."""
+    import torch
+
+    B, dim, page = 70000, 64, 32
+    rng = np.random.default_rng(7)
+    n = rng.integers(0, 2, B)
+    n[100], n[B - 1] = 9, 300
+    offsets = np.concatenate([[0], np.cumsum(n)]) + 3
+    N = int(offsets[-1]) + 4
+    tokens = np.where(n > 0, n + rng.integers(0, 20, B), 0)
+    pool = S.PagePool(B + 40, page)
+    table, held = i32(np.full((B, 10), -1)), i32(np.zeros(B))
+    assert not pool.reserve(table, held, i32(tokens)).any()
+    assert held.tolist() == (-(-tokens // page)).tolist()
+    lay = pool.layout(table, i32(tokens - n), i32(n), N)
+    assert lay.offsets.tolist() == (offsets - 3).tolist() and lay.seq_lens.tolist() == tokens.tolist()
+    cache = S.KVCache(B + 40, page, 1, dim)
+    k, v = rand(1, 1, 32, 1, dim), rand(2, 1, 32, 1, dim)
+    ids = torch.arange(B + 40, dtype=torch.int32, device="cuda")[:, None]
+    cache.write(k.expand(B + 40, 32, 1, dim), v.expand(B + 40, 32, 1, dim), ids,
+                torch.zeros_like(ids[:, 0]))
+    q = rand(3, N, 2, dim)
+    for max_q in (None, 300):
+        out = cache.attend_packed(q, table, lay.seq_lens, lay.offsets, max_q=max_q)
+        one = torch.from_numpy(np.flatnonzero(n == 1)).cuda()
+        rows = lay.offsets[one].long()
+        want = cache.attend(q[rows][:, None], table[one].contiguous(), lay.seq_lens[one])[:, 0]
+        assert (out[rows].float() - want.float()).abs().max() <= 2.0 ** -9 * want.abs().max()
+        for b in (100, B - 1):
+            lo, hi = int(lay.offsets[b]), int(lay.offsets[b + 1])
+            want = cache.attend(q[None, lo:hi], table[b:b + 1], lay.seq_lens[b:b + 1])[0]
+            assert (out[lo:hi].float() - want.float()).abs().max() <= 2.0 ** -9 * want.abs().max()
+        assert out[int(lay.offsets[-1]):].eq(0).all()
+    # prompts of one token see themselves alone
+    k, v = rand(4, N, 1, dim), rand(5, N, 1, dim)
+    out = S.attend_prompt(q, k, v, lay.offsets)
+    assert torch.equal(out[rows], v[rows].expand(-1, 2, -1))
