@@ -590,7 +590,9 @@ int sfx_kv_attention_packed(const sfx_kv_cache* cache, int32_t B, int32_t N, int
  *   out [N, q_heads, head_dim], dense, aligned to 16 bytes: softmax(scale * q k) v in fp32 sums;
  *   zero for rows of no request.  It may be q if q is dense, and shares no memory with q, k and v
  *   otherwise (SFX_EINVAL).  head_dim: 64, 128 or 256; scale in [2^-64, 2^64].
- * Weights are rounded to `type` before they meet the values.
+ * Weights are rounded to `type` before they meet the values.  Finite scores and values of any size give
+ * finite results; NaN and infinite values reach the rows that see them and no others (an infinity as
+ * itself, or as NaN beside its opposite or where its weight rounds to zero).
  * workspace: sfx_prompt_attention_workspace_bytes (may be 0), aligned to 16 bytes. */
 int sfx_prompt_attention_workspace_bytes(int32_t B, int32_t N, int32_t q_heads, int32_t kv_heads,
                                          int32_t head_dim, int32_t window, int32_t sinks,

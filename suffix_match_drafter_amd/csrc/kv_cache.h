@@ -72,9 +72,9 @@ struct KvSlotArgs {
 
 // Tokens a wavefront looks at: as many as leave 8192 wavefronts, the card's fill.  In prompts only one
 // of 32 tokens starts a block, so wavefronts of few tokens mostly find nothing (18432 tokens of prompts,
-// 8 heads of 128 in bf16: 113 us with one token each, 41 with 8, 24 with 32); where every token starts
-// one, a wavefront of many works on one after the other (256 single tokens: 9 us with one token
-// each, 25 with 8, 85 with 32).
+// 8 heads of 128 in bf16: a call of 113 us with one token each, 41 with 8, 24 to 27 with 32); where
+// every token starts one, a wavefront of many works on one after the other (256 single tokens: 9 us
+// with one token each, 25 with 8, 85 with 32).
 inline int32_t kv_slot_window(int64_t N, int64_t heads) {
   const int64_t w = N * heads / 4096;
   return w < 1 ? 1 : (w > 32 ? 32 : (int32_t)w);

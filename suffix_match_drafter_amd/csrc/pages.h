@@ -15,12 +15,11 @@ struct ReserveArgs {
   int32_t* free_pages;
   int32_t* num_free;
   int32_t* missing;  // NULL: not wanted
-  int32_t* plan;     // workspace of calls in two launches: reserve_plan_words(B) words
+  int32_t* plan;     // workspace of calls in two launches: reserve_plan_words words
 };
 
 // Words of workspace: 0 for calls that one workgroup does.
 size_t reserve_plan_words(int32_t B, int32_t max_pages);
-int64_t reserve_threads(int32_t B, int32_t max_pages);
 
 struct LayoutArgs {
   int32_t B, N, max_pages, page_size, num_pages;

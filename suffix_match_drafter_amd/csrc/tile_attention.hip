@@ -45,9 +45,13 @@
 // Measured (8 heads of keys and values of 128, 4 query heads each, bf16): two prompts of 8192 tokens
 // 1045 to 1108 us by the card, 990 to 1050 TFLOP/s, where a library product of 8192^3 reaches 1345; a
 // chunk of 2048 tokens over 32768 cached ones 1025 to 1086 us, 920 to 975 TFLOP/s; 16 prompts of 128 to
-// 2048 tokens 266 to 286 us.  Bound by the matrix unit (busy half of the cycles) and by power: the clock falls from 2.1 to
-// 1.9 GHz as the unit is kept busier.  Workgroups of four wavefronts, two a CU: 1178 us instead of
-// 1055 for the two prompts; a higher priority for half the wavefronts: no difference.
+// 2048 tokens 266 to 294 us by their lengths.  No unit is full: of the cycles the matrix unit is busy in
+// 49% (prompts) and 40% (chunks), the LDS in 31% and 27%; of the wavefronts' time a quarter issues vector
+// instructions, a quarter to a third waits for loads and barriers and as much for its turn to issue.  The
+// clock falls from 2.1 to 1.9 GHz as the matrix unit is kept busier.  At 64 and 256 dims the unit is busy
+// in 30% and 28%: half as many products for each weight, and a single wavefront a SIMD, whose waits
+// nothing fills.  Workgroups of four wavefronts, two a CU: 1178 us instead of 1055 for the two prompts; a
+// higher priority for half the wavefronts: no difference.
 #include "tile_attention.h"
 
 #include <hip/hip_bf16.h>
@@ -928,7 +932,8 @@ size_t tile_attention_plan(TileAttentionArgs* a, int dim, bool paged) {
   // As many splits as find a place on the card at once, of at least four tiles.
   a->least = 4;
   int64_t row_tiles = (int64_t)a->N * a->group / tile_rows(dim);
-  // every request has one (where those of few rows are left out, most of the rows are of others)
+  // Every request has one.  Where those of few rows are left out their rows count all the same, as the
+  // plan does not know the offsets: many drafts beside one short chunk leave it with too few splits.
   const int64_t least = a->few > 0 ? 1 : (a->B < a->N ? a->B : a->N);
   row_tiles = row_tiles < least ? least : row_tiles;
   const int64_t pairs = row_tiles * a->heads;
